@@ -87,6 +87,10 @@ typedef enum {
 /* Element type of an unquantized operand: fp32, or bf16 (bfloat16). */
 typedef enum { MXQ_F32 = 0, MXQ_BF16 = 1, MXQ_DTYPE_MAX_ENUM = 0x7FFFFFFF } mxq_dtype;
 
+/* Element format of a quantized cache: MXFP8 (E4M3) or MXFP4 (E2M1), both with
+ * one E8M0 scale per 32 elements. */
+typedef enum { MXQ_MXFP8 = 0, MXQ_MXFP4 = 1, MXQ_FORMAT_MAX_ENUM = 0x7FFFFFFF } mxq_format;
+
 /* Static, NUL-terminated description of a status code (host memory). */
 MXQ_API const char *mxq_status_string(mxq_status s);
 
@@ -332,6 +336,89 @@ MXQ_API mxq_status mxq_transfp4_dequantize(const uint8_t *q, const uint8_t *s,
                                    const uint8_t *meta, const uint16_t *res,
                                    const float *gscale, int64_t rows, int64_t k, void *y,
                                    mxq_dtype ydt, hipStream_t stream);
+
+/*
+ * Residual addition, root-mean-square norm and MXFP8 quantize in one pass,
+ * the activations of mxq_gemm_w4a8.  For each of `rows` rows of k elements:
+ *   r = x + residual, rounded to xdt (r = x if residual is NULL);
+ *   y_i = r_i * (1 / sqrt(mean_j r_j^2 + eps)) * weight_i, in fp32 in this
+ *   order, the sum of squares in fp32, the row's one factor rounded once;
+ *   (q, s) = MXFP8 of the fp32 y, as mxq_quantize_fp8.
+ * x, residual, r [rows][k] and weight [k] of type xdt; q [rows][k]; s
+ * [rows][k/32].  r receives the sum and may be x or residual itself (in
+ * place); with residual NULL it is not written and may be NULL.  q and s must
+ * not overlap any other array.  k % 32 == 0; eps finite and > 0.
+ */
+MXQ_API mxq_status mxq_rmsnorm_quantize_fp8(const void *x, const void *residual, const void *weight,
+                                    mxq_dtype xdt, int64_t rows, int64_t k, float eps, void *r,
+                                    uint8_t *q, uint8_t *s, hipStream_t stream);
+
+/*
+ * Paged MX cache of keys and values.  `pages` pages of page_size tokens
+ * (P, a power of two from 16 to 1024), kv_heads heads of head_dim elements
+ * (D, a multiple of 32; kv_heads * D <= 2^20), fmt MXQ_MXFP8 or MXQ_MXFP4:
+ *   kq, vq [pages][kv_heads][P][D] E4M3 codes, or [P][D/2] packed E2M1 codes
+ *   ks     [pages][kv_heads][P][D/32] E8M0 codes of the keys
+ *   vs     [pages][kv_heads][D/32][P] E8M0 codes of the values
+ * Blocks of 32 run along D, so a token is quantized once, when it is
+ * written.  A token's place is its slot, page * P + position in the page.
+ *
+ * mxq_kv_append writes tokens: k and v of type dt, row t at k + t * k_stride
+ * (v + t * v_stride) elements, [kv_heads][D] contiguous inside a row, so
+ * slices of a fused projection's output serve as they are; strides are
+ * multiples of 8 and at least kv_heads * D.  slots[tokens] in device memory;
+ * a slot outside [0, pages * P) is skipped (-1 marks padding).  Codes and
+ * scales are those of mxq_quantize_fp8 (mxq_quantize) of the token's rows.
+ * Two tokens with the same slot in one call: the slot's content is undefined.
+ *
+ * mxq_kv_read reads slots back: k, v [tokens][kv_heads][D] of type dt, exact
+ * in fp32 and bf16 as mxq_dequantize; a slot outside the cache reads as zeros.
+ */
+MXQ_API mxq_status mxq_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                         mxq_dtype dt, const int64_t *slots, int64_t tokens, int64_t pages,
+                         int64_t kv_heads, int64_t page_size, int64_t head_dim, mxq_format fmt,
+                         uint8_t *kq, uint8_t *ks, uint8_t *vq, uint8_t *vs, hipStream_t stream);
+MXQ_API mxq_status mxq_kv_read(const uint8_t *kq, const uint8_t *ks, const uint8_t *vq, const uint8_t *vs,
+                       const int64_t *slots, int64_t tokens, int64_t pages, int64_t kv_heads,
+                       int64_t page_size, int64_t head_dim, mxq_format fmt, void *k, void *v,
+                       mxq_dtype dt, hipStream_t stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache (which holds
+ * that token already).  For each sequence b and query head h, with cache head
+ * h / (q_heads / kv_heads) and t over the visible positions
+ * [max(0, lens[b] - window), lens[b]) (all of [0, lens[b]) for window 0):
+ *   o = sum_t p_t V_t / (sum_t p_t + [sinks] exp(sinks[h])),
+ *   p_t = exp(scale * q . K_t)
+ * (evaluated with the maximum subtracted).  Position t is in page
+ * table[b * table_stride + t / P].  A sequence with no visible position gives
+ * zeros.  What the cache holds outside the visible positions has no effect.
+ * Lengths below 0 count as 0, and above table_width * P as that; positions
+ * whose table entry is outside [0, pages) are not visible.  The table and the
+ * lengths are device memory, and the host does not read them.
+ * q bf16, row b at q + b * q_stride elements (a multiple of 8, at least
+ * q_heads * head_dim), [q_heads][head_dim] contiguous inside a row; sinks fp32
+ * [q_heads] or NULL; out [batch][q_heads][head_dim] of type odt.  head_dim
+ * 64, 128 or 256; q_heads a multiple of kv_heads; scale finite.  Scores,
+ * probabilities and sums are fp32 (probabilities enter their product as two
+ * bf16 terms).
+ * The length is split over blocks whose partial results go to `workspace`
+ * (16-byte aligned, at least the bytes that mxq_paged_attention_workspace
+ * gives for the same sizes; may be NULL for 0).  Its content need not be
+ * prepared, and it may be reused by any later call on the same stream.
+ * The call is split for sequences of table_width * P tokens: pass a table no
+ * wider than the batch needs.
+ */
+MXQ_API mxq_status mxq_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                         int64_t page_size, int64_t head_dim, int64_t table_width,
+                                         int64_t window, int64_t *bytes);
+MXQ_API mxq_status mxq_paged_attention(const void *q, int64_t q_stride, const uint8_t *kq, const uint8_t *ks,
+                               const uint8_t *vq, const uint8_t *vs, const int32_t *table,
+                               int64_t table_width, int64_t table_stride, const int32_t *lens,
+                               const float *sinks, int64_t batch, int64_t q_heads, int64_t pages,
+                               int64_t kv_heads, int64_t page_size, int64_t head_dim, mxq_format fmt,
+                               float scale, int64_t window, void *workspace, int64_t workspace_bytes,
+                               void *out, mxq_dtype odt, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,14 @@ library is not built, or the device is not gfx950, calls raise.
     y = nvq.dequantize(q, s, g)         # (also nv_quantize / nv_dequantize / nv_gemm)
     y = nvq.gemm(wq, ws, g, x)
 
+and, between the products of a served model's decode step:
+
+    q, s, r = rmsnorm_quantize_fp8(x, w, residual)   # r = x + residual, MXFP8 of its norm
+    cache = kv_cache(pages, 64, kv_heads, 128)       # paged MXFP8 (or "mxfp4") keys and values
+    kv_append(cache, k, v, slots)                    # quantize new tokens into their slots
+    o = paged_attention(q, cache, table, lens)       # one new token per sequence
+    k, v = kv_read(cache, slots)                     # read slots back
+
 Every tensor argument is checked before anything is enqueued: dtype, shape
 (scales and caller-supplied outputs must match the operands exactly),
 contiguity, and that it lives on the operands' device; the NVFP4 tensor
@@ -22,13 +30,17 @@ scale must be a 1-element fp32 device tensor.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxq.so")
 
 MXQ_F32 = 0
 MXQ_BF16 = 1
+MXQ_MXFP8 = 0
+MXQ_MXFP4 = 1
 STATUS = {
     0: "MXQ_SUCCESS",
     1: "MXQ_ERROR_INVALID_VALUE",
@@ -40,6 +52,7 @@ API = (
     "mxq_status_string", "mxq_version", "mxq_quantize", "mxq_quantize_hadamard", "mxq_quantize_fp8",
     "mxq_dequantize", "mxq_gemv_w4a16", "mxq_gemm_w4a4", "mxq_gemm_w4a4_quant", "mxq_gemm_w4a4_dynamic",
     "mxq_gemm_w4a8", "mxq_gemm_w4a8_dynamic", "nvq_quantize", "nvq_dequantize", "nvq_gemm", "mxq_transfp4_quantize", "mxq_transfp4_dequantize",
+    "mxq_rmsnorm_quantize_fp8", "mxq_kv_append", "mxq_kv_read", "mxq_paged_attention_workspace", "mxq_paged_attention",
 )
 
 
@@ -83,6 +96,13 @@ def capi() -> ctypes.CDLL:
     lib.nvq_gemm.argtypes = [P, P, P, I64, I64, P, I64, P, I, P]
     lib.mxq_transfp4_quantize.argtypes = [P, I, I64, I64, P, I, P, P, P, P, P]
     lib.mxq_transfp4_dequantize.argtypes = [P, P, P, P, P, I64, I64, P, I, P]
+    F = ctypes.c_float
+    lib.mxq_rmsnorm_quantize_fp8.argtypes = [P, P, P, I, I64, I64, F, P, P, P, P]
+    lib.mxq_kv_append.argtypes = [P, I64, P, I64, I, P, I64, I64, I64, I64, I64, I, P, P, P, P, P]
+    lib.mxq_kv_read.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I, P, P, I, P]
+    lib.mxq_paged_attention_workspace.argtypes = [I64, I64, I64, I64, I64, I64, I64, ctypes.POINTER(I64)]
+    lib.mxq_paged_attention.argtypes = [P, I64, P, P, P, P, P, I64, I64, P, P, I64, I64, I64, I64, I64, I64, I, F,
+                                        I64, P, I64, P, I, P]
     for name in API[2:]:
         getattr(lib, name).restype = I
     _lib = lib
@@ -458,6 +478,188 @@ def transfp4_dequantize(q, s, meta, res, g, dtype=None, y=None):
     _check(capi().mxq_transfp4_dequantize(_p(q), _p(s), _p(meta), _p(res), _p(g), rows, k, _p(y),
                                           _dtype_code(y.dtype), _stream()), "mxq_transfp4_dequantize")
     return y
+
+
+# ------------------------------------------------------------------ norm, paged cache, attention
+
+def rmsnorm_quantize_fp8(x, weight, residual=None, eps=1e-6, q=None, s=None, r=None):
+    """r = x + residual (rounded to x's dtype), y = r / sqrt(mean r^2 + eps) * weight
+    along rows, MXFP8 of y: (q[rows, k] E4M3 codes u8, s[rows, k/32] E8M0 u8, r).
+
+    x, residual [rows, k] and weight [k], all bf16 or all fp32; k % 32 == 0.
+    Without a residual r is x itself.  Pass r=residual (or r=x) to update the
+    residual stream in place."""
+    torch = _torch()
+    _need(x, "x", _floats())
+    rows, k = x.shape
+    _k_blocks(k, 32, "rmsnorm_quantize_fp8")
+    _need(weight, "weight", x.dtype, (k,))
+    if not eps > 0:
+        raise ValueError(f"eps must be > 0, got {eps}")
+    q = _out(q, "q", (rows, k), torch.uint8, x.device)
+    s = _out(s, "s", (rows, k // 32), torch.uint8, x.device)
+    if residual is None:
+        if r is not None and r is not x:
+            raise ValueError("r is only written with a residual")
+        _on_device(x=x, weight=weight, q=q, s=s)
+        rp, op, r = None, None, x
+    else:
+        _need(residual, "residual", x.dtype, (rows, k))
+        r = _out(r, "r", (rows, k), x.dtype, x.device)
+        _on_device(x=x, weight=weight, q=q, s=s, residual=residual, r=r)
+        rp, op = residual.data_ptr(), r.data_ptr()
+    _check(capi().mxq_rmsnorm_quantize_fp8(x.data_ptr(), rp, weight.data_ptr(), _dtype_code(x.dtype), rows, k, eps,
+                                           op, q.data_ptr(), s.data_ptr(), _stream()), "mxq_rmsnorm_quantize_fp8")
+    return q, s, r
+
+
+class KVCache(NamedTuple):
+    """A paged MXFP8 or MXFP4 cache: kq, vq [pages, kv_heads, page_size, D] E4M3
+    codes (or [..., D/2] packed E2M1), ks [pages, kv_heads, page_size, D/32] and
+    vs [pages, kv_heads, D/32, page_size] E8M0 codes, all uint8 and contiguous.
+    A token's slot is page * page_size + its position in the page."""
+    kq: object
+    ks: object
+    vq: object
+    vs: object
+
+
+def kv_cache(pages, page_size, kv_heads, head_dim, fmt="mxfp8", device="cuda"):
+    """A new zero-filled KVCache; fmt "mxfp8" or "mxfp4", page_size a power of
+    two from 16 to 1024, head_dim a multiple of 32 (64, 128 or 256 for
+    paged_attention)."""
+    torch = _torch()
+    if fmt not in ("mxfp8", "mxfp4"):
+        raise ValueError(f"fmt must be 'mxfp8' or 'mxfp4', got {fmt!r}")
+    _k_blocks(head_dim, 32, "kv_cache")
+    code = head_dim if fmt == "mxfp8" else head_dim // 2
+    shapes = ((pages, kv_heads, page_size, code), (pages, kv_heads, page_size, head_dim // 32),
+              (pages, kv_heads, page_size, code), (pages, kv_heads, head_dim // 32, page_size))
+    return KVCache(*(torch.zeros(sh, dtype=torch.uint8, device=device) for sh in shapes))
+
+
+def _cache(cache):
+    """(pages, kv_heads, page_size, head_dim, format) of a KVCache after validation."""
+    torch = _torch()
+    kq, ks, vq, vs = cache
+    _need(kq, "kq", torch.uint8, ndim=4)
+    _need(ks, "ks", torch.uint8, ndim=4)
+    pages, heads, page, w = kq.shape
+    d = ks.shape[3] * 32
+    if w != d and 2 * w != d:
+        raise ValueError(f"kq has {w} bytes a row, ks names head_dim {d}: MXFP8 has {d}, MXFP4 {d // 2}")
+    _need(ks, "ks", torch.uint8, (pages, heads, page, d // 32))
+    _need(vq, "vq", torch.uint8, (pages, heads, page, w))
+    _need(vs, "vs", torch.uint8, (pages, heads, d // 32, page))
+    return pages, heads, page, d, MXQ_MXFP8 if w == d else MXQ_MXFP4
+
+
+def _rows(t, name, dtype, heads, dim):
+    """[n, heads, dim] whose rows are contiguous inside (a slice of a fused
+    projection's output): the row stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in dtype:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtype)}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape [n, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    row, inner, one = t.stride()
+    if one != 1 or (inner != dim and t.shape[1] > 1):
+        raise ValueError(f"{name} must be contiguous in its last two dims")
+    return row if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def _slots(slots, n=None):
+    torch = _torch()
+    _need(slots, "slots", torch.int64, None if n is None else (n,), ndim=1)
+
+
+def kv_append(cache, k, v, slots):
+    """Quantize new tokens k, v [tokens, kv_heads, head_dim] (bf16 or fp32, row
+    stride free) into their slots (int64 [tokens]; outside the cache, e.g. -1:
+    skipped).  The cache is updated in place."""
+    pages, heads, page, d, fmt = _cache(cache)
+    k_stride = _rows(k, "k", _floats(), heads, d)
+    v_stride = _rows(v, "v", (k.dtype,), heads, d)
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError(f"k has {n} tokens, v {v.shape[0]}")
+    _slots(slots, n)
+    kq, ks, vq, vs = cache
+    _on_device(kq=kq, ks=ks, vq=vq, vs=vs, k=k, v=v, slots=slots)
+    _check(capi().mxq_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, _dtype_code(k.dtype),
+                                slots.data_ptr(), n, pages, heads, page, d, fmt, kq.data_ptr(), ks.data_ptr(),
+                                vq.data_ptr(), vs.data_ptr(), _stream()), "mxq_kv_append")
+
+
+def kv_read(cache, slots, dtype=None, k=None, v=None):
+    """The slots' keys and values, (k, v) [tokens, kv_heads, head_dim] in dtype
+    (default bf16); a slot outside the cache reads as zeros."""
+    torch = _torch()
+    pages, heads, page, d, fmt = _cache(cache)
+    _slots(slots)
+    kq, ks, vq, vs = cache
+    n = slots.shape[0]
+    dtype = dtype or (k.dtype if k is not None else torch.bfloat16)
+    k = _out(k, "k", (n, heads, d), dtype, kq.device, real=True)
+    v = _out(v, "v", (n, heads, d), dtype, kq.device, real=True)
+    _on_device(kq=kq, ks=ks, vq=vq, vs=vs, slots=slots, k=k, v=v)
+    _check(capi().mxq_kv_read(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), slots.data_ptr(), n, pages,
+                              heads, page, d, fmt, k.data_ptr(), v.data_ptr(), _dtype_code(dtype), _stream()),
+           "mxq_kv_read")
+    return k, v
+
+
+def paged_attention(q, cache, table, lens, scale=None, window=0, sinks=None, out_dtype=None, out=None, workspace=None):
+    """Attention of one new token per sequence over the cache: out[batch, q_heads, D].
+
+    q [batch, q_heads, D] bf16 (row stride free); table [batch, width] int32 page
+    ids (row stride free); lens [batch] int32 lengths including the new token;
+    scale defaults to 1/sqrt(D); window > 0 sees the last `window` positions
+    only; sinks [q_heads] fp32 adds exp(sinks) to each head's denominator.  A
+    sequence with nothing visible gives zeros.  workspace: a uint8 device
+    tensor to use for partial results (allocated if None).  A table no wider
+    than the batch needs gives the best split."""
+    torch = _torch()
+    pages, heads, page, d, fmt = _cache(cache)
+    q_stride = _rows(q, "q", (torch.bfloat16,), None, d)
+    batch, q_heads = q.shape[0], q.shape[1]
+    if q_heads % heads != 0:
+        raise ValueError(f"{q_heads} query heads over {heads} cache heads")
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32:
+        raise TypeError("table must be an int32 tensor")
+    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must have shape [{batch}, width] with contiguous rows, got {tuple(table.shape)}")
+    width = table.shape[1]
+    table_stride = table.stride(0) if batch > 1 else max(width, table.stride(0))
+    _need(lens, "lens", torch.int32, (batch,))
+    kq, ks, vq, vs = cache
+    dev = kq.device
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    out = _out(out, "out", (batch, q_heads, d), out_dtype, dev, real=True)
+    on = {"kq": kq, "ks": ks, "vq": vq, "vs": vs, "q": q, "table": table, "lens": lens, "out": out}
+    if sinks is not None:
+        _need(sinks, "sinks", torch.float32, (q_heads,))
+        on["sinks"] = sinks
+    need = ctypes.c_int64()
+    _check(capi().mxq_paged_attention_workspace(batch, q_heads, heads, page, d, width, window, ctypes.byref(need)),
+           "mxq_paged_attention_workspace")
+    if workspace is None:
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, ndim=1)
+        if workspace.shape[0] < need.value:
+            raise ValueError(f"workspace has {workspace.shape[0]} bytes, {need.value} are needed")
+    on["workspace"] = workspace
+    _on_device(**on)
+    _check(capi().mxq_paged_attention(q.data_ptr(), q_stride, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(),
+                                      vs.data_ptr(), table.data_ptr(), width, table_stride, lens.data_ptr(),
+                                      None if sinks is None else sinks.data_ptr(), batch, q_heads, pages, heads, page,
+                                      d, fmt, 1.0 / math.sqrt(d) if scale is None else scale, window,
+                                      workspace.data_ptr(), workspace.shape[0], out.data_ptr(),
+                                      _dtype_code(out_dtype), _stream()), "mxq_paged_attention")
+    return out
 
 
 from . import nvq  # noqa: E402  (the NVFP4 names: nvq.quantize / nvq.dequantize / nvq.gemm)

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "../../include/mxq.h"
 #include "mxq_launch.h"
@@ -257,6 +258,135 @@ mxq_status mxq_transfp4_dequantize(const uint8_t* q, const uint8_t* s, const uin
   mxq_status d = check_device();
   if (d != MXQ_SUCCESS) return d;
   return launched(mxq::launch_tf4_dequantize(q, s, meta, res, gscale, rows, k, y, ydt == MXQ_BF16, stream));
+}
+
+mxq_status mxq_rmsnorm_quantize_fp8(const void* x, const void* residual, const void* weight, mxq_dtype xdt,
+                                    int64_t rows, int64_t k, float eps, void* r, uint8_t* q, uint8_t* s,
+                                    hipStream_t stream) {
+  if (rows < 1 || k < 1 || k % 32 != 0 || !valid_dtype(xdt)) return MXQ_ERROR_INVALID_VALUE;
+  if (rows > kMaxElems / k || !(eps > 0) || !std::isfinite(eps)) return MXQ_ERROR_INVALID_VALUE;
+  if (!x || !weight || !q || !s || (residual && !r)) return MXQ_ERROR_INVALID_VALUE;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(q) || !aligned16(s)) return MXQ_ERROR_MISALIGNED;
+  if (residual && (!aligned16(residual) || !aligned16(r))) return MXQ_ERROR_MISALIGNED;
+  mxq_status d = check_device();
+  if (d != MXQ_SUCCESS) return d;
+  return launched(
+      mxq::launch_rmsnorm_quantize_fp8(x, residual, weight, xdt == MXQ_BF16, rows, k, eps, r, q, s, stream));
+}
+
+// Sizes of a paged cache; true and *c filled if they are valid.
+static bool cache_shape(int64_t pages, int64_t kv_heads, int64_t page_size, int64_t head_dim, mxq::KvShape* c) {
+  if (pages < 1 || kv_heads < 1 || head_dim < 32 || head_dim % 32 != 0) return false;
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return false;
+  if (head_dim > (1 << 20) || kv_heads > (1 << 20) / head_dim) return false;
+  if (pages > kMaxElems / (kv_heads * head_dim * page_size)) return false;
+  c->pages = pages;
+  c->heads = (unsigned)kv_heads;
+  c->dim = (unsigned)head_dim;
+  c->page_shift = (unsigned)__builtin_ctzll((unsigned long long)page_size);
+  return true;
+}
+
+static bool valid_format(mxq_format f) { return f == MXQ_MXFP8 || f == MXQ_MXFP4; }
+
+static mxq_status cache_pointers(const uint8_t* kq, const uint8_t* ks, const uint8_t* vq, const uint8_t* vs) {
+  if (!kq || !ks || !vq || !vs) return MXQ_ERROR_INVALID_VALUE;
+  return aligned16(kq) && aligned16(ks) && aligned16(vq) && aligned16(vs) ? MXQ_SUCCESS : MXQ_ERROR_MISALIGNED;
+}
+
+mxq_status mxq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, mxq_dtype dt,
+                         const int64_t* slots, int64_t tokens, int64_t pages, int64_t kv_heads, int64_t page_size,
+                         int64_t head_dim, mxq_format fmt, uint8_t* kq, uint8_t* ks, uint8_t* vq, uint8_t* vs,
+                         hipStream_t stream) {
+  mxq::KvShape c;
+  if (!cache_shape(pages, kv_heads, page_size, head_dim, &c) || !valid_dtype(dt) || !valid_format(fmt))
+    return MXQ_ERROR_INVALID_VALUE;
+  const int64_t row = kv_heads * head_dim;
+  if (tokens < 1 || k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return MXQ_ERROR_INVALID_VALUE;
+  if (tokens > kMaxElems / k_stride || tokens > kMaxElems / v_stride || !k || !v || !slots)
+    return MXQ_ERROR_INVALID_VALUE;
+  mxq_status e = cache_pointers(kq, ks, vq, vs);
+  if (e != MXQ_SUCCESS) return e;
+  if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 7u)) return MXQ_ERROR_MISALIGNED;
+  e = check_device();
+  if (e != MXQ_SUCCESS) return e;
+  return launched(mxq::launch_kv_append(k, k_stride, v, v_stride, dt == MXQ_BF16, slots, tokens, c, fmt == MXQ_MXFP4,
+                                        kq, ks, vq, vs, stream));
+}
+
+mxq_status mxq_kv_read(const uint8_t* kq, const uint8_t* ks, const uint8_t* vq, const uint8_t* vs,
+                       const int64_t* slots, int64_t tokens, int64_t pages, int64_t kv_heads, int64_t page_size,
+                       int64_t head_dim, mxq_format fmt, void* k, void* v, mxq_dtype dt, hipStream_t stream) {
+  mxq::KvShape c;
+  if (!cache_shape(pages, kv_heads, page_size, head_dim, &c) || !valid_dtype(dt) || !valid_format(fmt))
+    return MXQ_ERROR_INVALID_VALUE;
+  if (tokens < 1 || tokens > kMaxElems / (kv_heads * head_dim) || !k || !v || !slots) return MXQ_ERROR_INVALID_VALUE;
+  mxq_status e = cache_pointers(kq, ks, vq, vs);
+  if (e != MXQ_SUCCESS) return e;
+  if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 7u)) return MXQ_ERROR_MISALIGNED;
+  e = check_device();
+  if (e != MXQ_SUCCESS) return e;
+  return launched(mxq::launch_kv_read(kq, ks, vq, vs, slots, tokens, c, fmt == MXQ_MXFP4, k, v, dt == MXQ_BF16, stream));
+}
+
+// Sizes of an attention call over a cache of shape c.
+static bool attend_sizes(int64_t batch, int64_t q_heads, const mxq::KvShape& c, int64_t table_width, int64_t window) {
+  if (batch < 1 || q_heads < 1 || q_heads % c.heads != 0 || (c.dim != 64 && c.dim != 128 && c.dim != 256)) return false;
+  if (table_width < 1 || table_width > 0x7FFFFFFF || window < 0) return false;
+  // blocks of 256 threads of both launches: below 2^32 threads
+  if (q_heads > (1 << 20) || batch > (1 << 24) / q_heads) return false;
+  return mxq::attend_blocks(batch, (unsigned)q_heads, c, table_width, window) < (1 << 24);
+}
+
+mxq_status mxq_paged_attention_workspace(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t page_size,
+                                         int64_t head_dim, int64_t table_width, int64_t window, int64_t* bytes) {
+  mxq::KvShape c;
+  if (!bytes || !cache_shape(1, kv_heads, page_size, head_dim, &c) ||
+      !attend_sizes(batch, q_heads, c, table_width, window))
+    return MXQ_ERROR_INVALID_VALUE;
+  *bytes = mxq::attend_workspace(batch, (unsigned)q_heads, c, table_width, window);
+  return MXQ_SUCCESS;
+}
+
+mxq_status mxq_paged_attention(const void* q, int64_t q_stride, const uint8_t* kq, const uint8_t* ks,
+                               const uint8_t* vq, const uint8_t* vs, const int32_t* table, int64_t table_width,
+                               int64_t table_stride, const int32_t* lens, const float* sinks, int64_t batch,
+                               int64_t q_heads, int64_t pages, int64_t kv_heads, int64_t page_size, int64_t head_dim,
+                               mxq_format fmt, float scale, int64_t window, void* workspace, int64_t workspace_bytes,
+                               void* out, mxq_dtype odt, hipStream_t stream) {
+  mxq::KvShape c;
+  if (!cache_shape(pages, kv_heads, page_size, head_dim, &c) || !valid_dtype(odt) || !valid_format(fmt) ||
+      !attend_sizes(batch, q_heads, c, table_width, window))
+    return MXQ_ERROR_INVALID_VALUE;
+  if (q_stride < q_heads * head_dim || q_stride % 8 != 0 || q_stride > kMaxElems / batch ||
+      table_stride < table_width || table_stride > kMaxElems / batch || !std::isfinite(scale))
+    return MXQ_ERROR_INVALID_VALUE;
+  if (!q || !table || !lens || !out) return MXQ_ERROR_INVALID_VALUE;
+  const int64_t need = mxq::attend_workspace(batch, (unsigned)q_heads, c, table_width, window);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERROR_INVALID_VALUE;
+  mxq_status e = cache_pointers(kq, ks, vq, vs);
+  if (e != MXQ_SUCCESS) return e;
+  if (!aligned16(q) || !aligned16(out) || (need > 0 && !aligned16(workspace))) return MXQ_ERROR_MISALIGNED;
+  if (((uintptr_t)table & 3u) || ((uintptr_t)lens & 3u) || ((uintptr_t)sinks & 3u)) return MXQ_ERROR_MISALIGNED;
+  e = check_device();
+  if (e != MXQ_SUCCESS) return e;
+  mxq::AttendArgs a;
+  a.q = (const uint16_t*)q;
+  a.q_stride = q_stride;
+  a.kq = kq, a.ks = ks, a.vq = vq, a.vs = vs;
+  a.table = table;
+  a.table_width = table_width;
+  a.table_stride = table_stride;
+  a.lens = lens;
+  a.sinks = sinks;
+  a.batch = batch;
+  a.window = window;
+  a.q_heads = (unsigned)q_heads;
+  a.scale = scale;
+  a.out = out;
+  a.bf16_out = odt == MXQ_BF16;
+  return launched(mxq::launch_attend(a, c, fmt == MXQ_MXFP4, workspace, stream));
 }
 
 }  // extern "C"

@@ -214,4 +214,62 @@ __device__ __forceinline__ void mx8_quantize_lane_bf16(const bf16x8 (&xb)[4], un
   *code = c;
 }
 
+// Largest |x| of 8 fp32 values as magnitude bits.
+__device__ __forceinline__ unsigned f32x8_absmax_bits(const float (&v)[8]) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// MXFP4 of one lane's 8 consecutive fp32 values, four lanes (a DPP quad, all
+// of it active) forming one block: the rules of mx_quantize_quad_bf16.
+__device__ __forceinline__ unsigned mx_quantize_quad_f32(const float (&v)[8], unsigned* code) {
+  unsigned m = f32x8_absmax_bits(v);
+  m = max(m, dpp_quad_xor1(m));
+  m = max(m, dpp_quad_xor2(m));
+  const unsigned c = e8m0_code_from_expfield(m >> 23);
+  const float scale = e8m0_as_scale(c);
+  unsigned out = 0;
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[0], v[1], scale, 0);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[2], v[3], scale, 1);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[4], v[5], scale, 2);
+  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[6], v[7], scale, 3);
+  *code = c;
+  return out;
+}
+
+// MXFP8 of one lane's 8 consecutive fp32 values of a quad's block, every
+// magnitude clamped to 448 * 2^e ahead of the convert (as mx8_encode8_bf16;
+// fp32 bits of the limit: exponent field code + 8, mantissa .11).
+__device__ __forceinline__ u32x2 mx8_quantize_quad_f32(const float (&v)[8], unsigned* code) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  unsigned m = f32x8_absmax_bits(v);
+  m = max(m, dpp_quad_xor1(m));
+  m = max(m, dpp_quad_xor2(m));
+  const unsigned c = e8m0_code_e4m3(m >> 23);
+  const float scale = e8m0_as_scale(c);
+  const unsigned lim = ((c + 8u) << 23) | 0x600000u;
+  auto clamp = [&](float f) {
+    const unsigned w = __float_as_uint(f);
+    return __uint_as_float(min(w & 0x7FFFFFFFu, lim) | (w & 0x80000000u));
+  };
+  s16x2 lo = {0, 0}, hi = {0, 0};
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, clamp(v[0]), clamp(v[1]), scale, false);
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, clamp(v[2]), clamp(v[3]), scale, true);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, clamp(v[4]), clamp(v[5]), scale, false);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, clamp(v[6]), clamp(v[7]), scale, true);
+  *code = c;
+  return (u32x2){__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
+}
+
+// MXFP8 of one lane's 8 consecutive bf16 values of a quad's block.
+__device__ __forceinline__ u32x2 mx8_quantize_quad_bf16(bf16x8 xb, unsigned* code) {
+  unsigned m = bf16x8_absmax_bits(xb);
+  m = max(m, dpp_quad_xor1(m));
+  m = max(m, dpp_quad_xor2(m));
+  *code = e8m0_code_e4m3(m >> 7);
+  return mx8_encode8_bf16(xb, *code);
+}
+
 }  // namespace mxq

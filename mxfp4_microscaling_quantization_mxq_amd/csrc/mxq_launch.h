@@ -8,6 +8,49 @@
 
 namespace mxq {
 
+// A paged cache: `pages` pages of 2^page_shift tokens, `heads` key/value
+// heads of `dim` elements.
+struct KvShape {
+  int64_t pages;
+  unsigned heads, dim, page_shift;
+};
+
+// r = x + residual (r = x without one), y = r / sqrt(mean r^2 + eps) * weight,
+// (q[rows][k], s[rows][k/32]) = MXFP8(y).
+hipError_t launch_rmsnorm_quantize_fp8(const void* x, const void* residual, const void* weight, bool bf16,
+                                       int64_t rows, int64_t k, float eps, void* r, uint8_t* q, uint8_t* s,
+                                       hipStream_t st);
+// New tokens' keys and values (row strides in elements) quantized into their
+// slots, and the slots' values read back.
+hipError_t launch_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, bool bf16,
+                            const int64_t* slots, int64_t tokens, const KvShape& c, bool fp4, uint8_t* kq, uint8_t* ks,
+                            uint8_t* vq, uint8_t* vs, hipStream_t st);
+hipError_t launch_kv_read(const uint8_t* kq, const uint8_t* ks, const uint8_t* vq, const uint8_t* vs,
+                          const int64_t* slots, int64_t tokens, const KvShape& c, bool fp4, void* k, void* v,
+                          bool bf16, hipStream_t st);
+
+// Attention of one new token per sequence over the paged cache.
+struct AttendArgs {
+  const uint16_t* q;  // bf16 [batch][q_heads][dim], rows q_stride elements apart
+  int64_t q_stride;
+  const uint8_t *kq, *ks, *vq, *vs;
+  const int32_t* table;  // [batch][table_width], rows table_stride apart
+  int64_t table_width, table_stride;
+  const int32_t* lens;  // [batch]
+  const float* sinks;   // [q_heads] or null
+  int64_t batch, window;
+  unsigned q_heads;
+  float scale;
+  void* out;  // [batch][q_heads][dim]
+  bool bf16_out;
+};
+// Blocks of such a call (sequences x splits of the length x cache heads x
+// groups of query heads), and the bytes of workspace its partial results take
+// (0 for one split).
+int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window);
+int64_t attend_workspace(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window);
+hipError_t launch_attend(const AttendArgs& a, const KvShape& c, bool fp4, void* workspace, hipStream_t st);
+
 hipError_t launch_mx_quantize(const void* x, bool bf16, int64_t rows, int64_t k, uint8_t* q, uint8_t* s,
                               hipStream_t st);
 // MXFP8: q[rows][k] E4M3 codes, s[rows][k/32] E8M0 codes.

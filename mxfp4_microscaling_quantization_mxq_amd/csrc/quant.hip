@@ -94,19 +94,11 @@ __global__ __launch_bounds__(256) void k_mx_quantize_f32(const u32x4* __restrict
                                                          int64_t nlanes) {
   int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= nlanes) return;
-  u32x4 a = __builtin_nontemporal_load(&x[2 * t]);
-  u32x4 b = __builtin_nontemporal_load(&x[2 * t + 1]);
-  unsigned m = max(max(max(a.x & 0x7FFFFFFFu, a.y & 0x7FFFFFFFu), max(a.z & 0x7FFFFFFFu, a.w & 0x7FFFFFFFu)),
-                   max(max(b.x & 0x7FFFFFFFu, b.y & 0x7FFFFFFFu), max(b.z & 0x7FFFFFFFu, b.w & 0x7FFFFFFFu)));
-  m = max(m, dpp_quad_xor1(m));
-  m = max(m, dpp_quad_xor2(m));
-  unsigned code = e8m0_code_from_expfield(m >> 23);
-  float scale = e8m0_as_scale(code);
-  unsigned out = 0;
-  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, __uint_as_float(a.x), __uint_as_float(a.y), scale, 0);
-  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, __uint_as_float(a.z), __uint_as_float(a.w), scale, 1);
-  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, __uint_as_float(b.x), __uint_as_float(b.y), scale, 2);
-  out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, __uint_as_float(b.z), __uint_as_float(b.w), scale, 3);
+  const f32x4 a = __builtin_nontemporal_load((const f32x4*)&x[2 * t]);
+  const f32x4 b = __builtin_nontemporal_load((const f32x4*)&x[2 * t + 1]);
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  unsigned code;
+  const unsigned out = mx_quantize_quad_f32(v, &code);
   st_stream(&q[t], out);
   if ((t & 3) == 0) s[t >> 2] = (uint8_t)code;
 }
@@ -172,8 +164,6 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(const unsigned* __restric
 // saturating (seen in the bit-exact comparison with the CPU oracle), and the
 // clamp is exact (448 * 2^e is a bf16 / fp32 number, and x * 2^-e is exact).
 // One lane = 8 elements, a quad = one block; a lane stores 8 code bytes.
-typedef short s16x2 __attribute__((ext_vector_type(2)));
-
 __global__ __launch_bounds__(256) void k_mx8_quantize_bf16(const u32x4* __restrict__ x, u32x2* __restrict__ q,
                                                            uint8_t* __restrict__ s, int64_t nlanes) {
   // kQuant8U chunks of 256 lanes per block, loads first (as k_mx_quantize_bf16)
@@ -188,11 +178,8 @@ __global__ __launch_bounds__(256) void k_mx8_quantize_bf16(const u32x4* __restri
 #pragma unroll
   for (int u = 0; u < kQuant8U; u++) {
     const int64_t t = t0 + 256 * u;
-    unsigned m = bf16x8_absmax_bits(xb[u]);
-    m = max(m, dpp_quad_xor1(m));
-    m = max(m, dpp_quad_xor2(m));
-    const unsigned code = e8m0_code_e4m3(m >> 7);
-    const u32x2 out = mx8_encode8_bf16(xb[u], code);
+    unsigned code;
+    const u32x2 out = mx8_quantize_quad_bf16(xb[u], &code);
     if (t < nlanes) {
       q[t] = out;
       if ((t & 3) == 0) s[t >> 2] = (uint8_t)code;
@@ -204,23 +191,11 @@ __global__ __launch_bounds__(256) void k_mx8_quantize_f32(const u32x4* __restric
                                                           uint8_t* __restrict__ s, int64_t nlanes) {
   int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= nlanes) return;
-  const u32x4 a = __builtin_nontemporal_load(&x[2 * t]);
-  const u32x4 b = __builtin_nontemporal_load(&x[2 * t + 1]);
-  unsigned m = max(max(max(a.x & 0x7FFFFFFFu, a.y & 0x7FFFFFFFu), max(a.z & 0x7FFFFFFFu, a.w & 0x7FFFFFFFu)),
-                   max(max(b.x & 0x7FFFFFFFu, b.y & 0x7FFFFFFFu), max(b.z & 0x7FFFFFFFu, b.w & 0x7FFFFFFFu)));
-  m = max(m, dpp_quad_xor1(m));
-  m = max(m, dpp_quad_xor2(m));
-  const unsigned code = e8m0_code_e4m3(m >> 23);
-  const float scale = e8m0_as_scale(code);
-  // |x| clamped to 448 * 2^e (fp32 bits: exponent field code + 8, mantissa .11)
-  const unsigned lim = ((code + 8u) << 23) | 0x600000u;
-  auto clamp = [&](unsigned w) { return __uint_as_float(min(w & 0x7FFFFFFFu, lim) | (w & 0x80000000u)); };
-  s16x2 lo = {0, 0}, hi = {0, 0};
-  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, clamp(a.x), clamp(a.y), scale, false);
-  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, clamp(a.z), clamp(a.w), scale, true);
-  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, clamp(b.x), clamp(b.y), scale, false);
-  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, clamp(b.z), clamp(b.w), scale, true);
-  q[t] = (u32x2){__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
+  const f32x4 a = __builtin_nontemporal_load((const f32x4*)&x[2 * t]);
+  const f32x4 b = __builtin_nontemporal_load((const f32x4*)&x[2 * t + 1]);
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  unsigned code;
+  q[t] = mx8_quantize_quad_f32(v, &code);
   if ((t & 3) == 0) s[t >> 2] = (uint8_t)code;
 }
 
@@ -335,18 +310,8 @@ __global__ __launch_bounds__(256) void k_mx_quantize_hadamard(const u32x4* __res
     const int64_t t = t0 + 256 * u;
     rotate8<HK>(v[u], lane);
     // MXFP4 of the rotated block (as k_mx_quantize_f32)
-    unsigned m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(v[u][i]) & 0x7FFFFFFFu);
-    m = max(m, dpp_quad_xor1(m));
-    m = max(m, dpp_quad_xor2(m));
-    const unsigned code = e8m0_code_from_expfield(m >> 23);
-    const float scale = e8m0_as_scale(code);
-    unsigned out = 0;
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[u][0], v[u][1], scale, 0);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[u][2], v[u][3], scale, 1);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[u][4], v[u][5], scale, 2);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[u][6], v[u][7], scale, 3);
+    unsigned code;
+    const unsigned out = mx_quantize_quad_f32(v[u], &code);
     if (t < nlanes) {
       q[t] = out;
       if ((t & 3) == 0) s[t >> 2] = (uint8_t)code;

@@ -1,0 +1,446 @@
+"""GPU tests of the serving operators against float64: the norm with MXFP8
+output, the paged cache's write and read, and attention over it.
+
+Tolerances, from the kernels' number formats (u = 2^-24 is the fp32 unit):
+- norm: codes must be the MXFP8 codes of some y' with |y' - y| <= delta |y|.
+  A thread adds at most 64 squares in a row (rows up to 2^16 elements), then at
+  most 22 partial sums, all positive, so the sum is within 86 u and its root
+  within half that; the factor's rounding and two products add 3 u:
+  delta = 64 u = 2^-18 covers 46 u.
+- cache: bit-exact.
+- attention, with A = sum_t p_t |V_t| / denominator: a score is a sum of D
+  exact products in fp32 (at most D roundings of at most M = |scale| sum |q K|),
+  rounded again when scaled: e_s = (D + 4) u M; a probability is then within
+  2 e_s (its own and the maximum's part cancel only in exact arithmetic) plus
+  2^-21 for the exponential's argument and result; the sums over n tokens, the
+  waves and the splits add at most (n / 8 + 64) u, and P's terms leave 2^-17
+  (bf16 output) or less (fp32).  bound = A (2 e_s + 2^-21 + (n / 8 + 64) u [+
+  2^-16 for bf16 output]), plus half a bf16 unit for bf16 output.
+"""
+import numpy as np
+import pytest
+
+import oracle
+import mxfp4_microscaling_quantization_mxq_amd as mxq
+from mxfp4_microscaling_quantization_mxq_amd import synth
+
+import serving_model as model
+from gpu_util import check_product, dev, host, w4a8_block_sum_allowance
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    mxq.capi()  # raises if the library is not built
+    yield
+    torch.cuda.synchronize()
+
+
+def stored(x, dtype):
+    """fp32 array -> (as stored: bf16 bits or fp32, its float64 values)."""
+    x = np.ascontiguousarray(x, dtype=np.float32)
+    a = synth.f32_to_bf16_bits(x) if dtype == "bf16" else x
+    return a, oracle.to_f64(a)
+
+
+# ------------------------------------------------------------------ norm
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,k", [(1, 32), (3, 96), (5, 512), (6, 544), (9, 1024), (7, 1056), (4, 2048), (3, 4096),
+                                    (5, 4128), (2, 8192), (3, 8224), (2, 16384), (2, 16416), (1, 32768), (2, 32800),
+                                    (1, 65536), (260, 64)])
+def test_norm(rows, k, residual, dtype):
+    rng = np.random.default_rng(rows * 1000003 + k)
+    spread = np.exp2(rng.integers(-12, 13, size=(rows, 1)))
+    x, x64 = stored(rng.laplace(size=(rows, k)) * spread, dtype)
+    w, w64 = stored(1 + 0.3 * rng.standard_normal(k), dtype)
+    p, p64 = stored(rng.standard_normal((rows, k)) * spread * 3, dtype) if residual else (None, None)
+    eps = 1e-5
+    q, s, r = mxq.rmsnorm_quantize_fp8(dev(x), dev(w), dev(p) if residual else None, eps=eps)
+    r64, y = model.norm_rows(x64, p64, w64, eps, dtype == "bf16")
+    assert np.array_equal(oracle.to_f64(host(r)), r64), "the stored sum"
+    model.check_mx8(host(q), host(s), y, 2.0 ** -18, f"{rows}x{k} {dtype}")
+
+
+def test_norm_zero_rows_signs_and_extremes():
+    k = 1056
+    x = np.zeros((6, k), dtype=np.float32)
+    x[1] = -0.0
+    x[2, 7] = 2.0 ** -40  # all but one element zero, far below eps
+    x[3] = -3.0
+    x[4, :] = np.float32(1e15)  # squares near 1e30, their sum 1e33
+    x[5, ::2], x[5, 1::2] = 2.0 ** -60, -(2.0 ** -60)  # squares below fp32's normal range
+    w = np.ones(k, dtype=np.float32)
+    w[::5] = -2
+    for dtype in ("bf16", "f32"):
+        a, a64 = stored(x, dtype)
+        wa, w64 = stored(w, dtype)
+        q, s, r = mxq.rmsnorm_quantize_fp8(dev(a), dev(wa), eps=1e-6)
+        _, y = model.norm_rows(a64, None, w64, 1e-6, dtype == "bf16")
+        model.check_mx8(host(q), host(s), y, 2.0 ** -18, dtype)
+        assert not host(s)[0].any() and not (host(q)[0] & 0x7F).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [96, 4128, 40000])
+def test_norm_in_place(dtype, k):
+    rng = np.random.default_rng(k)
+    x, _ = stored(rng.standard_normal((3, k)), dtype)
+    p, _ = stored(rng.standard_normal((3, k)), dtype)
+    w, _ = stored(rng.standard_normal(k), dtype)
+    q, s, r = mxq.rmsnorm_quantize_fp8(dev(x), dev(w), dev(p))
+    for which in ("residual", "x"):
+        xd, pd = dev(x), dev(p)
+        target = pd if which == "residual" else xd
+        q2, s2, r2 = mxq.rmsnorm_quantize_fp8(xd, dev(w), pd, r=target)
+        assert r2 is target and torch.equal(target, r)
+        assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+def test_norm_feeds_the_w4a8_product():
+    """The codes go straight into gemm_w4a8: the same product as from the
+    codes of the separately quantized fp32 norm."""
+    rng = np.random.default_rng(3)
+    x, x64 = stored(rng.standard_normal((16, 512)), "f32")
+    w, w64 = stored(1 + 0.1 * rng.standard_normal(512), "f32")
+    q, s, _ = mxq.rmsnorm_quantize_fp8(dev(x), dev(w))
+    bq, bs = mxq.quantize(dev(rng.standard_normal((96, 512)).astype(np.float32)))
+    c = host(mxq.gemm_w4a8(q, s, bq, bs, torch.float32))
+    a = oracle.mx8_dequantize(host(q), host(s))
+    ref, size = oracle.gemm_nt(a, oracle.mx_dequantize(host(bq), host(bs)))
+    allowance = w4a8_block_sum_allowance(host(q), host(s), host(bq), host(bs))
+    check_product(c, ref, size, False, "norm into w4a8", allowance)
+    _, y = model.norm_rows(x64, None, w64, 1e-6, False)
+    assert (np.abs(a - y) <= np.abs(y).max() * 2.0 ** -3).all()
+
+
+# ------------------------------------------------------------------ cache
+
+def filled(shape, seed):
+    return np.random.default_rng(seed).integers(0, 256, size=shape, dtype=np.uint8)
+
+
+def new_cache(pages, page, heads, d, fmt, seed=0):
+    """A cache of arbitrary bytes (host arrays)."""
+    w = d if fmt == "mxfp8" else d // 2
+    return [filled((pages, heads, page, w), seed), filled((pages, heads, page, d // 32), seed + 1),
+            filled((pages, heads, page, w), seed + 2), filled((pages, heads, d // 32, page), seed + 3)]
+
+
+def on_device(cache):
+    return mxq.KVCache(*(dev(a) for a in cache))
+
+
+def write_model(cache, k, v, slots, fmt):
+    """The cache after the write; k, v as stored, [tokens, heads, D]."""
+    cache = [a.copy() for a in cache]
+    kq, ks, vq, vs = cache
+    pages, _, page = kq.shape[:3]
+    for t, slot in enumerate(slots):
+        if not 0 <= slot < pages * page:
+            continue
+        pg, pos = slot // page, slot % page
+        kq[pg, :, pos], ks[pg, :, pos] = model.quantize_rows(np.ascontiguousarray(k[t]), fmt)
+        vq[pg, :, pos], vs[pg, :, :, pos] = model.quantize_rows(np.ascontiguousarray(v[t]), fmt)
+    return cache
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens,heads,d,page", [(1, 1, 32, 16), (3, 2, 64, 16), (37, 8, 128, 16), (65, 3, 128, 64),
+                                                 (130, 5, 96, 32), (7, 2, 256, 1024), (1000, 1, 64, 256)])
+def test_cache_write_and_read(tokens, heads, d, page, dtype, fmt):
+    rng = np.random.default_rng(tokens * 7 + d)
+    pages = tokens // page + 3
+    cache = new_cache(pages, page, heads, d, fmt)
+    # views of a fused projection's output, the value ahead of the key
+    width = (2 * heads + 3) * d
+    x, _ = stored(rng.laplace(size=(tokens, width)) * np.exp2(rng.integers(-9, 10, size=(tokens, 1))), dtype)
+    xd = dev(x)
+    vd, kd = xd[:, d:(heads + 1) * d].unflatten(1, (heads, d)), xd[:, (heads + 3) * d:].unflatten(1, (heads, d))
+    v = x[:, d:(heads + 1) * d].reshape(tokens, heads, d)
+    k = x[:, (heads + 3) * d:].reshape(tokens, heads, d)
+    slots = rng.permutation(pages * page)[:tokens].astype(np.int64)
+    slots[rng.random(tokens) < 0.1] = -1
+    if tokens > 3:
+        slots[1], slots[3] = pages * page, 2 ** 40  # past the end: skipped
+    c = on_device(cache)
+    mxq.kv_append(c, kd, vd, dev(slots))
+    want = write_model(cache, k, v, slots, fmt)
+    for name, got, ref in zip(("kq", "ks", "vq", "vs"), c, want):
+        assert np.array_equal(host(got), ref), name
+    for out in (torch.float32, torch.bfloat16):
+        kr, vr = mxq.kv_read(c, dev(slots), dtype=out)
+        for t, slot in enumerate(slots):
+            ref = (0.0, 0.0)
+            if 0 <= slot < pages * page:
+                ref = model.token_rows(want, slot // page, slot % page, fmt)
+            assert np.array_equal(oracle.to_f64(host(kr[t])), np.broadcast_to(ref[0], (heads, d))), t
+            assert np.array_equal(oracle.to_f64(host(vr[t])), np.broadcast_to(ref[1], (heads, d))), t
+
+
+# ------------------------------------------------------------------ attention
+
+NAN_BYTES = {"mxfp8": 0x7F, "mxfp4": 0xFF}  # E4M3 NaN; E2M1 has none
+
+
+def filled_cache(rng, pages, page, heads, d, fmt):
+    """A host cache of quantized normal keys and values."""
+    out = []
+    for v in range(2):
+        x = rng.standard_normal((pages * heads * page, d)).astype(np.float32) * np.exp2(
+            rng.integers(-2, 3, size=(pages * heads * page, 1))).astype(np.float32)
+        q, s = model.quantize_rows(x, fmt)
+        s = s.reshape(pages, heads, page, d // 32)
+        out += [q.reshape(pages, heads, page, -1), np.ascontiguousarray(s.transpose(0, 1, 3, 2)) if v else s]
+    return out
+
+
+def poison(cache, table, lens, page, fmt, window=0):
+    """NaN codes and NaN scales everywhere but at the visible positions."""
+    kq, ks, vq, vs = cache
+    seen = np.zeros((kq.shape[0], page), dtype=bool)
+    for b, n in enumerate(lens):
+        for t in range(max(0, n - window) if window else 0, n):
+            if 0 <= table[b, t // page] < kq.shape[0]:
+                seen[table[b, t // page], t % page] = True
+    dead = ~seen
+    for a in (kq, vq):
+        a.transpose(0, 2, 1, 3)[dead] = NAN_BYTES[fmt]
+    ks.transpose(0, 2, 1, 3)[dead] = 255
+    vs.transpose(0, 3, 1, 2)[dead] = 255
+
+
+def attend_case(seed, lens, heads, group, d, page, fmt, out=torch.float32, window=0, sinks=False, scale=None,
+                holes=(), extra_width=2, q_scale=1.0):
+    rng = np.random.default_rng(seed)
+    batch = len(lens)
+    counts = [-(-n // page) for n in lens]
+    pages = sum(counts) + 2
+    cache = filled_cache(rng, pages, page, heads, d, fmt)
+    order = rng.permutation(pages).astype(np.int32)
+    table = np.full((batch, max(counts + [1]) + extra_width), -7, dtype=np.int32)
+    at = 0
+    for b, c in enumerate(counts):
+        table[b, :c] = order[at:at + c]
+        table[b, c:] = 2 ** 31 - 1 if b % 2 else -1  # names no page
+        at += c
+    for b, p in holes:
+        table[b, p] = pages if p % 2 else -1
+    poison(cache, table, lens, page, fmt, window)
+    qbits, q64 = stored(rng.standard_normal((batch, heads * group * d + 3 * d)) * q_scale, "bf16")
+    q64 = q64[:, d:d + heads * group * d].reshape(batch, heads * group, d)
+    qd = dev(qbits)[:, d:d + heads * group * d].unflatten(1, (heads * group, d))
+    sk = rng.standard_normal(heads * group).astype(np.float32) * 2 if sinks else None
+    y = mxq.paged_attention(qd, on_device(cache), dev(table), dev(np.array(lens, dtype=np.int32)), scale=scale,
+                            window=window, sinks=dev(sk) if sinks else None, out_dtype=out)
+    torch.cuda.synchronize()
+    ref, size, mag = model.attention(q64, cache, table, lens, fmt, d ** -0.5 if scale is None else scale, window, sk)
+    n = max(max(lens), 1)
+    bound = size * (2 * (d + 4) * U * mag[..., None] + 2.0 ** -21 + (n / 8 + 64) * U)
+    got = oracle.to_f64(host(y))
+    if out == torch.bfloat16:
+        bound = bound + size * 2.0 ** -16
+        bound = bound + (np.abs(ref) + bound) * 2.0 ** -8
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), (f"{int(bad.sum())} of {bad.size} off, first {np.argwhere(bad)[0]}: "
+                           f"{got[bad][0]} for {ref[bad][0]}, bound {bound[bad][0]}")
+    return got
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64])
+def test_attention_formats_and_lengths(page, d, fmt, out):
+    """Lengths around tile, page and split ends, an empty sequence among them."""
+    attend_case(d + page, [0, 1, 7, 15, 16, 17, 31, 32, 33, 63, 65, 127, 129, 300], 2, 3, d, page, fmt, out)
+
+
+@pytest.mark.parametrize("heads,group", [(1, 1), (3, 1), (2, 8), (1, 15), (2, 16), (1, 17), (1, 32), (1, 40), (1, 64),
+                                         (1, 65), (2, 71), (1, 128)])
+def test_attention_head_layouts(heads, group):
+    """Groups below, at and past 16 query heads a cache head, and past what one block takes."""
+    attend_case(group, [5, 97, 261], heads, group, 64, 16, "mxfp8")
+    attend_case(group, [130], heads, group, 128, 32, "mxfp4", torch.bfloat16)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256, 512, 1024])
+def test_attention_page_sizes(page):
+    attend_case(page, [page - 1, page + 1, 2 * page + 5], 1, 4, 64, page, "mxfp8")
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 31, 33, 100, 127, 128, 5000])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_attention_window_and_sinks(window, sinks):
+    attend_case(window, [0, 1, 33, 100, 128, 129, 517], 2, 4, 64, 16, "mxfp8", window=window, sinks=sinks)
+
+
+def test_attention_sinks_over_splits():
+    attend_case(11, [1500, 3, 0, 700], 2, 8, 128, 16, "mxfp8", sinks=True)
+    attend_case(12, [1500], 2, 8, 128, 64, "mxfp4", torch.bfloat16, sinks=True)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_attention_pages_the_table_does_not_name(fmt):
+    """Entries outside the cache hide their positions, a whole sequence's among them."""
+    attend_case(5, [100, 40, 70, 16], 2, 2, 64, 16, fmt,
+                holes=[(0, 0), (0, 3), (1, 2), (2, 1), (2, 4), (3, 0)])
+
+
+def test_attention_length_past_the_table():
+    rng = np.random.default_rng(0)
+    cache = filled_cache(rng, 3, 16, 1, 64, "mxfp8")
+    table = np.array([[2, 0], [1, 1]], dtype=np.int32)
+    qb, q64 = stored(rng.standard_normal((2, 2, 64)), "bf16")
+    y = mxq.paged_attention(dev(qb), on_device(cache), dev(table), dev(np.array([2 ** 31 - 1, -5], dtype=np.int32)),
+                            out_dtype=torch.float32)
+    ref, size, mag = model.attention(q64, cache, table, [32, 0], "mxfp8", 64 ** -0.5)
+    assert (np.abs(host(y) - ref) <= size * (2 * 68 * U * mag[..., None] + 2.0 ** -20)).all()
+    assert not host(y)[1].any()
+
+
+def test_attention_large_scores():
+    """Scores in the hundreds: one position takes nearly all the weight."""
+    attend_case(21, [33, 300], 1, 8, 128, 16, "mxfp8", q_scale=64.0)
+    attend_case(22, [33, 300], 1, 8, 128, 16, "mxfp8", scale=0.0)  # the mean of V
+    attend_case(23, [33, 300], 1, 8, 64, 16, "mxfp4", scale=-0.25)
+
+
+def test_attention_workspace_table_slice_and_repeat():
+    """A caller's workspace (of arbitrary content), a sliced table and a
+    repeated call give the same bits."""
+    rng = np.random.default_rng(9)
+    cache = on_device(filled_cache(rng, 60, 16, 2, 64, "mxfp8"))
+    table = dev(rng.permutation(60).astype(np.int32).reshape(1, 60))
+    wide = torch.cat((table, table[:, :5]), 1)
+    lens = dev(np.array([955], dtype=np.int32))
+    q = dev(stored(rng.standard_normal((1, 8, 64)), "bf16")[0])
+    a = mxq.paged_attention(q, cache, table, lens)
+    b = mxq.paged_attention(q, cache, wide[:, :60], lens)
+    ws = torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device="cuda")
+    c = mxq.paged_attention(q, cache, table, lens, workspace=ws)
+    out = torch.empty_like(a)
+    assert mxq.paged_attention(q, cache, table, lens, workspace=ws, out=out) is out
+    assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, out)
+
+
+def test_attention_many_small_pages_per_split():
+    """More page ids than one block keeps: the length is split further."""
+    rng = np.random.default_rng(2)
+    n = 40000
+    pages = 64
+    cache = filled_cache(rng, pages, 16, 1, 64, "mxfp4")
+    table = rng.integers(0, pages, size=(1, -(-n // 16))).astype(np.int32)
+    table = np.repeat(table, 1100, axis=0)  # so many sequences that one split each would do
+    qb, q64 = stored(rng.standard_normal((1100, 1, 64)), "bf16")
+    lens = np.full(1100, 16, dtype=np.int32)
+    lens[7] = n
+    y = host(mxq.paged_attention(dev(qb), on_device(cache), dev(table), dev(lens), out_dtype=torch.float32))
+    for b in (0, 7, 1099):
+        ref, size, mag = model.attention(q64[b:b + 1], cache, table[b:b + 1], lens[b:b + 1], "mxfp4", 0.125)
+        bound = size * (2 * 68 * U * mag[..., None] + 2.0 ** -21 + (n / 8 + 64) * U)
+        assert (np.abs(y[b:b + 1] - ref) <= bound).all(), b
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_offsets_past_32_bits(fmt):
+    """Slots whose codes lie more than 2^32 bytes into the cache."""
+    heads, d, page = 8, 128, 256
+    w = d if fmt == "mxfp8" else d // 2
+    pages = (1 << 32) // (heads * page * w) + 40
+    cache = mxq.kv_cache(pages, page, heads, d, fmt)
+    rng = np.random.default_rng(1)
+    n = 700
+    table = np.array([[pages - 1, 5, pages - 30]], dtype=np.int32)
+    slots = np.array([int(table[0, t // page]) * page + t % page for t in range(n)], dtype=np.int64)
+    k, _ = stored(rng.standard_normal((n, heads, d)), "bf16")
+    v, _ = stored(rng.standard_normal((n, heads, d)), "bf16")
+    mxq.kv_append(cache, dev(k), dev(v), dev(slots))
+    used = torch.from_numpy(table[0].astype(np.int64)).cuda()
+    small = [host(a[used]) for a in cache]
+    zero = [np.zeros_like(a) for a in small]
+    local = np.array([(t // page) * page + t % page for t in range(n)])
+    for got, ref in zip(small, write_model(zero, k, v, local, fmt)):
+        assert np.array_equal(got, ref)
+    kr, vr = mxq.kv_read(cache, dev(slots), dtype=torch.float32)
+    for t in (0, 255, 256, 699):
+        ref = model.token_rows(small, t // page, t % page, fmt)
+        assert np.array_equal(host(kr[t]), ref[0]) and np.array_equal(host(vr[t]), ref[1])
+    qb, q64 = stored(rng.standard_normal((1, heads, d)), "bf16")
+    y = host(mxq.paged_attention(dev(qb), cache, dev(table), dev(np.array([n], dtype=np.int32)),
+                                 out_dtype=torch.float32))
+    ref, size, mag = model.attention(q64, small, np.array([[0, 1, 2]]), [n], fmt, d ** -0.5)
+    assert (np.abs(y - ref) <= size * (2 * (d + 4) * U * mag[..., None] + 2.0 ** -21 + (n / 8 + 64) * U)).all()
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def step(x, w, res, cache, k, v, slots, q, table, lens, qo, so, ro, out, ws):
+    mxq.rmsnorm_quantize_fp8(x, w, res, q=qo, s=so, r=ro)
+    mxq.kv_append(cache, k, v, slots)
+    mxq.paged_attention(q, cache, table, lens, out=out, workspace=ws)
+
+
+def step_state(seed):
+    rng = np.random.default_rng(seed)
+    t = lambda *s: dev(stored(rng.standard_normal(s), "bf16")[0])  # noqa: E731
+    cache = on_device(filled_cache(rng, 40, 16, 2, 64, "mxfp8"))
+    table = dev(rng.permutation(40).astype(np.int32).reshape(2, 20))
+    lens = dev(np.array([300, 41], dtype=np.int32))
+    slots = torch.stack([table[0, 18].long() * 16 + 11, table[1, 2].long() * 16 + 8])
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    e = lambda *s, dt=torch.uint8: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    return (t(2, 256), t(256), t(2, 256), cache, t(2, 2, 64), t(2, 2, 64), slots, t(2, 8, 64), table, lens,
+            e(2, 256), e(2, 8), e(2, 256, dt=torch.bfloat16), e(2, 8, 64, dt=torch.bfloat16), ws)
+
+
+def results(s):
+    return [a.clone() for a in (s[10], s[11], s[12], s[13], *s[3])]
+
+
+def test_graph_replays_match_eager():
+    s = step_state(1)
+    step(*s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(*s)
+    for seed in (2, 3, 4):
+        fresh = step_state(seed)
+        for i in (0, 1, 2, 4, 5, 7):
+            s[i].copy_(fresh[i])
+        for a in (s[10], s[11], s[12], s[13]):
+            a.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = results(s)
+        step(*s)
+        torch.cuda.synchronize()
+        for a, b in zip(got, results(s)):
+            assert torch.equal(a, b)
+
+
+def test_work_on_another_stream():
+    s = step_state(5)
+    step(*s)
+    torch.cuda.synchronize()
+    want = results(s)
+    for a in (s[10], s[11], s[12], s[13]):
+        a.zero_()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        step(*s)
+        got = mxq.paged_attention(s[7], s[3], s[8], s[9])  # its own workspace, from this stream's pool
+    st.synchronize()
+    for a, b in zip(results(s), want):
+        assert torch.equal(a, b)
+    assert torch.equal(got, want[3])
