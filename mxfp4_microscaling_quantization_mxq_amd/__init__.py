@@ -120,15 +120,24 @@ def _check(code: int, what: str):
 
 # ------------------------------------------------------------------ helpers
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
-    torch = _torch()
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream of the current device as a raw handle.  (The Stream
+    object of torch.cuda.current_stream() costs 3 us to build, as much as a
+    launch.)"""
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _dtype_code(dt) -> int:
@@ -151,12 +160,12 @@ def _need(t, name, dtype=None, shape=None, ndim=2, device=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if dtype is not None:
+    if dtype is not None and t.dtype is not dtype:
         allowed = dtype if isinstance(dtype, tuple) else (dtype,)
         if t.dtype not in allowed:
             raise TypeError(f"{name} must be {' or '.join(str(d) for d in allowed)}, got {t.dtype}")
     if shape is not None:
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     elif t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
@@ -168,12 +177,14 @@ def _on_device(**tensors):
     """Every tensor of the call on one and the same device (cuda/hip)."""
     dev = None
     for name, t in tensors.items():
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0 or not t.is_cuda:
             raise ValueError(f"{name} must be a device (cuda/hip) tensor")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other operands on {dev}")
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name} is on {t.device}, the other operands on device {dev}")
+    return dev
 
 
 def _floats():

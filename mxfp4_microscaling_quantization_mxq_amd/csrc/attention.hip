@@ -7,15 +7,21 @@
 // Mapping.  The query heads that share a cache head are the 16 columns of the
 // 16x16x32 bf16 MFMA (more of them: further waves of the block take further
 // groups of 16), and a wave walks over tiles of 32 tokens:
-//   S^T = K Q^T: K rows as the A operand.  Lane (i = lane & 15, g = lane >> 4)
-//     holds token 8 (i / 4) + i % 4 (second product: + 4) and 32 consecutive
-//     elements 128 p + 32 g of its row, so its share has one scale and the
-//     result puts tokens 8 g .. 8 g + 7 of head i into lane (i, g);
+//   S^T = K Q^T: K rows as the A operand, 16 tokens a product.  Lane (i =
+//     lane & 15, g = lane >> 4) holds tokens i and 16 + i and 32 consecutive
+//     elements 128 p + 32 g of their rows, so a share has one scale, and the
+//     results put tokens 4 g + r and 16 + 4 g + r (r < 4) of head i into lane
+//     (i, g);
 //   O^T += V^T P^T: those eight probabilities ARE the B operand's k slots, so
 //     P never crosses lanes.  The A operand is V^T: lane (i, g) loads D / 16
-//     consecutive elements of tokens 8 g .. 8 g + 7, and product j takes
+//     consecutive elements of the same eight tokens, and product j takes
 //     element j of them (row i <-> d = i D / 16 + j), which turns the
 //     transpose of V into byte selects inside the lane.
+// Either half of a tile lies in one page, so every address is a scalar base
+// (a buffer resource) plus a constant lane offset.  A half that is not there
+// (past the length, or a table entry that names no page) has a resource of
+// size zero: its loads return zeros and move nothing, so the loop loads
+// without branches and the compiler's wait counts leave the tiles ahead in flight.
 // Dequantized E4M3 / E2M1 values are exact in bf16.  Scores, maxima, sums and
 // O are fp32.  P enters the product as a sum of bf16 terms: two (2^-17 of P)
 // for bf16 output, where one term's 2^-9 would add to the output's own
@@ -29,7 +35,7 @@
 // are cut into equal ranges, one a block of 4 waves, so a batch of uneven
 // lengths keeps every CU busy to the end.  A range that ends inside a unit
 // leaves partial results (m, sum, O) in the workspace, and k_attend_join adds
-// a unit's parts in order.  Where no unit is long and there are many, a block
+// a unit's parts in order.  Where all sequences are short, a block of 8 waves
 // takes one unit and nothing is joined.
 #include "mxq_gemm_common.h"
 #include "mxq_kv.h"
@@ -39,11 +45,16 @@ namespace mxq {
 
 namespace {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kTile = 32;       // tokens a wave takes at a time
-constexpr int kWaves = 4;       // waves of a block
-constexpr int kThreads = 64 * kWaves;
+constexpr int kRangeWaves = 4;  // waves of a block that takes a range
+// Waves of a block that takes one unit: the partial O of eight waves of 256
+// elements a head would not leave LDS for a second block.
+constexpr int unit_waves(int d) { return d == 256 ? 4 : 8; }
+constexpr int kMaxUnitTiles16 = 4;  // head tiles of a unit: one to four waves share the range's cache head
 constexpr int kHeadTile = 16;   // query heads of one MFMA column set
-constexpr int64_t kMaxLen = 0x7FFFFFC0;  // tokens of a sequence (token indexes are 32 bits)
+constexpr int64_t kMaxLen = 0x7FFF0000;  // tokens of a sequence (token indexes, also a few tiles past it, are 32 bits)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendParams {
@@ -53,10 +64,18 @@ struct AttendParams {
   unsigned tiles16;      // head tiles of 16 per cache head
   unsigned tile_groups;  // units per sequence and cache head
   unsigned block_tiles;  // head tiles of a unit: 1, 2 or 4
-  bool ranges;           // blocks take ranges of the flattened list, or one unit each
-  unsigned* first;       // [batch + 1] first flattened tile of each sequence, then their sum
+  // Workspace: for each unit that spans blocks, {its parts, the block that
+  // opened it, the unit}.  With many units (by_block) the records are indexed
+  // by that block (a block opens at most one unit without closing it), else by
+  // unit; records with fewer than two parts name nothing to join.
+  bool by_block;
+  int* parts;               // [blocks or units][4]
   float *part_o, *part_ml;  // [2 blocks][16 block_tiles][D], [2 blocks][16 block_tiles][2]
 };
+
+// The compiler keeps what it cannot prove to be the same in every lane in
+// vector registers; loop bounds and addresses are scalar only with this.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Visible tokens of a sequence: [start, len), in tiles [t0, t1).  A length
 // above what the page table can name is cut to it.
@@ -72,79 +91,74 @@ __device__ __forceinline__ Span span_of(const AttendParams& p, int64_t b) {
   return span_tiles(p.a.window > 0 ? (int)max((int64_t)0, n - p.a.window) : 0, (int)n);
 }
 
-// Tiles of a range for a sum of all tiles: an equal share of each of 2^9
-// blocks (two a CU), and enough to give every wave one.
-constexpr int kRangeShift = 9;
-__device__ __forceinline__ unsigned range_tiles(unsigned sum) {
-  return max((sum >> kRangeShift) + ((sum & ((1u << kRangeShift) - 1)) != 0), (unsigned)kWaves);
+// Blocks that share the flattened list: as many as keep the memory busy.  Eight
+// waves a CU do that with rows of 128 bytes and more; sixteen with rows of 64
+// and less, whose tiles are half the bytes for the same instructions.
+constexpr int range_shift(int row_bytes) { return row_bytes >= 128 ? 9 : 10; }
+
+// Tiles of a range: an equal share of 2^shift blocks, and enough to give every
+// wave one.
+__device__ __forceinline__ unsigned range_tiles(unsigned sum, int shift) {
+  return max((sum >> shift) + ((sum & ((1u << shift) - 1)) != 0), (unsigned)kRangeWaves);
 }
 
 template <int D, bool kFp4>
 struct Tile {
-  static constexpr int kRow = kFp4 ? D / 2 : D;       // bytes of a token's row
-  static constexpr int kLaneK = kRow / 4;             // bytes of it per lane group
-  static constexpr int kLaneV = kRow / 16;            // bytes of it per lane column
+  static constexpr int kRow = kFp4 ? D / 2 : D;         // bytes of a token's row
   static constexpr int kRuns = D >= 128 ? D / 128 : 1;  // K: pieces of 32 elements a lane holds (D = 64: one of 16)
-  unsigned k[2][kLaneK / 4];
+  static constexpr int kRun = kRow / 4 / kRuns;         // bytes of one
+  static constexpr int kLaneV = kRow / 16;              // V: bytes of a token a lane holds
+  unsigned k[2][kRuns * kRun / 4], v[8][kLaneV >= 4 ? kLaneV / 4 : 1];
   uint8_t ks[2][kRuns];
-  unsigned v[8][kLaneV >= 4 ? kLaneV / 4 : 1];
-  u32x2 vs;
+  unsigned vs[2];
 };
 
-// Each byte of the cache is read by one wave (or by the waves of one block),
-// so the loads carry the streaming hint.
+// Loads of the cache's codes: each byte is read by one wave (or by the waves
+// of one block), so they carry the streaming hint (2).
 template <int N>
-__device__ __forceinline__ void load_bytes(const uint8_t* p, unsigned* o) {
+__device__ __forceinline__ void load_bytes(__amdgpu_buffer_rsrc_t r, int off, unsigned* o) {
   if constexpr (N == 2) {
-    o[0] = __builtin_nontemporal_load((const uint16_t*)p);
+    o[0] = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 2);
   } else if constexpr (N == 4) {
-    o[0] = __builtin_nontemporal_load((const unsigned*)p);
+    o[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 2);
   } else if constexpr (N == 8) {
-    const u32x2 w = __builtin_nontemporal_load((const u32x2*)p);
+    const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 2);
     o[0] = w.x, o[1] = w.y;
   } else {
     static_assert(N % 16 == 0);
 #pragma unroll
     for (int i = 0; i < N / 16; i++) {
-      const u32x4 w = __builtin_nontemporal_load(&((const u32x4*)p)[i]);
+      const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * i, 0, 2);
       o[4 * i] = w.x, o[4 * i + 1] = w.y, o[4 * i + 2] = w.z, o[4 * i + 3] = w.w;
     }
   }
 }
 
-// K rows of this lane's two tokens: rows `row` and `row` + 4 of a page that
-// starts at kq (codes) and ks (scales).
+// Where 16 consecutive tokens of one cache head lie: row `row` of the cache
+// (page * heads + head) * P + position, or nowhere (on = false).
 template <int D, bool kFp4>
-__device__ __forceinline__ void load_k(const uint8_t* kq, const uint8_t* ks, unsigned row, int g, Tile<D, kFp4>& t) {
+__device__ __forceinline__ void load_k(const AttendParams& p, int64_t row, bool on, int h, int i, int g, Tile<D, kFp4>& t) {
   typedef Tile<D, kFp4> T;
+  const __amdgpu_buffer_rsrc_t rq = panel_rsrc(p.a.kq + row * T::kRow, on ? 16 * T::kRow : 0);
+  const __amdgpu_buffer_rsrc_t rs = panel_rsrc(p.a.ks + row * (D / 32), on ? 16 * (D / 32) : 0);
 #pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const uint8_t* base = kq + (row + 4 * h) * T::kRow;
-    const uint8_t* sb = ks + (row + 4 * h) * (D / 32);
-    if constexpr (D == 64) {
-      load_bytes<T::kLaneK>(base + g * T::kLaneK, t.k[h]);
-      t.ks[h][0] = sb[g >> 1];
-    } else {
-      constexpr int kRun = T::kRow / T::kRuns / 4;  // bytes of 32 elements
-#pragma unroll
-      for (int r = 0; r < T::kRuns; r++) {
-        load_bytes<kRun>(base + r * 4 * kRun + g * kRun, t.k[h] + r * kRun / 4);
-        t.ks[h][r] = sb[4 * r + g];
-      }
-    }
+  for (int r = 0; r < T::kRuns; r++) {
+    load_bytes<T::kRun>(rq, i * T::kRow + g * T::kRun + r * 4 * T::kRun, t.k[h] + r * T::kRun / 4);
+    t.ks[h][r] = __builtin_amdgcn_raw_buffer_load_b8(rs, i * (D / 32) + (D == 64 ? g >> 1 : g + 4 * r), 0, 0);
   }
 }
-
-// V rows `row` .. `row` + 7 of a page that starts at vq (codes) and vs (scales).
 template <int D, bool kFp4>
-__device__ __forceinline__ void load_v(const uint8_t* vq, const uint8_t* vs, unsigned row, unsigned shift, int i,
+__device__ __forceinline__ void load_v(const AttendParams& p, int64_t ph, unsigned pos, bool on, int h, int i, int g,
                                        Tile<D, kFp4>& t) {
   typedef Tile<D, kFp4> T;
-  const uint8_t* base = vq + row * T::kRow + i * T::kLaneV;
+  const unsigned shift = p.c.page_shift;
+  const __amdgpu_buffer_rsrc_t rq = panel_rsrc(p.a.vq + ((ph << shift) + pos) * T::kRow, on ? 16 * T::kRow : 0);
+  const __amdgpu_buffer_rsrc_t rs =
+      panel_rsrc(p.a.vs + ((ph * (D / 32)) << shift) + pos, on ? ((D / 32 - 1) << shift) + 16 : 0);
 #pragma unroll
-  for (int r = 0; r < 8; r++) load_bytes<T::kLaneV>(base + r * T::kRow, t.v[r]);
-  const unsigned blk = i * (D / 16) / 32;
-  t.vs = *(const u32x2*)(vs + (blk << shift) + row);
+  for (int r = 0; r < 4; r++) load_bytes<T::kLaneV>(rq, 4 * g * T::kRow + i * T::kLaneV + r * T::kRow, t.v[4 * h + r]);
+  const int blk = i * (D / 16) / 32;
+  t.vs[h] = __builtin_amdgcn_raw_buffer_load_b32(rs, (blk << shift) + 4 * g, 0, 0);
 }
 
 __device__ __forceinline__ unsigned perm(unsigned hi, unsigned lo, unsigned sel) {
@@ -202,16 +216,20 @@ __device__ __forceinline__ f32x4 finish(const AttendArgs& a, int64_t hq, float m
   return o / sum;
 }
 
-// Occupancy 2 (blocks a CU): eight waves keep the memory busy, and with at
-// most 256 registers a wave the accumulators stay out of the AGPR file, whose
-// moves would cost 64 instructions a tile.
-template <int D, bool kFp4, int kTerms>
-__global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
+// Waves a SIMD: what range_shift counts on.  With two or more (at most 256
+// registers a wave) the accumulators stay out of the AGPR file, whose moves
+// would cost 64 instructions a tile.
+template <int D, bool kFp4, int kTerms, bool kRanges>
+__global__ __launch_bounds__(64 * (kRanges ? kRangeWaves : unit_waves(D)),
+                             kRanges ? 1 << (range_shift(kFp4 ? D / 2 : D) - 8) : 2) void k_attend(
+    AttendParams p) {
   typedef Tile<D, kFp4> T;
+  constexpr int kWaves = kRanges ? kRangeWaves : unit_waves(D), kThreads = 64 * kWaves;
+  constexpr int kRangeShift = range_shift(T::kRow);
   constexpr int kSteps = D / 32;  // QK products of half a tile
   constexpr int J = D / 16;       // PV products of a tile; elements of V per lane and token
   constexpr int kPad = D + 4;
-  constexpr int kBuf = D == 256 ? 1 : 2;  // tiles a wave has on their way
+  constexpr int kBuf = 1;  // tiles a wave has on their way
   __shared__ float lds_o[kWaves][kHeadTile][kPad];
   __shared__ float lds_m[kWaves][kHeadTile], lds_l[kWaves][kHeadTile];
   __shared__ unsigned lds_sum[kWaves];
@@ -222,10 +240,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
 
   // This block's tiles: [x, end) of the flattened list, starting in unit
   // (b, head, tile group tg), whose first tile is u_first.
-  unsigned x, end, u_first, head, tg;
+  unsigned x, end, u_first, head, tg, per = 0;
   int64_t b;
   Span s;
-  if (!p.ranges) {
+  if constexpr (!kRanges) {
     unsigned id = blockIdx.x;
     tg = id % p.tile_groups;
     id /= p.tile_groups;
@@ -264,13 +282,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
       if (w < wave) before += lds_sum[w];
       sum += lds_sum[w];
     }
-    const unsigned per = range_tiles(sum);
+    sum = __builtin_amdgcn_readfirstlane(sum);
+    per = range_tiles(sum, kRangeShift);
     x = blockIdx.x * per;
     end = min(x + per, sum);
     unsigned at = before + incl - own;  // first tile of this thread's sequences
-    if (blockIdx.x == 0 || (x >= at && x < at + own)) {
+    if (x >= at && x < at + own) {
       for (unsigned k = b0; k < b1; k++) {
-        if (blockIdx.x == 0) p.first[k] = at;
         s = span_of(p, k);
         const unsigned n = s.t1 - s.t0;
         if (x >= at && x < at + n * units) {
@@ -280,7 +298,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
         at += n * units;
       }
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.first[batch] = sum;
+    // the zeros of empty sequences, each by one block
+    for (unsigned k = blockIdx.x; k < batch; k += gridDim.x) {
+      s = span_of(p, k);
+      if (s.t0 == s.t1)
+        for (unsigned e = threadIdx.x; e < p.a.q_heads * (D / 4); e += kThreads)
+          store_out(p.a, (int64_t)k * p.a.q_heads * D + 4 * e, (f32x4){0, 0, 0, 0});
+      if (s.t0 == s.t1 && !p.by_block)
+        for (unsigned u = threadIdx.x; u < units; u += kThreads) p.parts[4 * (k * units + u)] = 0;
+    }
+    if (p.by_block && threadIdx.x == 0) p.parts[4 * blockIdx.x] = 0;
     if (x >= end) return;
     __syncthreads();
     b = __builtin_amdgcn_readfirstlane(lds_at[0]);
@@ -294,7 +321,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
   const unsigned per_tile = kWaves / p.block_tiles;  // waves per head tile
   const int sub = wave % per_tile;                   // this wave among them
   const unsigned shift = p.c.page_shift, pmask = (1u << shift) - 1;
-  const int ktok = 8 * (i >> 2) + (i & 3);
   // scores are scaled by |scale| (its sign is in q), never by less than what
   // keeps a masked score at -inf
   const float to_log2 = fmaxf(fabsf(p.a.scale) * kLog2e, 0x1p-100f);
@@ -302,6 +328,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
 
   while (true) {
     // tiles [first, last) of the unit
+    s = span_tiles(uniform(s.start), uniform(s.len));
+    x = uniform(x), end = uniform(end), u_first = uniform(u_first), head = uniform(head), tg = uniform(tg);
+    b = uniform((int)b);
     const int first = s.t0 + (int)(x - u_first), last = min(s.t1, s.t0 + (int)(end - u_first));
     const unsigned h0 = tg * p.block_tiles * kHeadTile;  // first query head of the unit
 
@@ -323,169 +352,146 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
 #pragma unroll
     for (int j = 0; j < J; j++) acc[j] = (f32x4){0, 0, 0, 0};
 
-    // This wave's tiles are first + sub + per_tile j.  Lane k keeps the page ids
-    // of tile 64 q + k (two where a tile spans two pages of 16), -1 where the
-    // table names no page of the cache; the ids of the next 64 tiles are
-    // loaded while these are in use.
-    const int32_t* row = p.a.table + b * p.a.table_stride;
-    const bool pair = shift == 4;
-    auto load_ids = [&](int j, int& ia, int& ib) {
-      const int64_t tile = first + sub + (int64_t)per_tile * j;
-      ia = ib = -1;
-      if (live && tile < last) {
-        const int tok = (int)tile * kTile;
-        ia = row[tok >> shift];
-        if (pair && tok + 16 < s.len) ib = row[(tok + 16) >> shift];
-        ia = ia >= 0 && ia < p.c.pages ? ia : -1;
-        ib = ib >= 0 && ib < p.c.pages ? ib : -1;
-      }
-    };
-    int ids_a, ids_b, next_a, next_b;
-    load_ids(lane, ids_a, ids_b);
-    load_ids(64 + lane, next_a, next_b);
+    // This wave's tiles are first + sub + per_tile j, j < count.  The page ids
+    // of the tile to load next are scalars, read from the table one tile
+    // earlier; -1 where the table names no page of the cache.
+    const __attribute__((address_space(4))) int32_t* row =
+        (const __attribute__((address_space(4))) int32_t*)(p.a.table + b * p.a.table_stride);
+    const int count = live && first + sub < last ? (last - first - sub + (int)per_tile - 1) / (int)per_tile : 0;
+    auto token_of = [&](int j) { return (first + sub + (int)per_tile * j) * kTile; };
+    auto id_of = [&](int token) { return uniform(row[(unsigned)min(token, s.len - 1) >> shift]); };
+    auto page_of = [&](int id, int token) { return token < s.len && id >= 0 && id < p.c.pages ? id : -1; };
+    int id0 = id_of(token_of(0)), id1 = id_of(token_of(0) + 16);
     int fetched = 0;  // tiles whose K is on its way
 
     T t[kBuf];
-    int page_a[kBuf], page_b[kBuf];  // of the tile in each buffer
-    // rows of a page; a tile (or half of one) without a page reads page 0 and is masked
-    auto row_of = [&](int page) { return ((int64_t)max(page, 0) * p.c.heads + head) << shift; };
-    auto fetch_k = [&](T& tb, int& pa, int& pb) {
-      if ((fetched & 63) == 0 && fetched > 0) {
-        ids_a = next_a, ids_b = next_b;
-        load_ids(fetched + 64 + lane, next_a, next_b);
-      }
-      pa = __builtin_amdgcn_readlane(ids_a, fetched & 63);
-      const int tok = (first + sub + (int)per_tile * fetched) * kTile;
-      if (!pair) {  // one page a tile: scalar addresses
-        const int64_t r = row_of(pa) + (tok & pmask);
-        load_k<D, kFp4>(p.a.kq + r * T::kRow, p.a.ks + r * (D / 32), ktok, g, tb);
-      } else {
-        pb = __builtin_amdgcn_readlane(ids_b, fetched & 63);
-        const int64_t ra = row_of(pa), rb = row_of(pb), r = ktok < 16 ? ra : rb;
-        load_k<D, kFp4>(p.a.kq + r * T::kRow, p.a.ks + r * (D / 32), ktok & 15, g, tb);
-      }
-      fetched++;
-    };
-    auto fetch_v = [&](int tile, T& tb, int pa, int pb) {
-      if (!pair) {
-        const int64_t r = row_of(pa);
-        const unsigned pos = (tile * kTile) & pmask;
-        load_v<D, kFp4>(p.a.vq + (r + pos) * T::kRow, p.a.vs + r * (D / 32) + pos, 8 * g, shift, i, tb);
-      } else {
-        const int64_t ra = row_of(pa), rb = row_of(pb), r = g < 2 ? ra : rb;
-        load_v<D, kFp4>(p.a.vq + r * T::kRow, p.a.vs + r * (D / 32), 8 * (g & 1), shift, i, tb);
-      }
-    };
+    int page[kBuf][2];  // of the halves of the tile in each buffer
+    auto fetch_k = [&](T& tb, int (&pg)[2]) {
+      const int tok = token_of(fetched);
+      const bool on = fetched < count;
+      pg[0] = on ? page_of(id0, tok) : -1;
+      pg[1] = on ? page_of(id1, tok + 16) : -1;
 #pragma unroll
-    for (int bf = 0; bf < kBuf; bf++) {
-      const int at = first + sub + (int)per_tile * bf;
-      page_a[bf] = page_b[bf] = -1;
-      if (live && at < last) {
-        fetch_k(t[bf], page_a[bf], page_b[bf]);
-        fetch_v(at, t[bf], page_a[bf], page_b[bf]);
-      }
-    }
-    for (int at0 = first + sub; live && at0 < last; at0 += kBuf * per_tile) {
+      for (int h = 0; h < 2; h++)
+        load_k<D, kFp4>(p, (((int64_t)max(pg[h], 0) * p.c.heads + head) << shift) + ((tok + 16 * h) & pmask), pg[h] >= 0,
+                        h, i, g, tb);
+      fetched++;
+      const int next = token_of(min(fetched, count - 1));
+      id0 = id_of(next);
+      id1 = id_of(next + 16);
+    };
+    auto fetch_v = [&](int j, T& tb, const int (&pg)[2]) {
+      const int tok = token_of(j);
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        load_v<D, kFp4>(p, (int64_t)max(pg[h], 0) * p.c.heads + head, (tok + 16 * h) & pmask, pg[h] >= 0, h, i, g, tb);
+    };
+    if (count > 0) {
 #pragma unroll
       for (int bf = 0; bf < kBuf; bf++) {
-        const int at = at0 + bf * (int)per_tile;
-        if (at >= last) break;
+        fetch_k(t[bf], page[bf]);
+        fetch_v(bf, t[bf], page[bf]);
+      }
+    }
+    for (int j0 = 0; j0 < count; j0 += kBuf) {
+#pragma unroll
+      for (int bf = 0; bf < kBuf; bf++) {
+        const int j = j0 + bf;
+        const bool here = bf == 0 || j < count;  // loads below are unconditional (see load_k)
         T& tb = t[bf];
-        const int next = at + kBuf * (int)per_tile;
-        const int t0 = at * kTile;
-        const int vpage = pair && g >= 2 ? page_b[bf] : page_a[bf];  // of tokens 8 g .. 8 g + 7
+        const int t0 = token_of(j);
+        const int pg0 = page[bf][0], pg1 = page[bf][1];
         // S^T
         f32x4 sc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        if (here) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          float scale[T::kRuns];
+          for (int st = 0; st < kSteps; st++)
 #pragma unroll
-          for (int r = 0; r < T::kRuns; r++) scale[r] = e8m0_as_scale(tb.ks[h][r]);
+            for (int h = 0; h < 2; h++) {
+              const float scale = e8m0_as_scale(tb.ks[h][D == 64 ? 0 : st / 4]);
+              u32x4 a;
 #pragma unroll
-          for (int st = 0; st < kSteps; st++) {
-            u32x4 a;
-#pragma unroll
-            for (int e = 0; e < 4; e++) a[e] = decode2<kFp4>(tb.k[h], 4 * st + e, scale[D == 64 ? 0 : st / 4]);
-            sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), qf[st], sc[h], 0, 0, 0);
-          }
+              for (int e = 0; e < 4; e++) a[e] = decode2<kFp4>(tb.k[h], 4 * st + e, scale);
+              sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), qf[st], sc[h], 0, 0, 0);
+            }
         }
-        if (next < last) fetch_k(tb, page_a[bf], page_b[bf]);
-        // softmax over the tile; this lane: head i, tokens t0 + 8 g ..+7
-        const int v0 = t0 + 8 * g;
-        float y[8];
+        fetch_k(tb, page[bf]);
+        if (here) {
+          // softmax over the tile; y[4 h + r]: head i, token t0 + 16 h + 4 g + r
+          float y[8];
 #pragma unroll
-        for (int r = 0; r < 8; r++) y[r] = sc[r >> 2][r & 3];
-        const bool whole = t0 >= s.start && t0 + kTile <= s.len && __builtin_amdgcn_ballot_w64(vpage < 0) == 0;
-        if (!whole) {
-          // a masked token's K and V bytes are whatever the page holds: its
-          // score is replaced, and its codes and scale are cleared, so nothing
-          // of it (NaN codes among it) reaches a product with a non-zero factor
+          for (int r = 0; r < 8; r++) y[r] = sc[r >> 2][r & 3];
+          const bool whole = t0 >= s.start && t0 + kTile <= s.len && pg0 >= 0 && pg1 >= 0;
+          if (!whole) {
+            // a masked token's K and V bytes are whatever the page holds: its
+            // score is replaced, and its codes and scale are cleared, so nothing
+            // of it (NaN codes among it) reaches a product with a non-zero factor
 #pragma unroll
-          for (int r = 0; r < 8; r++) {
-            const bool seen = vpage >= 0 && v0 + r >= s.start && v0 + r < s.len;
-            y[r] = seen ? y[r] : -INFINITY;
+            for (int r = 0; r < 8; r++) {
+              const int tok = t0 + 16 * (r >> 2) + 4 * g + (r & 3);
+              const bool seen = (r < 4 ? pg0 : pg1) >= 0 && tok >= s.start && tok < s.len;
+              y[r] = seen ? y[r] : -INFINITY;
 #pragma unroll
-            for (int w = 0; w < (int)(sizeof(tb.v[r]) / 4); w++) tb.v[r][w] = seen ? tb.v[r][w] : 0u;
-            const unsigned byte = 0xFFu << (8 * (r & 3));
-            if (r < 4) tb.vs.x = seen ? tb.vs.x : tb.vs.x & ~byte;
-            else tb.vs.y = seen ? tb.vs.y : tb.vs.y & ~byte;
-          }
-        }
-        float top = y[0];
-#pragma unroll
-        for (int r = 1; r < 8; r++) top = fmaxf(top, y[r]);
-        top = fmaxf(m, max_groups(top));
-        const float ref = top > -INFINITY ? top * to_log2 : 0.0f;  // nothing seen yet: every p is 0
-        if (__builtin_amdgcn_ballot_w64(top > m) != 0) {
-          const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf(m, to_log2, -ref));
-          l *= alpha;
-#pragma unroll
-          for (int j = 0; j < J; j++) acc[j] *= alpha;
-          m = top;
-        }
-        // P in bf16 terms: each takes the upper half of what the ones before
-        // it left (truncated; the last one rounded)
-        u32x4 pt[kTerms];
-#pragma unroll
-        for (int r = 0; r < 8; r += 2) {
-          float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r], to_log2, -ref));
-          float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r + 1], to_log2, -ref));
-          l += p0 + p1;
-#pragma unroll
-          for (int k = 0; k < kTerms; k++) {
-            if (k + 1 == kTerms) {
-              pt[k][r >> 1] = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)p0, (__bf16)p1});
-            } else {
-              const unsigned w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-              pt[k][r >> 1] = perm(w1, w0, 0x07060302u);
-              p0 -= __uint_as_float(w0 & 0xFFFF0000u);  // exact
-              p1 -= __uint_as_float(w1 & 0xFFFF0000u);
+              for (int w = 0; w < (int)(sizeof(tb.v[r]) / 4); w++) tb.v[r][w] = seen ? tb.v[r][w] : 0u;
+              tb.vs[r >> 2] = seen ? tb.vs[r >> 2] : tb.vs[r >> 2] & ~(0xFFu << (8 * (r & 3)));
             }
           }
-        }
-        // O^T
-        float vscale[8];
+          float top = y[0];
 #pragma unroll
-        for (int r = 0; r < 8; r++)
-          vscale[r] = e8m0_as_scale((r < 4 ? tb.vs.x >> (8 * r) : tb.vs.y >> (8 * (r - 4))) & 0xFFu);
+          for (int r = 1; r < 8; r++) top = fmaxf(top, y[r]);
+          top = fmaxf(m, max_groups(top));
+          const float ref = top > -INFINITY ? top * to_log2 : 0.0f;  // nothing seen yet: every p is 0
+          if (__builtin_amdgcn_ballot_w64(top > m) != 0) {
+            const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf(m, to_log2, -ref));
+            l *= alpha;
 #pragma unroll
-        for (int j2 = 0; j2 < J / 2; j2++) {
-          unsigned d[8];
+            for (int j = 0; j < J; j++) acc[j] *= alpha;
+            m = top;
+          }
+          // P in bf16 terms: each takes the upper half of what the ones before
+          // it left (truncated; the last one rounded)
+          u32x4 pt[kTerms];
 #pragma unroll
-          for (int r = 0; r < 8; r++) d[r] = decode2<kFp4>(tb.v[r], j2, vscale[r]);
+          for (int r = 0; r < 8; r += 2) {
+            float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r], to_log2, -ref));
+            float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r + 1], to_log2, -ref));
+            l += p0 + p1;
 #pragma unroll
-          for (int o = 0; o < 2; o++) {
-            u32x4 a;
+            for (int k = 0; k < kTerms; k++) {
+              if (k + 1 == kTerms) {
+                pt[k][r >> 1] = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)p0, (__bf16)p1});
+              } else {
+                const unsigned w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+                pt[k][r >> 1] = perm(w1, w0, 0x07060302u);
+                p0 -= __uint_as_float(w0 & 0xFFFF0000u);  // exact
+                p1 -= __uint_as_float(w1 & 0xFFFF0000u);
+              }
+            }
+          }
+          // O^T
+          float vscale[8];
 #pragma unroll
-            for (int r = 0; r < 4; r++) a[r] = perm(d[2 * r + 1], d[2 * r], o ? 0x07060302u : 0x05040100u);
-            const bf16x8 va = __builtin_bit_cast(bf16x8, a);
+          for (int r = 0; r < 8; r++) vscale[r] = e8m0_as_scale((tb.vs[r >> 2] >> (8 * (r & 3))) & 0xFFu);
+#pragma unroll
+          for (int j2 = 0; j2 < J / 2; j2++) {
+            unsigned d[8];
+#pragma unroll
+            for (int r = 0; r < 8; r++) d[r] = decode2<kFp4>(tb.v[r], j2, vscale[r]);
+            u32x4 va[2];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+              va[0][r] = perm(d[2 * r + 1], d[2 * r], 0x05040100u);
+              va[1][r] = perm(d[2 * r + 1], d[2 * r], 0x07060302u);
+            }
 #pragma unroll
             for (int k = 0; k < kTerms; k++)
-              acc[2 * j2 + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, __builtin_bit_cast(bf16x8, pt[k]),
-                                                                        acc[2 * j2 + o], 0, 0, 0);
+#pragma unroll
+              for (int o = 0; o < 2; o++)
+                acc[2 * j2 + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, va[o]), __builtin_bit_cast(bf16x8, pt[k]), acc[2 * j2 + o], 0, 0, 0);
           }
         }
-        if (next < last) fetch_v(next, tb, page_a[bf], page_b[bf]);
+        fetch_v(j + kBuf, tb, page[bf]);
       }
     }
 
@@ -507,6 +513,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
     // out: threads over (head tile, head, 4 elements)
     constexpr int kQuads = D / 4;
     const bool opens = first == s.t0, closes = last == s.t1;  // of the unit
+    if (kRanges && opens && threadIdx.x == 0 && !(p.by_block && closes)) {
+      const unsigned unit = ((unsigned)b * p.c.heads + head) * p.tile_groups + tg;
+      int* w = p.parts + 4 * (p.by_block ? blockIdx.x : unit);
+      w[0] = (int)((u_first + (unsigned)(s.t1 - s.t0) - 1) / per - blockIdx.x) + 1;
+      w[1] = (int)blockIdx.x, w[2] = (int)unit;
+    }
     for (unsigned e = threadIdx.x; e < p.block_tiles * kHeadTile * kQuads; e += kThreads) {
       const unsigned hh = e / kQuads, d4 = e % kQuads;  // head of the unit
       if (h0 + hh >= p.group) continue;
@@ -520,7 +532,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
         sum += mw > -INFINITY ? lds_l[wb + w][hh % kHeadTile] * __builtin_amdgcn_exp2f(mw - mx) : 0.0f;
         o += *(const f32x4*)&lds_o[wb + w][hh % kHeadTile][4 * d4];
       }
-      if (opens && closes) {
+      if (!kRanges || (opens && closes)) {
         const int64_t hq = (int64_t)head * p.group + h0 + hh;
         store_out(p.a, (b * p.a.q_heads + hq) * D + 4 * d4, finish(p.a, hq, mx, sum, o));
       } else {
@@ -535,6 +547,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
       }
     }
     // the next unit: the next tile group, cache head or sequence with tiles
+    if constexpr (!kRanges) break;
     x = u_first + (last - s.t0);
     if (x >= end) break;
     u_first = x;
@@ -550,58 +563,75 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendParams p) {
   }
 }
 
-// Adds the parts of one sequence and query head.  A unit's parts lie with
-// consecutive blocks; each of the 256 / (D / 4) rows of threads adds every
-// kRows-th of them in order, then the rows are added in order.
-template <int D>
+// Adds the parts of the unit of record blockIdx.x: slot 1 of the block that
+// opened it, then slot 0 of the blocks after it.  A block takes kHeads heads
+// (grid y), with kRows rows of D / 4 threads each; a row adds every kRows-th
+// part in order, then the rows are added in order.
+template <int D, int kHeads>
 __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
-  constexpr int kQuads = D / 4, kRows = 256 / kQuads;
-  __shared__ f32x4 lo[kRows][kQuads];
-  __shared__ float ll[kRows], lm[4];
-  const int64_t bh = blockIdx.x;
-  const int64_t b = bh / p.a.q_heads;
-  const unsigned hq = (unsigned)(bh % p.a.q_heads), head = hq / p.group, gh = hq % p.group;
-  const unsigned unit_heads = p.block_tiles * kHeadTile, units = p.c.heads * p.tile_groups;
-  const int d4 = threadIdx.x % kQuads, row = threadIdx.x / kQuads;
-  const unsigned begin = p.first[b], n = (p.first[b + 1] - begin) / units;
-  if (n == 0) {  // an empty sequence
-    if (row == 0) store_out(p.a, bh * D + 4 * d4, (f32x4){0, 0, 0, 0});
-    return;
-  }
-  const unsigned per = range_tiles(p.first[p.a.batch]);
-  const unsigned u_first = begin + (head * p.tile_groups + gh / unit_heads) * n;
-  const unsigned k0 = u_first / per, k1 = (u_first + n - 1) / per;
-  if (k0 == k1) return;  // one block had it all and wrote it
-  const unsigned hh = gh % unit_heads;
-  // part k of the unit: the block that opened it, then the ones after it
-  auto slot = [&](unsigned k) { return (int64_t)(2 * k + (k == k0 ? 1 : 0)) * unit_heads + hh; };
-  float top = -INFINITY;
-  for (unsigned k = k0 + threadIdx.x; k <= k1; k += 256) top = fmaxf(top, p.part_ml[2 * slot(k)]);
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
-  if ((threadIdx.x & 63) == 0) lm[threadIdx.x >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(lm[0], lm[1]), fmaxf(lm[2], lm[3]));
+  constexpr int kQuads = D / 4, kRows = 256 / kQuads / kHeads;
+  __shared__ f32x4 lo[256 / kQuads][kQuads];
+  __shared__ float ll[256 / kQuads], lm[256 / kQuads];
+  const int* w = p.parts + 4 * blockIdx.x;
+  const int parts = w[0];
+  if (parts < 2) return;
+  const unsigned k0 = w[1], unit = w[2];
+  const unsigned unit_heads = p.block_tiles * kHeadTile;
+  const unsigned h0 = unit % p.tile_groups * unit_heads, head = unit / p.tile_groups % p.c.heads;
+  const int64_t b = unit / (p.tile_groups * p.c.heads);
+  const int d4 = threadIdx.x % kQuads, line = threadIdx.x / kQuads, row = line % kRows;
+  const unsigned hh = blockIdx.y * kHeads + line / kRows;
+  const bool live = hh < unit_heads && h0 + hh < p.group;
+  auto slot = [&](int part) { return (int64_t)(2 * (k0 + part) + (part == 0 ? 1 : 0)) * unit_heads + hh; };
+  float top = -INFINITY, sum = 0;
   f32x4 o = {0, 0, 0, 0};
-  float sum = 0;
-#pragma unroll 4
-  for (unsigned k = k0 + row; k <= k1; k += kRows) {
-    const int64_t sl = slot(k);
-    const float mw = p.part_ml[2 * sl];
-    const float f = mw > -INFINITY ? __builtin_amdgcn_exp2f(mw - top) : 0.0f;
-    sum += f * p.part_ml[2 * sl + 1];
-    o += *(const f32x4*)(p.part_o + sl * D + 4 * d4) * f;
-  }
-  lo[row][d4] = o;
-  if (d4 == 0) ll[row] = sum;
-  __syncthreads();
-  if (row != 0) return;
+  if (live) {
+    // a row's parts four at a time, all loads first
+    constexpr int kN = 4;
+    for (int k = row; k < parts; k += kN * kRows) {
+      f32x2 ml[kN];
+      f32x4 po[kN];
 #pragma unroll
-  for (int r = 1; r < kRows; r++) {
-    o += lo[r][d4];
-    sum += ll[r];
+      for (int c = 0; c < kN; c++) {
+        const int64_t sl = slot(min(k + c * kRows, parts - 1));
+        ml[c] = *(const f32x2*)(p.part_ml + 2 * sl);
+        po[c] = *(const f32x4*)(p.part_o + sl * D + 4 * d4);
+      }
+      float m = top;
+#pragma unroll
+      for (int c = 0; c < kN; c++) m = fmaxf(m, ml[c].x);
+      const float ref = m > -INFINITY ? m : 0.0f, f0 = __builtin_amdgcn_exp2f(top - ref);
+      sum *= f0;
+      o *= f0;
+      top = m;
+#pragma unroll
+      for (int c = 0; c < kN; c++) {
+        const float f = k + c * kRows < parts ? __builtin_amdgcn_exp2f(ml[c].x - ref) : 0.0f;
+        sum += f * ml[c].y;
+        o += po[c] * f;
+      }
+    }
   }
-  store_out(p.a, bh * D + 4 * d4, finish(p.a, hq, top, sum, o));
+  if constexpr (kRows > 1) {
+    lo[line][d4] = o;
+    if (d4 == 0) ll[line] = sum, lm[line] = top;
+    __syncthreads();
+    if (row != 0) return;
+#pragma unroll
+    for (int r = 1; r < kRows; r++) top = fmaxf(top, lm[line + r]);
+    const float ref = top > -INFINITY ? top : 0.0f;
+    o = (f32x4){0, 0, 0, 0};
+    sum = 0;
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+      const float f = __builtin_amdgcn_exp2f(lm[line + r] - ref);
+      o += lo[line + r][d4] * f;
+      sum += ll[line + r] * f;
+    }
+  }
+  if (!live) return;
+  const int64_t hq = (int64_t)head * p.group + h0 + hh;
+  store_out(p.a, (b * p.a.q_heads + hq) * D + 4 * d4, finish(p.a, hq, top, sum, o));
 }
 
 constexpr int kUnitTiles = 16;  // see attend_ranges
@@ -610,7 +640,7 @@ constexpr int kUnitTiles = 16;  // see attend_ranges
 
 // Head tiles of 16 per cache head; a unit takes up to four.
 static int64_t head_tiles(unsigned q_heads, const KvShape& c) { return (q_heads / c.heads + kHeadTile - 1) / kHeadTile; }
-static int64_t tile_groups(unsigned q_heads, const KvShape& c) { return (head_tiles(q_heads, c) + kWaves - 1) / kWaves; }
+static int64_t tile_groups(unsigned q_heads, const KvShape& c) { return (head_tiles(q_heads, c) + kMaxUnitTiles16 - 1) / kMaxUnitTiles16; }
 static int64_t unit_tiles16(unsigned q_heads, const KvShape& c) {
   const int64_t t = head_tiles(q_heads, c);
   return t >= 3 ? 4 : t;
@@ -623,26 +653,38 @@ static int64_t most_tiles(const KvShape& c, int64_t table_width, int64_t window)
   return (most + kTile - 1) / kTile;
 }
 
-// Whether blocks take ranges of the flattened tiles; a block takes a unit
-// where none is longer than a few tiles, or all are short and there are enough
-// of them to fill the chip.
-static bool attend_ranges(int64_t units, int64_t tiles) {
-  return !(tiles <= kWaves || (tiles <= kUnitTiles && units >= 128));
-}
+// Whether blocks take ranges of the flattened tiles.  A unit of at most 16
+// tiles (two for each of its eight waves) is one block's.  64 query heads over
+// 8, D = 128, MXFP8, ranges / units: one sequence of 500 tokens 10.4 / 9.4 us,
+// 16 of 500 14.1 / 10.0, 64 of 300-500 25.6 / 19.3; at 1000 tokens (32
+// tiles) ranges win: 10.3 / 14.2.
+static bool attend_ranges(int64_t tiles) { return tiles > kUnitTiles; }
 
-int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window) {
+int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp4, int64_t table_width, int64_t window) {
   const int64_t units = batch * c.heads * tile_groups(q_heads, c), tiles = most_tiles(c, table_width, window);
   // flattened tile indexes are 32 bits, with room for one range more
   if (units > (0x7FFFFFFF - 4096) / tiles) return -1;
-  if (!attend_ranges(units, tiles)) return units;
-  return std::min<int64_t>(1 << kRangeShift, units * ((tiles + kWaves - 1) / kWaves));
+  if (!attend_ranges(tiles)) return units;
+  return std::min<int64_t>(1 << range_shift(fp4 ? c.dim / 2 : c.dim), units * ((tiles + kRangeWaves - 1) / kRangeWaves));
 }
 
 int64_t attend_workspace(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window) {
-  if (!attend_ranges(batch * c.heads * tile_groups(q_heads, c), most_tiles(c, table_width, window))) return 0;
-  const int64_t blocks = attend_blocks(batch, q_heads, c, table_width, window);
-  const int64_t first = ((batch + 1) * 4 + 15) / 16 * 16;
-  return first + 2 * blocks * unit_tiles16(q_heads, c) * kHeadTile * (int64_t)(c.dim + 2) * 4;
+  if (!attend_ranges(most_tiles(c, table_width, window))) return 0;
+  // for either format: the smaller rows take no fewer blocks (nor records)
+  const int64_t blocks = attend_blocks(batch, q_heads, c, true, table_width, window);
+  return blocks * (16 + 2 * unit_tiles16(q_heads, c) * kHeadTile * (int64_t)(c.dim + 2) * 4);
+}
+
+// With a range for each unit or so (by_block), a unit has two or three parts,
+// which one row of threads adds; with fewer units they have many, and the rows
+// of a block share them.
+template <int D>
+static void launch_join(const AttendParams& p, unsigned heads, int64_t records, hipStream_t st) {
+  constexpr int kLines = 256 / (D / 4), kFew = kLines > 8 ? kLines / 8 : 1;
+  if (p.by_block)
+    k_attend_join<D, kLines><<<dim3((unsigned)records, (heads + kLines - 1) / kLines), dim3(256), 0, st>>>(p);
+  else
+    k_attend_join<D, kFew><<<dim3((unsigned)records, (heads + kFew - 1) / kFew), dim3(256), 0, st>>>(p);
 }
 
 hipError_t launch_attend(const AttendArgs& a, const KvShape& c, bool fp4, void* workspace, hipStream_t st) {
@@ -653,24 +695,30 @@ hipError_t launch_attend(const AttendArgs& a, const KvShape& c, bool fp4, void* 
   p.tiles16 = (unsigned)head_tiles(a.q_heads, c);
   p.tile_groups = (unsigned)tile_groups(a.q_heads, c);
   p.block_tiles = (unsigned)unit_tiles16(a.q_heads, c);
-  const int64_t blocks = attend_blocks(a.batch, a.q_heads, c, a.table_width, a.window);
-  p.ranges = attend_ranges(a.batch * c.heads * p.tile_groups, most_tiles(c, a.table_width, a.window));
-  p.first = (unsigned*)workspace;
-  p.part_o = (float*)((uint8_t*)workspace + ((a.batch + 1) * 4 + 15) / 16 * 16);
+  const int64_t blocks = attend_blocks(a.batch, a.q_heads, c, fp4, a.table_width, a.window);
+  const int64_t units = a.batch * c.heads * p.tile_groups;
+  const bool ranges = attend_ranges(most_tiles(c, a.table_width, a.window));
+  p.by_block = units >= blocks / 2;
+  p.parts = (int*)workspace;  // at most a record a block, in either case
+  p.part_o = (float*)((uint8_t*)workspace + blocks * 16);
   p.part_ml = p.part_o + 2 * blocks * p.block_tiles * kHeadTile * c.dim;
-  const dim3 grid((unsigned)blocks), block(kThreads);
-#define MXQ_ATTEND_T(D, T) fp4 ? k_attend<D, true, T><<<grid, block, 0, st>>>(p) : k_attend<D, false, T><<<grid, block, 0, st>>>(p)
-#define MXQ_ATTEND(D)                                                                                  \
-  do {                                                                                                 \
-    if (a.bf16_out) MXQ_ATTEND_T(D, 2);                                                                \
-    else MXQ_ATTEND_T(D, 3);                                                                           \
-    if (p.ranges) k_attend_join<D><<<dim3((unsigned)(a.batch * a.q_heads)), dim3(256), 0, st>>>(p);    \
+  const dim3 grid((unsigned)blocks), block(64 * (ranges ? kRangeWaves : unit_waves(c.dim)));
+  const unsigned heads = std::min(p.group, p.block_tiles * kHeadTile);
+#define MXQ_ATTEND_R(D, F, T) \
+  ranges ? k_attend<D, F, T, true><<<grid, block, 0, st>>>(p) : k_attend<D, F, T, false><<<grid, block, 0, st>>>(p)
+#define MXQ_ATTEND(D)                                                                              \
+  do {                                                                                             \
+    if (a.bf16_out && fp4) MXQ_ATTEND_R(D, true, 2);                                               \
+    else if (a.bf16_out) MXQ_ATTEND_R(D, false, 2);                                                \
+    else if (fp4) MXQ_ATTEND_R(D, true, 3);                                                        \
+    else MXQ_ATTEND_R(D, false, 3);                                                                \
+    if (ranges) launch_join<D>(p, heads, p.by_block ? blocks : units, st);                         \
   } while (0)
   if (c.dim == 64) MXQ_ATTEND(64);
   else if (c.dim == 128) MXQ_ATTEND(128);
   else MXQ_ATTEND(256);
 #undef MXQ_ATTEND
-#undef MXQ_ATTEND_T
+#undef MXQ_ATTEND_R
   return hipGetLastError();
 }
 

@@ -336,7 +336,7 @@ static bool attend_sizes(int64_t batch, int64_t q_heads, const mxq::KvShape& c, 
   if (table_width < 1 || table_width > 0x7FFFFFFF || window < 0) return false;
   // blocks of 256 threads of both launches: below 2^32 threads
   if (q_heads > (1 << 20) || batch > (1 << 24) / q_heads) return false;
-  const int64_t blocks = mxq::attend_blocks(batch, (unsigned)q_heads, c, table_width, window);
+  const int64_t blocks = mxq::attend_blocks(batch, (unsigned)q_heads, c, true, table_width, window);
   return blocks > 0 && blocks < (1 << 24);
 }
 

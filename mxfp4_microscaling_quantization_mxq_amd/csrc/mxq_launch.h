@@ -47,7 +47,7 @@ struct AttendArgs {
 // Blocks of such a call (-1 where its tiles of 32 tokens, over all sequences
 // at the table's width and all cache heads, pass 2^31), and the bytes of
 // workspace that its partial results take.
-int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window);
+int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp4, int64_t table_width, int64_t window);
 int64_t attend_workspace(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window);
 hipError_t launch_attend(const AttendArgs& a, const KvShape& c, bool fp4, void* workspace, hipStream_t st);
 
