@@ -35,8 +35,8 @@
 // are cut into equal ranges, one a block of 4 waves, so a batch of uneven
 // lengths keeps every CU busy to the end.  A range that ends inside a unit
 // leaves partial results (m, sum, O) in the workspace, and k_attend_join adds
-// a unit's parts in order.  Where all sequences are short, a block of 8 waves
-// takes one unit and nothing is joined.
+// a unit's parts in order.  Where all sequences are short, a block takes
+// one unit and nothing is joined.
 #include "mxq_gemm_common.h"
 #include "mxq_kv.h"
 #include "mxq_launch.h"
@@ -48,10 +48,8 @@ namespace {
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;       // tokens a wave takes at a time
-constexpr int kRangeWaves = 4;  // waves of a block that takes a range
-// Waves of a block that takes one unit: the partial O of eight waves of 256
-// elements a head would not leave LDS for a second block.
-constexpr int unit_waves(int d) { return d == 256 ? 4 : 8; }
+constexpr int kWaves = 4;       // waves of a block
+constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxUnitTiles16 = 4;  // head tiles of a unit: one to four waves share the range's cache head
 constexpr int kHeadTile = 16;   // query heads of one MFMA column set
 constexpr int64_t kMaxLen = 0x7FFF0000;  // tokens of a sequence (token indexes, also a few tiles past it, are 32 bits)
@@ -99,7 +97,7 @@ constexpr int range_shift(int row_bytes) { return row_bytes >= 128 ? 9 : 10; }
 // Tiles of a range: an equal share of 2^shift blocks, and enough to give every
 // wave one.
 __device__ __forceinline__ unsigned range_tiles(unsigned sum, int shift) {
-  return max((sum >> shift) + ((sum & ((1u << shift) - 1)) != 0), (unsigned)kRangeWaves);
+  return max((sum >> shift) + ((sum & ((1u << shift) - 1)) != 0), (unsigned)kWaves);
 }
 
 template <int D, bool kFp4>
@@ -220,11 +218,8 @@ __device__ __forceinline__ f32x4 finish(const AttendArgs& a, int64_t hq, float m
 // registers a wave) the accumulators stay out of the AGPR file, whose moves
 // would cost 64 instructions a tile.
 template <int D, bool kFp4, int kTerms, bool kRanges>
-__global__ __launch_bounds__(64 * (kRanges ? kRangeWaves : unit_waves(D)),
-                             kRanges ? 1 << (range_shift(kFp4 ? D / 2 : D) - 8) : 2) void k_attend(
-    AttendParams p) {
+__global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8)) void k_attend(AttendParams p) {
   typedef Tile<D, kFp4> T;
-  constexpr int kWaves = kRanges ? kRangeWaves : unit_waves(D), kThreads = 64 * kWaves;
   constexpr int kRangeShift = range_shift(T::kRow);
   constexpr int kSteps = D / 32;  // QK products of half a tile
   constexpr int J = D / 16;       // PV products of a tile; elements of V per lane and token
@@ -634,7 +629,6 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
   store_out(p.a, (b * p.a.q_heads + hq) * D + 4 * d4, finish(p.a, hq, top, sum, o));
 }
 
-constexpr int kUnitTiles = 16;  // see attend_ranges
 
 }  // namespace
 
@@ -653,23 +647,28 @@ static int64_t most_tiles(const KvShape& c, int64_t table_width, int64_t window)
   return (most + kTile - 1) / kTile;
 }
 
-// Whether blocks take ranges of the flattened tiles.  A unit of at most 16
-// tiles (two for each of its eight waves) is one block's.  64 query heads over
-// 8, D = 128, MXFP8, ranges / units: one sequence of 500 tokens 10.4 / 9.4 us,
-// 16 of 500 14.1 / 10.0, 64 of 300-500 25.6 / 19.3; at 1000 tokens (32
-// tiles) ranges win: 10.3 / 14.2.
-static bool attend_ranges(int64_t tiles) { return tiles > kUnitTiles; }
+// Whether blocks take ranges of the flattened tiles: where a unit would keep
+// one block longer than the join of its parts takes.  A block needs about
+// 0.9 us for 4 tiles, and the more units there are, the longer the others take
+// anyway.  64 query heads over 8, D = 128, MXFP8, ranges / units: 1 sequence of
+// 500 tokens (16 tiles, 8 units) 10.4 / 8.2 us, of 1000 10.4 / 12.4; 8 of
+// 700-1000 (32 tiles, 64 units) 16.5 / 12.5; 16 of 1500-2000 (63 tiles, 128
+// units) 24.0 / 22.2, 64 53.9 / 46.4; 16 of 1000-4000 28.1 / 36.2, 64 73.4 / 75.1.
+// (Eight waves a unit measured slower: 64 of 300-500 19.1 against 15.1.)
+static bool attend_ranges(int64_t units, int64_t tiles) {
+  return tiles > (units >= 128 ? 64 : units >= 32 ? 32 : 16);
+}
 
 int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp4, int64_t table_width, int64_t window) {
   const int64_t units = batch * c.heads * tile_groups(q_heads, c), tiles = most_tiles(c, table_width, window);
   // flattened tile indexes are 32 bits, with room for one range more
   if (units > (0x7FFFFFFF - 4096) / tiles) return -1;
-  if (!attend_ranges(tiles)) return units;
-  return std::min<int64_t>(1 << range_shift(fp4 ? c.dim / 2 : c.dim), units * ((tiles + kRangeWaves - 1) / kRangeWaves));
+  if (!attend_ranges(units, tiles)) return units;
+  return std::min<int64_t>(1 << range_shift(fp4 ? c.dim / 2 : c.dim), units * ((tiles + kWaves - 1) / kWaves));
 }
 
 int64_t attend_workspace(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window) {
-  if (!attend_ranges(most_tiles(c, table_width, window))) return 0;
+  if (!attend_ranges(batch * c.heads * tile_groups(q_heads, c), most_tiles(c, table_width, window))) return 0;
   // for either format: the smaller rows take no fewer blocks (nor records)
   const int64_t blocks = attend_blocks(batch, q_heads, c, true, table_width, window);
   return blocks * (16 + 2 * unit_tiles16(q_heads, c) * kHeadTile * (int64_t)(c.dim + 2) * 4);
@@ -697,12 +696,12 @@ hipError_t launch_attend(const AttendArgs& a, const KvShape& c, bool fp4, void* 
   p.block_tiles = (unsigned)unit_tiles16(a.q_heads, c);
   const int64_t blocks = attend_blocks(a.batch, a.q_heads, c, fp4, a.table_width, a.window);
   const int64_t units = a.batch * c.heads * p.tile_groups;
-  const bool ranges = attend_ranges(most_tiles(c, a.table_width, a.window));
+  const bool ranges = attend_ranges(units, most_tiles(c, a.table_width, a.window));
   p.by_block = units >= blocks / 2;
   p.parts = (int*)workspace;  // at most a record a block, in either case
   p.part_o = (float*)((uint8_t*)workspace + blocks * 16);
   p.part_ml = p.part_o + 2 * blocks * p.block_tiles * kHeadTile * c.dim;
-  const dim3 grid((unsigned)blocks), block(64 * (ranges ? kRangeWaves : unit_waves(c.dim)));
+  const dim3 grid((unsigned)blocks), block(kThreads);
   const unsigned heads = std::min(p.group, p.block_tiles * kHeadTile);
 #define MXQ_ATTEND_R(D, F, T) \
   ranges ? k_attend<D, F, T, true><<<grid, block, 0, st>>>(p) : k_attend<D, F, T, false><<<grid, block, 0, st>>>(p)
