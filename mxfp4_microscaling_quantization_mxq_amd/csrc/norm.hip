@@ -2,14 +2,19 @@
 // one pass over the row (gfx950).
 //
 //   r = rnd(x + residual)                      (rnd: to the type of x; r = x without a residual)
-//   y_i = r_i * (1 / sqrt(mean_j r_j^2 + eps)) * w_i      (fp32, in this order)
+//   y_i = r_i * w_i / sqrt(mean_j r_j^2 + eps)
 //   (q, s) = MXFP8(y): blocks of 32, code max(expfield(amax) - 8, 0), E4M3 nearest even
 //
 // The norm is taken of the rounded r, the value that is stored and that the
 // next layer adds to, so fused and unfused programs see the same stream.
-// The sum of squares is held in fp32; mean, sum and square root of the row's
-// one scale are in fp64 and rounded once, so every y_i carries two fp32
-// roundings.
+//
+// Roundings.  Squares are summed in fp32 over a lane's 8 elements and in fp64
+// from there on; the row's factor is fp64.  y is formed in fp32 (within 2 ulp
+// of its value), which decides its E4M3 code unless it lies that close to the
+// midpoint of two codes; then, and where a lane's largest |y| is that close to
+// a power of two (the block scale), the lane's y are formed again in fp64 and
+// rounded to odd, so that one rounding to the code remains.  (About 1 chunk of
+// 64 lanes in 200 has such a lane.)
 //
 // Memory bound: x and residual are read once, r, q and s written once (7.03
 // bytes an element in bf16); the row stays in registers between the sum and
@@ -21,53 +26,91 @@ namespace mxq {
 
 namespace {
 
-// 8 consecutive elements (lane c of the row) as fp32.
+// 8 consecutive elements as loaded, and as fp32.
 template <bool kBf16>
-__device__ __forceinline__ void load8_f32(const void* p, int64_t c, float (&v)[8]) {
-  if constexpr (kBf16) {
-    const u32x4 w = ((const u32x4*)p)[c];
-    const unsigned ww[4] = {w.x, w.y, w.z, w.w};
+struct Raw8 {
+  u32x4 w[kBf16 ? 1 : 2];
+};
+template <bool kBf16>
+__device__ __forceinline__ Raw8<kBf16> load_raw(const void* p, int64_t c) {
+  constexpr int kN = kBf16 ? 1 : 2;
+  Raw8<kBf16> r;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      v[2 * i] = __uint_as_float(ww[i] << 16);
-      v[2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
-    }
-  } else {
-    const f32x4 a = ((const f32x4*)p)[2 * c], b = ((const f32x4*)p)[2 * c + 1];
+  for (int i = 0; i < kN; i++) r.w[i] = ((const u32x4*)p)[kN * c + i];
+  return r;
+}
+// Streams (x, residual and r are touched once): in bf16 with the streaming
+// hint (16384 x 8192: 172 -> 164 us; the codes are stored plainly, 161 -> 155).  An fp32 lane takes its 32 bytes in two
+// instructions, and with the hint the second one fetches its line again (1003
+// x 4128: 6.2 -> 8.4 us), so those are plain.
+template <bool kBf16>
+__device__ __forceinline__ Raw8<kBf16> load_raw_stream(const void* p, int64_t c) {
+  if constexpr (!kBf16) return load_raw<kBf16>(p, c);
+  return {__builtin_nontemporal_load((const u32x4*)p + c)};
+}
+template <bool kBf16>
+__device__ __forceinline__ void to_f32(const Raw8<kBf16>& r, float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
+  for (int i = 0; i < 8; i++) {
+    if constexpr (kBf16) v[i] = __uint_as_float(i & 1 ? r.w[0][i >> 1] & 0xFFFF0000u : r.w[0][i >> 1] << 16);
+    else v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
   }
 }
 
-// v rounded to the stored type; stores it at p unless p is null.
+// a + b rounded to the stored type, in a.
 template <bool kBf16>
-__device__ __forceinline__ void round_store8(void* p, int64_t c, float (&v)[8]) {
-  if constexpr (kBf16) {
-    u32x4 w;
+__device__ __forceinline__ void add_round(Raw8<kBf16>& a, const Raw8<kBf16>& b) {
+  float u[8], v[8];
+  to_f32<kBf16>(a, u);
+  to_f32<kBf16>(b, v);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const unsigned lo = f32_to_bf16_rne(v[2 * i]), hi = f32_to_bf16_rne(v[2 * i + 1]);
-      w[i] = lo | (hi << 16);
-      v[2 * i] = __uint_as_float(lo << 16);
-      v[2 * i + 1] = __uint_as_float(hi << 16);
+  for (int i = 0; i < 8; i++) u[i] += v[i];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (kBf16) {
+      a.w[0][i] = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)u[2 * i], (__bf16)u[2 * i + 1]});
+    } else {
+      a.w[0][i] = __float_as_uint(u[i]);
+      a.w[1][i] = __float_as_uint(u[4 + i]);
     }
-    ((u32x4*)p)[c] = w;
+  }
+}
+template <bool kBf16>
+__device__ __forceinline__ void store_raw_stream(void* p, int64_t c, const Raw8<kBf16>& r) {
+  if constexpr (kBf16) {
+    __builtin_nontemporal_store(r.w[0], (u32x4*)p + c);
   } else {
-    ((f32x4*)p)[2 * c] = (f32x4){v[0], v[1], v[2], v[3]};
-    ((f32x4*)p)[2 * c + 1] = (f32x4){v[4], v[5], v[6], v[7]};
+    ((u32x4*)p)[2 * c] = r.w[0];
+    ((u32x4*)p)[2 * c + 1] = r.w[1];
   }
 }
 
-__device__ __forceinline__ float sum_wave(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+// v moved across lanes by a DPP control word (every lane reads a live one).
+template <int kCtrl>
+__device__ __forceinline__ double dpp64(double v) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, (u32x2){(unsigned)__builtin_amdgcn_update_dpp(0, (int)w.x, kCtrl, 0xF, 0xF, false),
+                                            (unsigned)__builtin_amdgcn_update_dpp(0, (int)w.y, kCtrl, 0xF, 0xF, false)});
+}
+__device__ __forceinline__ double lane64(double v, int lane) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, (u32x2){(unsigned)__builtin_amdgcn_readlane((int)w.x, lane),
+                                            (unsigned)__builtin_amdgcn_readlane((int)w.y, lane)});
+}
+// Sum over the wave, in every lane: inside rows of 16 by DPP (lane ^ 1, lane ^
+// 2, half row and row mirrored), then the four rows.
+__device__ __forceinline__ double sum_wave(double v) {
+  v += dpp64<kDppQuadXor1>(v);
+  v += dpp64<kDppQuadXor2>(v);
+  v += dpp64<0x141>(v);
+  v += dpp64<0x140>(v);
+  return (lane64(v, 0) + lane64(v, 16)) + (lane64(v, 32) + lane64(v, 48));
 }
 
 // Sum over the T threads of a row, the same in every thread and in every run
-// (fixed tree).  part holds one float per wave of the block.
+// (fixed tree).  part: one value per wave.
 template <int T>
-__device__ __forceinline__ float sum_row(float v, float* part) {
+__device__ __forceinline__ double sum_row(double v, double* part) {
   v = sum_wave(v);
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
@@ -79,52 +122,99 @@ __device__ __forceinline__ float sum_row(float v, float* part) {
   return v;
 }
 
-__device__ __forceinline__ float row_scale(float sum, int64_t k, float eps) {
-  return (float)(1.0 / sqrt((double)sum / (double)k + (double)eps));
+__device__ __forceinline__ float squares(const float (&v)[8]) {
+  float s = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) s = __builtin_fmaf(v[i], v[i], s);
+  return s;
+}
+
+// 1 / sqrt(sum / k + eps) within 2^-40: the fp32 reciprocal root and one Newton
+// step in fp64 (the library's divide and root take over a microsecond of the
+// row's latency), or in full where the argument leaves fp32's range.
+__device__ __forceinline__ double row_factor(double sum, double inv_k, float eps) {
+  const double m = sum * inv_k + (double)eps;
+  if (!(m > 1e-30 && m < 1e30)) return 1.0 / sqrt(m);
+  const double y = (double)__builtin_amdgcn_rsqf((float)m);
+  return __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
+}
+
+// The MXFP8 block codes of y = v * f * w (see the top of the file).
+__device__ __forceinline__ u32x2 scale_quantize(const float (&v)[8], const float (&w)[8], double f, unsigned* code) {
+  const float f32 = (float)f;
+  float y[8];
+  unsigned near = ~0u;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    y[i] = v[i] * f32 * w[i];
+    // 20 bits of the significand lie below E4M3's; their distance to one half,
+    // shifted to the top: within 3 units gives at most 6 << 12
+    near = min(near, (__float_as_uint(y[i]) << 12) + 0x80003000u);
+  }
+  const unsigned top = f32x8_absmax_bits(y);
+  if (near <= 0x6000u || (top > 0x800000u && ((top + 3u) & 0x7FFFFFu) <= 6u)) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const double d = (double)v[i] * f * (double)w[i];
+      const float n = (float)d;
+      // rounded to odd: an inexact result with an even significand moves one
+      // unit towards d
+      unsigned b = __float_as_uint(n);
+      if ((double)n != d && (b & 1u) == 0) b += (fabs(d) > fabs((double)n)) ? 1u : ~0u;
+      y[i] = __uint_as_float(b);
+    }
+  }
+  return mx8_quantize_quad_f32(y, code);
 }
 
 // One row by T threads with U chunks of 8 elements each (k <= 8 T U): T = 64
-// puts four rows into a block, one a wave.  Lanes of a chunk past k hold
-// zeros and store nothing; k % 32 == 0 keeps the quads of a block whole.
+// puts four rows into a block, one a wave.  Lanes of a chunk past k hold zeros
+// and store nothing (skipping their waves measured slower where there are
+// none); k % 32 == 0 keeps the quads of a block whole.  Measured: 16384 x 8192
+// bf16 with residual 152 us (6.2 TB/s), 1 x 8192 3.2 us.
 template <bool kBf16, bool kRes, int T, int U>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void k_rmsnorm_mx8(const void* x, const void* residual,
                                                                    const void* __restrict__ weight, int64_t rows,
-                                                                   int64_t k, float eps, void* r,
+                                                                   int64_t k, double inv_k, float eps, void* r,
                                                                    u32x2* __restrict__ q, uint8_t* __restrict__ s) {
-  __shared__ float part[T / 64];
+  __shared__ double part[T / 64];
   const int tid = T == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t row = T == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (T == 64 && row >= rows) return;
   const int64_t lanes = k / 8, base = row * lanes;
-  float v[U][8], w[U][8], sum = 0;
+  Raw8<kBf16> a[U], p[U], wr[U];
 #pragma unroll
   for (int u = 0; u < U; u++) {
     const int64_t c = u * T + tid;
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[u][i] = 0, w[u][i] = 0;
+    a[u] = {}, wr[u] = {};
     if (c >= lanes) continue;
-    load8_f32<kBf16>(x, base + c, v[u]);
-    load8_f32<kBf16>(weight, c, w[u]);
-    if constexpr (kRes) {
-      float p[8];
-      load8_f32<kBf16>(residual, base + c, p);
-#pragma unroll
-      for (int i = 0; i < 8; i++) v[u][i] += p[i];
-      round_store8<kBf16>(r, base + c, v[u]);
-    }
+    a[u] = load_raw_stream<kBf16>(x, base + c);
+    if constexpr (kRes) p[u] = load_raw_stream<kBf16>(residual, base + c);
+    wr[u] = load_raw<kBf16>(weight, c);
   }
-#pragma unroll
-  for (int u = 0; u < U; u++)
-#pragma unroll
-    for (int i = 0; i < 8; i++) sum = __builtin_fmaf(v[u][i], v[u][i], sum);
-  const float rs = row_scale(sum_row<T>(sum, part), k, eps);
+  double sum = 0;
 #pragma unroll
   for (int u = 0; u < U; u++) {
     const int64_t c = u * T + tid;
+    if constexpr (kRes) {
+      if (c < lanes) {
+        add_round<kBf16>(a[u], p[u]);
+        store_raw_stream<kBf16>(r, base + c, a[u]);
+      }
+    }
+    float v[8];
+    to_f32<kBf16>(a[u], v);
+    sum += (double)squares(v);
+  }
+  const double f = row_factor(sum_row<T>(sum, part), inv_k, eps);
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[u][i] = v[u][i] * rs * w[u][i];
+  for (int u = 0; u < U; u++) {
+    const int64_t c = u * T + tid;
+    float v[8], w[8];
+    to_f32<kBf16>(a[u], v);
+    to_f32<kBf16>(wr[u], w);
     unsigned code;
-    const u32x2 out = mx8_quantize_quad_f32(v[u], &code);
+    const u32x2 out = scale_quantize(v, w, f, &code);
     if (c < lanes) {
       q[base + c] = out;
       if ((c & 3) == 0) s[(base + c) >> 2] = (uint8_t)code;
@@ -136,33 +226,28 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void k_rmsnorm_mx8(const void* x
 // again.
 template <bool kBf16, bool kRes>
 __global__ __launch_bounds__(1024) void k_rmsnorm_mx8_long(const void* x, const void* residual,
-                                                           const void* __restrict__ weight, int64_t k, float eps,
+                                                           const void* __restrict__ weight, int64_t k, double inv_k, float eps,
                                                            void* r, u32x2* __restrict__ q, uint8_t* __restrict__ s) {
-  __shared__ float part[16];
+  __shared__ double part[16];
   const int64_t lanes = k / 8, base = (int64_t)blockIdx.x * lanes;
-  float sum = 0;
+  double sum = 0;
   for (int64_t c = threadIdx.x; c < lanes; c += 1024) {
-    float v[8];
-    load8_f32<kBf16>(x, base + c, v);
+    Raw8<kBf16> a = load_raw<kBf16>(x, base + c);
     if constexpr (kRes) {
-      float p[8];
-      load8_f32<kBf16>(residual, base + c, p);
-#pragma unroll
-      for (int i = 0; i < 8; i++) v[i] += p[i];
-      round_store8<kBf16>(r, base + c, v);
+      add_round<kBf16>(a, load_raw<kBf16>(residual, base + c));
+      store_raw_stream<kBf16>(r, base + c, a);
     }
-#pragma unroll
-    for (int i = 0; i < 8; i++) sum = __builtin_fmaf(v[i], v[i], sum);
+    float v[8];
+    to_f32<kBf16>(a, v);
+    sum += (double)squares(v);
   }
-  const float rs = row_scale(sum_row<1024>(sum, part), k, eps);
+  const double f = row_factor(sum_row<1024>(sum, part), inv_k, eps);
   for (int64_t c = threadIdx.x; c < lanes; c += 1024) {
     float v[8], w[8];
-    load8_f32<kBf16>(kRes ? r : x, base + c, v);  // what this thread itself stored
-    load8_f32<kBf16>(weight, c, w);
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = v[i] * rs * w[i];
+    to_f32<kBf16>(load_raw<kBf16>(kRes ? r : x, base + c), v);  // what this thread itself stored
+    to_f32<kBf16>(load_raw<kBf16>(weight, c), w);
     unsigned code;
-    const u32x2 out = mx8_quantize_quad_f32(v, &code);
+    const u32x2 out = scale_quantize(v, w, f, &code);
     q[base + c] = out;
     if ((c & 3) == 0) s[(base + c) >> 2] = (uint8_t)code;
   }
@@ -175,16 +260,21 @@ void launch_norm(const void* x, const void* residual, const void* weight, int64_
   u32x2* q2 = (u32x2*)q;
 #define MXQ_NORM(T, U)                                                                                             \
   k_rmsnorm_mx8<kBf16, kRes, T, U><<<dim3((unsigned)(T == 64 ? (rows + 3) / 4 : rows)), dim3(T == 64 ? 256 : T), 0, \
-                                     st>>>(x, residual, weight, rows, k, eps, r, q2, s)
+                                     st>>>(x, residual, weight, rows, k, 1.0 / (double)k, eps, r, q2, s)
   if (lanes <= 64) MXQ_NORM(64, 1);
   else if (lanes <= 128) MXQ_NORM(64, 2);
   else if (lanes <= 256) MXQ_NORM(256, 1);
   else if (lanes <= 512) MXQ_NORM(256, 2);
-  else if (lanes <= 1024) MXQ_NORM(256, 4);
+  // Without a residual a block of 512 has half the bytes on their way, and
+  // twice the blocks of 256 do better once there are enough rows: 16384 x 8192
+  // bf16 83 -> 77 us (with a residual even, 152 us; 64 rows 4.0 us with 512
+  // threads, 4.4 with 256).
+  else if (lanes <= 1024 && !kRes && rows >= 1024) MXQ_NORM(256, 4);
+  else if (lanes <= 1024) MXQ_NORM(512, 2);
   else if (lanes <= 2048) MXQ_NORM(1024, 2);
   else if (lanes <= 4096) MXQ_NORM(1024, 4);
   else
-    k_rmsnorm_mx8_long<kBf16, kRes><<<dim3((unsigned)rows), dim3(1024), 0, st>>>(x, residual, weight, k, eps, r, q2, s);
+    k_rmsnorm_mx8_long<kBf16, kRes><<<dim3((unsigned)rows), dim3(1024), 0, st>>>(x, residual, weight, k, 1.0 / (double)k, eps, r, q2, s);
 #undef MXQ_NORM
 }
 
