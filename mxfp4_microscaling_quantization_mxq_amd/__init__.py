@@ -132,12 +132,15 @@ def _torch():
     return _torch_module
 
 
-def _stream():
-    """The current stream of the current device as a raw handle.  (The Stream
-    object of torch.cuda.current_stream() costs 3 us to build, as much as a
-    launch.)"""
+def _stream(dev=None):
+    """The current stream of the current device as a raw handle; with `dev`, the
+    operands have to be on that device.  (The Stream object of
+    torch.cuda.current_stream() costs 3 us to build, as much as a launch.)"""
     c = _torch()._C
-    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    current = c._cuda_getDevice()
+    if dev is not None and dev != current:
+        raise ValueError(f"the operands are on device {dev}, the current device is {current}")
+    return c._cuda_getCurrentRawStream(current)
 
 
 def _dtype_code(dt) -> int:
@@ -493,6 +496,10 @@ def transfp4_dequantize(q, s, meta, res, g, dtype=None, y=None):
 
 # ------------------------------------------------------------------ norm, paged cache, attention
 
+# These run between the products of a decode step, where a call's host time is
+# its cost: one pass of plain comparisons accepts a good call, and only a call
+# that fails it goes through the named checks (which then raise).
+
 def rmsnorm_quantize_fp8(x, weight, residual=None, eps=1e-6, q=None, s=None, r=None):
     """r = x + residual (rounded to x's dtype), y = r / sqrt(mean r^2 + eps) * weight
     along rows, MXFP8 of y: (q[rows, k] E4M3 codes u8, s[rows, k/32] E8M0 u8, r).
@@ -501,27 +508,50 @@ def rmsnorm_quantize_fp8(x, weight, residual=None, eps=1e-6, q=None, s=None, r=N
     Without a residual r is x itself.  Pass r=residual (or r=x) to update the
     residual stream in place."""
     torch = _torch()
-    _need(x, "x", _floats())
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _need(x, "x", _floats())
     rows, k = x.shape
-    _k_blocks(k, 32, "rmsnorm_quantize_fp8")
-    _need(weight, "weight", x.dtype, (k,))
-    if not eps > 0:
-        raise ValueError(f"eps must be > 0, got {eps}")
-    q = _out(q, "q", (rows, k), torch.uint8, x.device)
-    s = _out(s, "s", (rows, k // 32), torch.uint8, x.device)
+    dt, dev = x.dtype, x.get_device()
+    code = MXQ_BF16 if dt is torch.bfloat16 else MXQ_F32
+    good = ((code == MXQ_BF16 or dt is torch.float32) and dev >= 0 and k % 32 == 0 and eps > 0 and x.is_contiguous()
+            and _same(weight, dt, (k,), dev) and (r is None or residual is not None or r is x)
+            and (residual is None or _same(residual, dt, x.shape, dev))
+            and (q is None or _same(q, torch.uint8, x.shape, dev)) and (s is None or _same(s, torch.uint8, (rows, k // 32), dev))
+            and (r is None or _same(r, dt, x.shape, dev)))
+    if not good:
+        _need(x, "x", _floats())
+        _k_blocks(k, 32, "rmsnorm_quantize_fp8")
+        _need(weight, "weight", x.dtype, (k,))
+        if not eps > 0:
+            raise ValueError(f"eps must be > 0, got {eps}")
+        on = {"x": x, "weight": weight, "q": _out(q, "q", (rows, k), torch.uint8, x.device),
+              "s": _out(s, "s", (rows, k // 32), torch.uint8, x.device)}
+        if residual is None:
+            if r is not None and r is not x:
+                raise ValueError("r is only written with a residual")
+        else:
+            _need(residual, "residual", x.dtype, (rows, k))
+            on["residual"], on["r"] = residual, _out(r, "r", (rows, k), x.dtype, x.device)
+        _on_device(**on)
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.uint8)
+    if s is None:
+        s = x.new_empty((rows, k // 32), dtype=torch.uint8)
     if residual is None:
-        if r is not None and r is not x:
-            raise ValueError("r is only written with a residual")
-        _on_device(x=x, weight=weight, q=q, s=s)
         rp, op, r = None, None, x
     else:
-        _need(residual, "residual", x.dtype, (rows, k))
-        r = _out(r, "r", (rows, k), x.dtype, x.device)
-        _on_device(x=x, weight=weight, q=q, s=s, residual=residual, r=r)
+        if r is None:
+            r = torch.empty_like(x)
         rp, op = residual.data_ptr(), r.data_ptr()
-    _check(capi().mxq_rmsnorm_quantize_fp8(x.data_ptr(), rp, weight.data_ptr(), _dtype_code(x.dtype), rows, k, eps,
-                                           op, q.data_ptr(), s.data_ptr(), _stream()), "mxq_rmsnorm_quantize_fp8")
+    _check(capi().mxq_rmsnorm_quantize_fp8(x.data_ptr(), rp, weight.data_ptr(), code, rows, k, eps, op, q.data_ptr(),
+                                           s.data_ptr(), _stream(dev)), "mxq_rmsnorm_quantize_fp8")
     return q, s, r
+
+
+def _same(t, dtype, shape, dev):
+    """A contiguous tensor of this dtype, shape and device (an index)."""
+    return (isinstance(t, _torch_module.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous())
 
 
 class KVCache(NamedTuple):
@@ -549,10 +579,20 @@ def kv_cache(pages, page_size, kv_heads, head_dim, fmt="mxfp8", device="cuda"):
     return KVCache(*(torch.zeros(sh, dtype=torch.uint8, device=device) for sh in shapes))
 
 
-def _cache(cache):
-    """(pages, kv_heads, page_size, head_dim, format) of a KVCache after validation."""
+def _cache(cache, dev):
+    """(pages, kv_heads, page_size, head_dim, format) of a KVCache after
+    validation; its tensors are on device `dev` (an index) or the call is
+    refused by the caller's _on_device."""
     torch = _torch()
     kq, ks, vq, vs = cache
+    if isinstance(kq, torch.Tensor) and isinstance(ks, torch.Tensor) and kq.dim() == 4 and ks.dim() == 4:
+        u8 = torch.uint8
+        pages, heads, page, w = kq.shape
+        n = ks.shape[3]
+        d = 32 * n
+        if ((w == d or 2 * w == d) and _same(kq, u8, kq.shape, dev) and _same(ks, u8, (pages, heads, page, n), dev)
+                and _same(vq, u8, kq.shape, dev) and _same(vs, u8, (pages, heads, n, page), dev)):
+            return pages, heads, page, d, MXQ_MXFP8 if w == d else MXQ_MXFP4
     _need(kq, "kq", torch.uint8, ndim=4)
     _need(ks, "ks", torch.uint8, ndim=4)
     pages, heads, page, w = kq.shape
@@ -562,7 +602,13 @@ def _cache(cache):
     _need(ks, "ks", torch.uint8, (pages, heads, page, d // 32))
     _need(vq, "vq", torch.uint8, (pages, heads, page, w))
     _need(vs, "vs", torch.uint8, (pages, heads, d // 32, page))
-    return pages, heads, page, d, MXQ_MXFP8 if w == d else MXQ_MXFP4
+    _on_device(kq=kq, ks=ks, vq=vq, vs=vs)
+    raise ValueError("the cache and the other operands are on different devices")
+
+
+def _index(t):
+    """The device index of a tensor (-1: host); other things fail their own check later."""
+    return t.get_device() if isinstance(t, _torch().Tensor) else -1
 
 
 def _rows(t, name, dtype, heads, dim):
@@ -573,51 +619,52 @@ def _rows(t, name, dtype, heads, dim):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtype:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtype)}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must have shape [n, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must have shape [n, {heads or 'heads'}, {dim}], got {tuple(shape)}")
     row, inner, one = t.stride()
-    if one != 1 or (inner != dim and t.shape[1] > 1):
+    if one != 1 or (inner != dim and shape[1] > 1):
         raise ValueError(f"{name} must be contiguous in its last two dims")
-    return row if t.shape[0] > 1 else t.shape[1] * dim
-
-
-def _slots(slots, n=None):
-    torch = _torch()
-    _need(slots, "slots", torch.int64, None if n is None else (n,), ndim=1)
+    return row if shape[0] > 1 else shape[1] * dim
 
 
 def kv_append(cache, k, v, slots):
     """Quantize new tokens k, v [tokens, kv_heads, head_dim] (bf16 or fp32, row
     stride free) into their slots (int64 [tokens]; outside the cache, e.g. -1:
     skipped).  The cache is updated in place."""
-    pages, heads, page, d, fmt = _cache(cache)
+    torch = _torch()
+    dev = _index(cache[0])
+    pages, heads, page, d, fmt = _cache(cache, dev)
     k_stride = _rows(k, "k", _floats(), heads, d)
     v_stride = _rows(v, "v", (k.dtype,), heads, d)
     n = k.shape[0]
     if v.shape[0] != n:
         raise ValueError(f"k has {n} tokens, v {v.shape[0]}")
-    _slots(slots, n)
     kq, ks, vq, vs = cache
-    _on_device(kq=kq, ks=ks, vq=vq, vs=vs, k=k, v=v, slots=slots)
+    if dev < 0 or not _same(slots, torch.int64, (n,), dev) or k.get_device() != dev or v.get_device() != dev:
+        _need(slots, "slots", torch.int64, (n,))
+        _on_device(kq=kq, k=k, v=v, slots=slots)
     _check(capi().mxq_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, _dtype_code(k.dtype),
                                 slots.data_ptr(), n, pages, heads, page, d, fmt, kq.data_ptr(), ks.data_ptr(),
-                                vq.data_ptr(), vs.data_ptr(), _stream()), "mxq_kv_append")
+                                vq.data_ptr(), vs.data_ptr(), _stream(dev)), "mxq_kv_append")
 
 
 def kv_read(cache, slots, dtype=None, k=None, v=None):
     """The slots' keys and values, (k, v) [tokens, kv_heads, head_dim] in dtype
     (default bf16); a slot outside the cache reads as zeros."""
     torch = _torch()
-    pages, heads, page, d, fmt = _cache(cache)
-    _slots(slots)
+    dev = _index(cache[0])
+    pages, heads, page, d, fmt = _cache(cache, dev)
     kq, ks, vq, vs = cache
+    _need(slots, "slots", torch.int64, ndim=1)
     n = slots.shape[0]
     dtype = dtype or (k.dtype if k is not None else torch.bfloat16)
     k = _out(k, "k", (n, heads, d), dtype, kq.device, real=True)
     v = _out(v, "v", (n, heads, d), dtype, kq.device, real=True)
-    _on_device(kq=kq, ks=ks, vq=vq, vs=vs, slots=slots, k=k, v=v)
+    if dev < 0 or slots.get_device() != dev or k.get_device() != dev or v.get_device() != dev:
+        _on_device(kq=kq, slots=slots, k=k, v=v)
     _check(capi().mxq_kv_read(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), slots.data_ptr(), n, pages,
-                              heads, page, d, fmt, k.data_ptr(), v.data_ptr(), _dtype_code(dtype), _stream()),
+                              heads, page, d, fmt, k.data_ptr(), v.data_ptr(), _dtype_code(dtype), _stream(dev)),
            "mxq_kv_read")
     return k, v
 
@@ -633,43 +680,58 @@ def paged_attention(q, cache, table, lens, scale=None, window=0, sinks=None, out
     tensor to use for partial results (allocated if None).  A table no wider
     than the batch needs gives the best split."""
     torch = _torch()
-    pages, heads, page, d, fmt = _cache(cache)
+    dev = _index(cache[0])
+    pages, heads, page, d, fmt = _cache(cache, dev)
     q_stride = _rows(q, "q", (torch.bfloat16,), None, d)
-    batch, q_heads = q.shape[0], q.shape[1]
+    batch, q_heads, _ = q.shape
     if q_heads % heads != 0:
         raise ValueError(f"{q_heads} query heads over {heads} cache heads")
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32:
+    if not isinstance(table, torch.Tensor) or table.dtype is not torch.int32:
         raise TypeError("table must be an int32 tensor")
-    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must have shape [{batch}, width] with contiguous rows, got {tuple(table.shape)}")
-    width = table.shape[1]
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must have shape [{batch}, width] with contiguous rows, got {tuple(shape)}")
+    width = shape[1]
     table_stride = table.stride(0) if batch > 1 else max(width, table.stride(0))
-    _need(lens, "lens", torch.int32, (batch,))
+    if not _same(lens, torch.int32, (batch,), dev):
+        _need(lens, "lens", torch.int32, (batch,))
     kq, ks, vq, vs = cache
-    dev = kq.device
     out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
-    out = _out(out, "out", (batch, q_heads, d), out_dtype, dev, real=True)
-    on = {"kq": kq, "ks": ks, "vq": vq, "vs": vs, "q": q, "table": table, "lens": lens, "out": out}
-    if sinks is not None:
+    if out is None and out_dtype is torch.bfloat16:
+        out = q.new_empty((batch, q_heads, d))
+    else:
+        out = _out(out, "out", (batch, q_heads, d), out_dtype, kq.device, real=True)
+    if sinks is not None and not _same(sinks, torch.float32, (q_heads,), dev):
         _need(sinks, "sinks", torch.float32, (q_heads,))
-        on["sinks"] = sinks
+    lib = capi()
     need = ctypes.c_int64()
-    _check(capi().mxq_paged_attention_workspace(batch, q_heads, heads, page, d, width, window, ctypes.byref(need)),
-           "mxq_paged_attention_workspace")
+    code = lib.mxq_paged_attention_workspace(batch, q_heads, heads, page, d, width, window, ctypes.byref(need))
+    if code != 0:
+        _check(code, "mxq_paged_attention_workspace")
+    need = need.value
     if workspace is None:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        wp = None
+        if need:
+            workspace = kq.new_empty(need)
+            wp = workspace.data_ptr()
     else:
         _need(workspace, "workspace", torch.uint8, ndim=1)
-        if workspace.shape[0] < need.value:
-            raise ValueError(f"workspace has {workspace.shape[0]} bytes, {need.value} are needed")
-    on["workspace"] = workspace
-    _on_device(**on)
-    _check(capi().mxq_paged_attention(q.data_ptr(), q_stride, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(),
-                                      vs.data_ptr(), table.data_ptr(), width, table_stride, lens.data_ptr(),
-                                      None if sinks is None else sinks.data_ptr(), batch, q_heads, pages, heads, page,
-                                      d, fmt, 1.0 / math.sqrt(d) if scale is None else scale, window,
-                                      workspace.data_ptr(), workspace.shape[0], out.data_ptr(),
-                                      _dtype_code(out_dtype), _stream()), "mxq_paged_attention")
+        need, least = workspace.shape[0], need
+        if need < least:
+            raise ValueError(f"workspace has {need} bytes, {least} are needed")
+        wp = workspace.data_ptr()
+    if (dev < 0 or q.get_device() != dev or table.get_device() != dev or lens.get_device() != dev
+            or out.get_device() != dev or (sinks is not None and sinks.get_device() != dev)
+            or (workspace is not None and workspace.get_device() != dev)):
+        on = {"kq": kq, "q": q, "table": table, "lens": lens, "out": out, "sinks": sinks, "workspace": workspace}
+        _on_device(**{name: t for name, t in on.items() if t is not None})
+    code = lib.mxq_paged_attention(q.data_ptr(), q_stride, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(),
+                                   table.data_ptr(), width, table_stride, lens.data_ptr(),
+                                   None if sinks is None else sinks.data_ptr(), batch, q_heads, pages, heads, page, d,
+                                   fmt, 1.0 / math.sqrt(d) if scale is None else scale, window, wp, need,
+                                   out.data_ptr(), _dtype_code(out_dtype), _stream(dev))
+    if code != 0:
+        _check(code, "mxq_paged_attention")
     return out
 
 
