@@ -75,6 +75,20 @@ struct AttendParams {
 // vector registers; loop bounds and addresses are scalar only with this.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// The arguments of a kernel whose only argument is p.  With kAgain they are read
+// again at each call: what only one phase of the kernel uses then occupies no
+// scalar register in the others (the tile loop's resources take most of them,
+// and scalars that do not fit are kept in vector registers).  The kernel of
+// ranges is 3 % faster with it on MXFP4, that of units, which has fewer phases,
+// 8-25 % slower (the loop waits for scalar loads it would have kept).
+template <bool kAgain>
+__device__ __forceinline__ const AttendParams& args(const AttendParams& p) {
+  if constexpr (!kAgain) return p;
+  uint64_t k = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(k));
+  return *(const AttendParams*)(const __attribute__((address_space(4))) AttendParams*)k;
+}
+
 // Visible tokens of a sequence: [start, len), in tiles [t0, t1).  A length
 // above what the page table can name is cut to it.
 struct Span {
@@ -132,13 +146,17 @@ __device__ __forceinline__ void load_bytes(__amdgpu_buffer_rsrc_t r, int off, un
   }
 }
 
-// Where 16 consecutive tokens of one cache head lie: row `row` of the cache
+// Where 16 consecutive tokens of one cache head lie: row `row` of the cache,
 // (page * heads + head) * P + position, or nowhere (on = false).
+struct Half {
+  int64_t row;
+  bool on;
+};
 template <int D, bool kFp4>
-__device__ __forceinline__ void load_k(const AttendParams& p, int64_t row, bool on, int h, int i, int g, Tile<D, kFp4>& t) {
+__device__ __forceinline__ void load_k(const AttendParams& p, Half f, int h, int i, int g, Tile<D, kFp4>& t) {
   typedef Tile<D, kFp4> T;
-  const __amdgpu_buffer_rsrc_t rq = panel_rsrc(p.a.kq + row * T::kRow, on ? 16 * T::kRow : 0);
-  const __amdgpu_buffer_rsrc_t rs = panel_rsrc(p.a.ks + row * (D / 32), on ? 16 * (D / 32) : 0);
+  const __amdgpu_buffer_rsrc_t rq = panel_rsrc(p.a.kq + f.row * T::kRow, f.on ? 16 * T::kRow : 0);
+  const __amdgpu_buffer_rsrc_t rs = panel_rsrc(p.a.ks + f.row * (D / 32), f.on ? 16 * (D / 32) : 0);
 #pragma unroll
   for (int r = 0; r < T::kRuns; r++) {
     load_bytes<T::kRun>(rq, i * T::kRow + g * T::kRun + r * 4 * T::kRun, t.k[h] + r * T::kRun / 4);
@@ -146,13 +164,13 @@ __device__ __forceinline__ void load_k(const AttendParams& p, int64_t row, bool 
   }
 }
 template <int D, bool kFp4>
-__device__ __forceinline__ void load_v(const AttendParams& p, int64_t ph, unsigned pos, bool on, int h, int i, int g,
+__device__ __forceinline__ void load_v(const AttendParams& p, Half f, unsigned pos, int h, int i, int g,
                                        Tile<D, kFp4>& t) {
   typedef Tile<D, kFp4> T;
   const unsigned shift = p.c.page_shift;
-  const __amdgpu_buffer_rsrc_t rq = panel_rsrc(p.a.vq + ((ph << shift) + pos) * T::kRow, on ? 16 * T::kRow : 0);
+  const __amdgpu_buffer_rsrc_t rq = panel_rsrc(p.a.vq + f.row * T::kRow, f.on ? 16 * T::kRow : 0);
   const __amdgpu_buffer_rsrc_t rs =
-      panel_rsrc(p.a.vs + ((ph * (D / 32)) << shift) + pos, on ? ((D / 32 - 1) << shift) + 16 : 0);
+      panel_rsrc(p.a.vs + (f.row - pos) * (D / 32) + pos, f.on ? ((D / 32 - 1) << shift) + 16 : 0);
 #pragma unroll
   for (int r = 0; r < 4; r++) load_bytes<T::kLaneV>(rq, 4 * g * T::kRow + i * T::kLaneV + r * T::kRow, t.v[4 * h + r]);
   const int blk = i * (D / 16) / 32;
@@ -218,15 +236,14 @@ __device__ __forceinline__ f32x4 finish(const AttendArgs& a, int64_t hq, float m
 // registers a wave) the accumulators stay out of the AGPR file, whose moves
 // would cost 64 instructions a tile.
 template <int D, bool kFp4, int kTerms, bool kRanges>
-__global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8)) void k_attend(AttendParams p) {
+__global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8)) void k_attend(AttendParams params) {
   typedef Tile<D, kFp4> T;
   constexpr int kRangeShift = range_shift(T::kRow);
   constexpr int kSteps = D / 32;  // QK products of half a tile
   constexpr int J = D / 16;       // PV products of a tile; elements of V per lane and token
   constexpr int kPad = D + 4;
-  constexpr int kBuf = 1;  // tiles a wave has on their way
   __shared__ float lds_o[kWaves][kHeadTile][kPad];
-  __shared__ float lds_m[kWaves][kHeadTile], lds_l[kWaves][kHeadTile];
+  __shared__ float lds_m[kWaves][kHeadTile], lds_l[kWaves][kHeadTile], lds_top[kWaves][kHeadTile];
   __shared__ unsigned lds_sum[kWaves];
   __shared__ int lds_at[5];
 
@@ -239,6 +256,7 @@ __global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8))
   int64_t b;
   Span s;
   if constexpr (!kRanges) {
+    const AttendParams& p = args<kRanges>(params);
     unsigned id = blockIdx.x;
     tg = id % p.tile_groups;
     id /= p.tile_groups;
@@ -254,14 +272,17 @@ __global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8))
       return;
     }
   } else {
+    const AttendParams& p = args<kRanges>(params);
     // each thread sums the tiles of a run of sequences; scan over the block
     const unsigned units = p.c.heads * p.tile_groups;  // of a sequence
     const unsigned batch = (unsigned)p.a.batch, each = (batch + kThreads - 1) / kThreads;
     const unsigned b0 = min(threadIdx.x * each, batch), b1 = min(b0 + each, batch);
     unsigned own = 0;
+    bool empty = false;  // a sequence of this thread's run has no tiles
     for (unsigned k = b0; k < b1; k++) {
       s = span_of(p, k);
       own += (s.t1 - s.t0) * units;
+      empty |= s.t0 == s.t1;
     }
     unsigned incl = own;
 #pragma unroll
@@ -270,56 +291,56 @@ __global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8))
       if (lane >= m) incl += o;
     }
     if (lane == 63) lds_sum[wave] = incl;
-    __syncthreads();
+    const bool any_empty = __syncthreads_or(empty);
     unsigned sum = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; w++) {
       if (w < wave) before += lds_sum[w];
       sum += lds_sum[w];
     }
-    sum = __builtin_amdgcn_readfirstlane(sum);
+    sum = uniform(sum);
     per = range_tiles(sum, kRangeShift);
     x = blockIdx.x * per;
     end = min(x + per, sum);
     unsigned at = before + incl - own;  // first tile of this thread's sequences
     if (x >= at && x < at + own) {
-      for (unsigned k = b0; k < b1; k++) {
+      unsigned k = b0;
+      if (each > 1) {  // (a run of one sequence: s is its span)
         s = span_of(p, k);
-        const unsigned n = s.t1 - s.t0;
-        if (x >= at && x < at + n * units) {
-          const unsigned u = (x - at) / n;
-          lds_at[0] = (int)k, lds_at[1] = (int)u, lds_at[2] = (int)(at + u * n), lds_at[3] = s.start, lds_at[4] = s.len;
+        while (x >= at + (s.t1 - s.t0) * units) {
+          at += (s.t1 - s.t0) * units;
+          s = span_of(p, ++k);
         }
-        at += n * units;
       }
+      const unsigned n = s.t1 - s.t0, u = (x - at) / n;
+      lds_at[0] = (int)k, lds_at[1] = (int)u, lds_at[2] = (int)(at + u * n), lds_at[3] = s.start, lds_at[4] = s.len;
     }
     // the zeros of empty sequences, each by one block
-    for (unsigned k = blockIdx.x; k < batch; k += gridDim.x) {
+    for (unsigned k = any_empty ? blockIdx.x : batch; k < batch; k += gridDim.x) {
       s = span_of(p, k);
-      if (s.t0 == s.t1)
-        for (unsigned e = threadIdx.x; e < p.a.q_heads * (D / 4); e += kThreads)
-          store_out(p.a, (int64_t)k * p.a.q_heads * D + 4 * e, (f32x4){0, 0, 0, 0});
-      if (s.t0 == s.t1 && !p.by_block)
+      if (s.t0 != s.t1) continue;
+      for (unsigned e = threadIdx.x; e < p.a.q_heads * (D / 4); e += kThreads)
+        store_out(p.a, (int64_t)k * p.a.q_heads * D + 4 * e, (f32x4){0, 0, 0, 0});
+      if (!p.by_block)
         for (unsigned u = threadIdx.x; u < units; u += kThreads) p.parts[4 * (k * units + u)] = 0;
     }
     if (p.by_block && threadIdx.x == 0) p.parts[4 * blockIdx.x] = 0;
     if (x >= end) return;
     __syncthreads();
-    b = __builtin_amdgcn_readfirstlane(lds_at[0]);
-    const unsigned u = __builtin_amdgcn_readfirstlane(lds_at[1]);
-    u_first = __builtin_amdgcn_readfirstlane(lds_at[2]);
-    s = span_tiles(__builtin_amdgcn_readfirstlane(lds_at[3]), __builtin_amdgcn_readfirstlane(lds_at[4]));
-    head = u / p.tile_groups;
-    tg = u % p.tile_groups;
+    b = uniform(lds_at[0]);
+    const unsigned u = uniform(lds_at[1]);
+    u_first = uniform(lds_at[2]);
+    s = span_tiles(uniform(lds_at[3]), uniform(lds_at[4]));
+    head = u, tg = 0;
+    if (p.tile_groups > 1) head = u / p.tile_groups, tg = u % p.tile_groups;
   }
 
-  const unsigned per_tile = kWaves / p.block_tiles;  // waves per head tile
-  const int sub = wave % per_tile;                   // this wave among them
-  const unsigned shift = p.c.page_shift, pmask = (1u << shift) - 1;
-  // scores are scaled by |scale| (its sign is in q), never by less than what
-  // keeps a masked score at -inf
-  const float to_log2 = fmaxf(fabsf(p.a.scale) * kLog2e, 0x1p-100f);
-  const unsigned q_sign = p.a.scale < 0 ? 0x80008000u : 0u;
+  // waves per head tile (a power of two), and this wave among them
+  const unsigned block_tiles = args<kRanges>(params).block_tiles;
+  const unsigned per_shift = block_tiles == 4 ? 0 : block_tiles == 2 ? 1 : 2;
+  const unsigned per_tile = 1u << per_shift;
+  const int sub = wave & (per_tile - 1);
+  const unsigned wave_h0 = (wave >> per_shift) * kHeadTile;
 
   while (true) {
     // tiles [first, last) of the unit
@@ -327,185 +348,185 @@ __global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8))
     x = uniform(x), end = uniform(end), u_first = uniform(u_first), head = uniform(head), tg = uniform(tg);
     b = uniform((int)b);
     const int first = s.t0 + (int)(x - u_first), last = min(s.t1, s.t0 + (int)(end - u_first));
-    const unsigned h0 = tg * p.block_tiles * kHeadTile;  // first query head of the unit
+    unsigned h0;  // first query head of the unit
 
-    // Q^T as the B operand: lane (i, g) holds the elements of head i that pair
-    // with the K elements of lane group g
-    const unsigned gh = h0 + wave / per_tile * kHeadTile + i;
-    const bool live = h0 + wave / per_tile * kHeadTile < p.group;
-    bf16x8 qf[kSteps];
-#pragma unroll
-    for (int st = 0; st < kSteps; st++) {
-      const int d = D == 64 ? 16 * g + 8 * st : 128 * (st / 4) + 32 * g + 8 * (st & 3);
-      u32x4 w = {0, 0, 0, 0};
-      if (gh < p.group) w = *(const u32x4*)(p.a.q + b * p.a.q_stride + (int64_t)(head * p.group + gh) * D + d);
-      qf[st] = __builtin_bit_cast(bf16x8, w ^ q_sign);
-    }
-
-    float m = -INFINITY, l = 0;  // of the unscaled scores, and of this lane's tokens
+    // of the unscaled scores, and of this lane's tokens
+    float m = -INFINITY, l = 0, to_log2;
     f32x4 acc[J];
 #pragma unroll
     for (int j = 0; j < J; j++) acc[j] = (f32x4){0, 0, 0, 0};
+    {
+      const AttendParams& p = args<kRanges>(params);
+      h0 = tg * p.block_tiles * kHeadTile;
+      const unsigned shift = p.c.page_shift, pmask = (1u << shift) - 1;
+      // scores are scaled by |scale| (its sign is in q), never by less than what
+      // keeps a masked score at -inf
+      to_log2 = fmaxf(fabsf(p.a.scale) * kLog2e, 0x1p-100f);
+      const unsigned q_sign = p.a.scale < 0 ? 0x80008000u : 0u;
 
-    // This wave's tiles are first + sub + per_tile j, j < count.  The page ids
-    // of the tile to load next are scalars, read from the table one tile
-    // earlier; -1 where the table names no page of the cache.
-    const __attribute__((address_space(4))) int32_t* row =
-        (const __attribute__((address_space(4))) int32_t*)(p.a.table + b * p.a.table_stride);
-    const int count = live && first + sub < last ? (last - first - sub + (int)per_tile - 1) / (int)per_tile : 0;
-    auto token_of = [&](int j) { return (first + sub + (int)per_tile * j) * kTile; };
-    auto id_of = [&](int token) { return uniform(row[(unsigned)min(token, s.len - 1) >> shift]); };
-    auto page_of = [&](int id, int token) { return token < s.len && id >= 0 && id < p.c.pages ? id : -1; };
-    int id0 = id_of(token_of(0)), id1 = id_of(token_of(0) + 16);
-    int fetched = 0;  // tiles whose K is on its way
-
-    T t[kBuf];
-    int page[kBuf][2];  // of the halves of the tile in each buffer
-    auto fetch_k = [&](T& tb, int (&pg)[2]) {
-      const int tok = token_of(fetched);
-      const bool on = fetched < count;
-      pg[0] = on ? page_of(id0, tok) : -1;
-      pg[1] = on ? page_of(id1, tok + 16) : -1;
+      // Q^T as the B operand: lane (i, g) holds the elements of head i that pair
+      // with the K elements of lane group g
+      const unsigned gh = h0 + wave_h0 + i;
+      const bool live = h0 + wave_h0 < p.group;
+      bf16x8 qf[kSteps];
 #pragma unroll
-      for (int h = 0; h < 2; h++)
-        load_k<D, kFp4>(p, (((int64_t)max(pg[h], 0) * p.c.heads + head) << shift) + ((tok + 16 * h) & pmask), pg[h] >= 0,
-                        h, i, g, tb);
-      fetched++;
-      const int next = token_of(min(fetched, count - 1));
-      id0 = id_of(next);
-      id1 = id_of(next + 16);
-    };
-    auto fetch_v = [&](int j, T& tb, const int (&pg)[2]) {
-      const int tok = token_of(j);
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-        load_v<D, kFp4>(p, (int64_t)max(pg[h], 0) * p.c.heads + head, (tok + 16 * h) & pmask, pg[h] >= 0, h, i, g, tb);
-    };
-    if (count > 0) {
-#pragma unroll
-      for (int bf = 0; bf < kBuf; bf++) {
-        fetch_k(t[bf], page[bf]);
-        fetch_v(bf, t[bf], page[bf]);
+      for (int st = 0; st < kSteps; st++) {
+        const int d = D == 64 ? 16 * g + 8 * st : 128 * (st / 4) + 32 * g + 8 * (st & 3);
+        u32x4 w = {0, 0, 0, 0};
+        if (gh < p.group) w = *(const u32x4*)(p.a.q + b * p.a.q_stride + (int64_t)(head * p.group + gh) * D + d);
+        qf[st] = __builtin_bit_cast(bf16x8, w ^ q_sign);
       }
-    }
-    for (int j0 = 0; j0 < count; j0 += kBuf) {
+
+      // This wave's tiles are first + sub + per_tile j, j < count.  The page ids
+      // of the tile to load next are scalars, read from the table one tile
+      // earlier; -1 where the table names no page of the cache.
+      const __attribute__((address_space(4))) int32_t* row =
+          (const __attribute__((address_space(4))) int32_t*)(p.a.table + b * p.a.table_stride);
+      const int count = live && first + sub < last ? (last - first - sub + (int)per_tile - 1) >> per_shift : 0;
+      auto token_of = [&](int j) { return (first + sub + (j << per_shift)) * kTile; };
+      auto id_of = [&](int token) { return uniform(row[(unsigned)min(token, s.len - 1) >> shift]); };
+      int id0 = id_of(token_of(0)), id1 = id_of(token_of(0) + 16);
+      int fetched = 0;  // tiles whose K is on its way
+
+      T t;
+      Half half[2];  // of the tile in t
+      auto fetch_k = [&]() {
+        const int tok = token_of(fetched);
 #pragma unroll
-      for (int bf = 0; bf < kBuf; bf++) {
-        const int j = j0 + bf;
-        const bool here = bf == 0 || j < count;  // loads below are unconditional (see load_k)
-        T& tb = t[bf];
+        for (int h = 0; h < 2; h++) {
+          const int id = h ? id1 : id0, th = tok + 16 * h;
+          half[h].on = fetched < count && th < s.len && id >= 0 && id < p.c.pages;
+          half[h].row = (((int64_t)(half[h].on ? id : 0) * p.c.heads + head) << shift) + (th & pmask);
+          load_k<D, kFp4>(p, half[h], h, i, g, t);
+        }
+        fetched++;
+        const int next = token_of(min(fetched, count - 1));
+        id0 = id_of(next);
+        id1 = id_of(next + 16);
+      };
+      auto fetch_v = [&](int j) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) load_v<D, kFp4>(p, half[h], (token_of(j) + 16 * h) & pmask, h, i, g, t);
+      };
+      if (count > 0) {
+        fetch_k();
+        fetch_v(0);
+      }
+      for (int j = 0; j < count; j++) {
         const int t0 = token_of(j);
-        const int pg0 = page[bf][0], pg1 = page[bf][1];
+        const bool on0 = half[0].on, on1 = half[1].on;
         // S^T
         f32x4 sc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        if (here) {
 #pragma unroll
-          for (int st = 0; st < kSteps; st++)
+        for (int st = 0; st < kSteps; st++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              const float scale = e8m0_as_scale(tb.ks[h][D == 64 ? 0 : st / 4]);
-              u32x4 a;
+          for (int h = 0; h < 2; h++) {
+            const float scale = e8m0_as_scale(t.ks[h][D == 64 ? 0 : st / 4]);
+            u32x4 a;
 #pragma unroll
-              for (int e = 0; e < 4; e++) a[e] = decode2<kFp4>(tb.k[h], 4 * st + e, scale);
-              sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), qf[st], sc[h], 0, 0, 0);
-            }
-        }
-        fetch_k(tb, page[bf]);
-        if (here) {
-          // softmax over the tile; y[4 h + r]: head i, token t0 + 16 h + 4 g + r
-          float y[8];
-#pragma unroll
-          for (int r = 0; r < 8; r++) y[r] = sc[r >> 2][r & 3];
-          const bool whole = t0 >= s.start && t0 + kTile <= s.len && pg0 >= 0 && pg1 >= 0;
-          if (!whole) {
-            // a masked token's K and V bytes are whatever the page holds: its
-            // score is replaced, and its codes and scale are cleared, so nothing
-            // of it (NaN codes among it) reaches a product with a non-zero factor
-#pragma unroll
-            for (int r = 0; r < 8; r++) {
-              const int tok = t0 + 16 * (r >> 2) + 4 * g + (r & 3);
-              const bool seen = (r < 4 ? pg0 : pg1) >= 0 && tok >= s.start && tok < s.len;
-              y[r] = seen ? y[r] : -INFINITY;
-#pragma unroll
-              for (int w = 0; w < (int)(sizeof(tb.v[r]) / 4); w++) tb.v[r][w] = seen ? tb.v[r][w] : 0u;
-              tb.vs[r >> 2] = seen ? tb.vs[r >> 2] : tb.vs[r >> 2] & ~(0xFFu << (8 * (r & 3)));
-            }
+            for (int e = 0; e < 4; e++) a[e] = decode2<kFp4>(t.k[h], 4 * st + e, scale);
+            sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), qf[st], sc[h], 0, 0, 0);
           }
-          float top = y[0];
+        fetch_k();
+        // softmax over the tile; y[4 h + r]: head i, token t0 + 16 h + 4 g + r
+        float y[8];
 #pragma unroll
-          for (int r = 1; r < 8; r++) top = fmaxf(top, y[r]);
-          top = fmaxf(m, max_groups(top));
-          const float ref = top > -INFINITY ? top * to_log2 : 0.0f;  // nothing seen yet: every p is 0
-          if (__builtin_amdgcn_ballot_w64(top > m) != 0) {
-            const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf(m, to_log2, -ref));
-            l *= alpha;
+        for (int r = 0; r < 8; r++) y[r] = sc[r >> 2][r & 3];
+        const bool whole = t0 >= s.start && t0 + kTile <= s.len && on0 && on1;
+        if (!whole) {
+          // a masked token's K and V bytes are whatever the page holds: its
+          // score is replaced, and its codes and scale are cleared, so nothing
+          // of it (NaN codes among it) reaches a product with a non-zero factor
 #pragma unroll
-            for (int j = 0; j < J; j++) acc[j] *= alpha;
-            m = top;
-          }
-          // P in bf16 terms: each takes the upper half of what the ones before
-          // it left (truncated; the last one rounded)
-          u32x4 pt[kTerms];
+          for (int r = 0; r < 8; r++) {
+            const int tok = t0 + 16 * (r >> 2) + 4 * g + (r & 3);
+            const bool seen = (r < 4 ? on0 : on1) && tok >= s.start && tok < s.len;
+            y[r] = seen ? y[r] : -INFINITY;
 #pragma unroll
-          for (int r = 0; r < 8; r += 2) {
-            float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r], to_log2, -ref));
-            float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r + 1], to_log2, -ref));
-            l += p0 + p1;
-#pragma unroll
-            for (int k = 0; k < kTerms; k++) {
-              if (k + 1 == kTerms) {
-                pt[k][r >> 1] = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)p0, (__bf16)p1});
-              } else {
-                const unsigned w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
-                pt[k][r >> 1] = perm(w1, w0, 0x07060302u);
-                p0 -= __uint_as_float(w0 & 0xFFFF0000u);  // exact
-                p1 -= __uint_as_float(w1 & 0xFFFF0000u);
-              }
-            }
-          }
-          // O^T
-          float vscale[8];
-#pragma unroll
-          for (int r = 0; r < 8; r++) vscale[r] = e8m0_as_scale((tb.vs[r >> 2] >> (8 * (r & 3))) & 0xFFu);
-#pragma unroll
-          for (int j2 = 0; j2 < J / 2; j2++) {
-            unsigned d[8];
-#pragma unroll
-            for (int r = 0; r < 8; r++) d[r] = decode2<kFp4>(tb.v[r], j2, vscale[r]);
-            u32x4 va[2];
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-              va[0][r] = perm(d[2 * r + 1], d[2 * r], 0x05040100u);
-              va[1][r] = perm(d[2 * r + 1], d[2 * r], 0x07060302u);
-            }
-#pragma unroll
-            for (int k = 0; k < kTerms; k++)
-#pragma unroll
-              for (int o = 0; o < 2; o++)
-                acc[2 * j2 + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, va[o]), __builtin_bit_cast(bf16x8, pt[k]), acc[2 * j2 + o], 0, 0, 0);
+            for (int w = 0; w < (int)(sizeof(t.v[r]) / 4); w++) t.v[r][w] = seen ? t.v[r][w] : 0u;
+            t.vs[r >> 2] = seen ? t.vs[r >> 2] : t.vs[r >> 2] & ~(0xFFu << (8 * (r & 3)));
           }
         }
-        fetch_v(j + kBuf, tb, page[bf]);
+        float top = y[0];
+#pragma unroll
+        for (int r = 1; r < 8; r++) top = fmaxf(top, y[r]);
+        top = fmaxf(m, max_groups(top));
+        const float ref = top > -INFINITY ? top * to_log2 : 0.0f;  // nothing seen yet: every p is 0
+        if (__builtin_amdgcn_ballot_w64(top > m) != 0) {
+          const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf(m, to_log2, -ref));
+          l *= alpha;
+#pragma unroll
+          for (int j = 0; j < J; j++) acc[j] *= alpha;
+          m = top;
+        }
+        // P in bf16 terms: each takes the upper half of what the ones before
+        // it left (truncated; the last one rounded)
+        u32x4 pt[kTerms];
+#pragma unroll
+        for (int r = 0; r < 8; r += 2) {
+          float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r], to_log2, -ref));
+          float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r + 1], to_log2, -ref));
+          l += p0 + p1;
+#pragma unroll
+          for (int k = 0; k < kTerms; k++) {
+            if (k + 1 == kTerms) {
+              pt[k][r >> 1] = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)p0, (__bf16)p1});
+            } else {
+              const unsigned w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+              pt[k][r >> 1] = perm(w1, w0, 0x07060302u);
+              p0 -= __uint_as_float(w0 & 0xFFFF0000u);  // exact
+              p1 -= __uint_as_float(w1 & 0xFFFF0000u);
+            }
+          }
+        }
+        // O^T
+        float vscale[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++) vscale[r] = e8m0_as_scale((t.vs[r >> 2] >> (8 * (r & 3))) & 0xFFu);
+#pragma unroll
+        for (int j2 = 0; j2 < J / 2; j2++) {
+          unsigned d[8];
+#pragma unroll
+          for (int r = 0; r < 8; r++) d[r] = decode2<kFp4>(t.v[r], j2, vscale[r]);
+          u32x4 va[2];
+#pragma unroll
+          for (int r = 0; r < 4; r++) {
+            va[0][r] = perm(d[2 * r + 1], d[2 * r], 0x05040100u);
+            va[1][r] = perm(d[2 * r + 1], d[2 * r], 0x07060302u);
+          }
+#pragma unroll
+          for (int k = 0; k < kTerms; k++)
+#pragma unroll
+            for (int o = 0; o < 2; o++)
+              acc[2 * j2 + o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, va[o]), __builtin_bit_cast(bf16x8, pt[k]), acc[2 * j2 + o], 0, 0, 0);
+        }
+        fetch_v(j + 1);
       }
     }
 
     // join the waves of a head tile (maxima in log2 units from here on)
+    const AttendParams& p = args<kRanges>(params);
     l = sum_groups(l);
     m *= to_log2;
-    if (g == 0) lds_m[wave][i] = m, lds_l[wave][i] = l;
+    if (g == 0) lds_m[wave][i] = m;
     __syncthreads();
-    const int w0 = wave - sub;
     float mt = -INFINITY;
-    for (unsigned w = 0; w < per_tile; w++) mt = fmaxf(mt, lds_m[w0 + w][i]);
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) {
+      const float mw = lds_m[w][i];
+      mt = w >> per_shift == wave >> per_shift ? fmaxf(mt, mw) : mt;
+    }
     const float f = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mt) : 0.0f;
+    if (g == 0) lds_l[wave][i] = l * f;
+    if (g == 0 && sub == 0) lds_top[wave][i] = mt;
 #pragma unroll
     for (int j = 0; j < J; j++)
 #pragma unroll
       for (int r = 0; r < 4; r++) lds_o[wave][i][(4 * g + r) * J + j] = acc[j][r] * f;
     __syncthreads();
 
-    // out: threads over (head tile, head, 4 elements)
+    // out: threads over (head of the unit, 4 elements)
     constexpr int kQuads = D / 4;
     const bool opens = first == s.t0, closes = last == s.t1;  // of the unit
     if (kRanges && opens && threadIdx.x == 0 && !(p.by_block && closes)) {
@@ -514,17 +535,17 @@ __global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8))
       w[0] = (int)((u_first + (unsigned)(s.t1 - s.t0) - 1) / per - blockIdx.x) + 1;
       w[1] = (int)blockIdx.x, w[2] = (int)unit;
     }
-    for (unsigned e = threadIdx.x; e < p.block_tiles * kHeadTile * kQuads; e += kThreads) {
-      const unsigned hh = e / kQuads, d4 = e % kQuads;  // head of the unit
-      if (h0 + hh >= p.group) continue;
-      const unsigned wb = hh / kHeadTile * per_tile;
-      float mx = -INFINITY;
-      for (unsigned w = 0; w < per_tile; w++) mx = fmaxf(mx, lds_m[wb + w][hh % kHeadTile]);
+    const unsigned heads = min(p.group - h0, p.block_tiles * kHeadTile);
+    for (unsigned e = threadIdx.x; e < heads * kQuads; e += kThreads) {
+      const unsigned hh = e / kQuads, d4 = e % kQuads;
+      const unsigned wb = hh / kHeadTile << per_shift;
+      const float mx = lds_top[wb][hh % kHeadTile];
       float sum = 0;
       f32x4 o = {0, 0, 0, 0};
-      for (unsigned w = 0; w < per_tile; w++) {
-        const float mw = lds_m[wb + w][hh % kHeadTile];
-        sum += mw > -INFINITY ? lds_l[wb + w][hh % kHeadTile] * __builtin_amdgcn_exp2f(mw - mx) : 0.0f;
+#pragma unroll
+      for (unsigned w = 0; w < kWaves; w++) {
+        if (w >= per_tile) break;
+        sum += lds_l[wb + w][hh % kHeadTile];
         o += *(const f32x4*)&lds_o[wb + w][hh % kHeadTile][4 * d4];
       }
       if (!kRanges || (opens && closes)) {
@@ -648,16 +669,16 @@ static int64_t most_tiles(const KvShape& c, int64_t table_width, int64_t window)
 }
 
 // Whether blocks take ranges of the flattened tiles: where a unit would keep
-// one block longer than the join of its parts takes.  A block needs about
-// 0.9 us for 4 tiles, and the more units there are, the longer the others take
-// anyway.  64 query heads over 8, D = 128, MXFP8, ranges / units: 1 sequence of
-// 500 tokens (16 tiles, 8 units) 10.4 / 8.2 us, of 1000 10.4 / 12.4; 8 of
-// 700-1000 (32 tiles, 64 units) 16.5 / 12.5; 16 of 1500-2000 (63 tiles, 128
-// units) 24.0 / 22.2, 64 53.9 / 46.4; 16 of 1000-4000 28.1 / 36.2, 64 73.4 / 75.1.
-// (Eight waves a unit measured slower: 64 of 300-500 19.1 against 15.1.)
-static bool attend_ranges(int64_t units, int64_t tiles) {
-  return tiles > (units >= 128 ? 64 : units >= 32 ? 32 : 16);
-}
+// one block longer than the join of its parts takes, which is a second launch
+// (4 us of GPU time and 4 us of the host's).  A block needs about 1 us for 4
+// tiles, and the more units there are, the longer the others take anyway.  64
+// query heads over 8, D = 128, MXFP8, ranges / units on the GPU: 1 sequence of
+// 500 tokens (16 tiles, 8 units) 10.4 / 7.8 us, of 1000 9.8 / 12 (16 / 12.6
+// with the launches); 8 of 700-1000 (32 tiles, 64 units) 16.5 / 12.0; 16 of
+// 1500-2000 (63 tiles, 128 units) 24.0 / 21.5, 64 53.9 / 46.5; 16 of 1000-4000
+// 27.4 / 36.2, 64 73 / 75.  (Eight waves a unit measured slower: 64 sequences
+// of 300-500 19.1 against 15.1.)
+static bool attend_ranges(int64_t units, int64_t tiles) { return tiles > (units >= 128 ? 64 : 32); }
 
 int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp4, int64_t table_width, int64_t window) {
   const int64_t units = batch * c.heads * tile_groups(q_heads, c), tiles = most_tiles(c, table_width, window);

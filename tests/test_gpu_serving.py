@@ -314,6 +314,41 @@ def test_attention_large_scores():
     attend_case(23, [33, 300], 1, 8, 64, 16, "mxfp4", scale=-0.25)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("seed,batch,most,heads,group,d,page", [
+    (1, 20, 400, 2, 3, 128, 16),    # ranges that end inside units, several units a range
+    (2, 300, 40, 2, 2, 64, 16),     # more sequences than threads of a block; parts by block
+    (3, 4, 700, 1, 70, 64, 16),     # two units a cache head
+    (4, 3, 900, 1, 33, 128, 32),    # three head tiles: one wave each
+    (5, 6, 500, 2, 20, 64, 64),     # two head tiles: two waves each
+    (6, 2, 1500, 3, 4, 256, 16),
+    (7, 40, 300, 8, 1, 64, 128),
+    (8, 1, 3000, 1, 16, 128, 256)])
+def test_attention_ranges(seed, batch, most, heads, group, d, page, fmt):
+    """A table much wider than the sequences: the work is split by ranges of
+    tiles over all of them, empty ones among them, and joined."""
+    rng = np.random.default_rng(seed)
+    lens = [int(n) for n in rng.integers(0, most + 1, size=batch)]
+    lens[rng.integers(batch)] = most
+    if batch > 2:
+        lens[0] = lens[-1] = 0
+    for sinks in (False, True):
+        attend_case(seed, lens, heads, group, d, page, fmt, torch.bfloat16 if seed % 2 else torch.float32,
+                    sinks=sinks, extra_width=4096 // page)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_attention_random(seed):
+    rng = np.random.default_rng(1000 + seed)
+    pick = lambda *a: a[rng.integers(len(a))]  # noqa: E731
+    heads, group, page = pick(1, 2, 3, 8), pick(1, 2, 5, 8, 16, 24), pick(16, 32, 64, 256)
+    batch, most = pick(1, 2, 7, 19), pick(1, 30, 200, 600)
+    lens = [int(n) for n in rng.integers(0, most + 1, size=batch)]
+    attend_case(seed, lens, heads, group, pick(64, 128, 256), page, pick("mxfp8", "mxfp4"),
+                pick(torch.bfloat16, torch.float32), window=pick(0, 0, 1, 40, 150), sinks=bool(pick(0, 1)),
+                extra_width=pick(0, 1, 5000 // page))
+
+
 def test_attention_workspace_table_slice_and_repeat():
     """A caller's workspace (of arbitrary content), a sliced table and a
     repeated call give the same bits."""
