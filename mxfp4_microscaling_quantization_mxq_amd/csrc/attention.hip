@@ -50,7 +50,6 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr int kTile = 32;       // tokens a wave takes at a time
 constexpr int kWaves = 4;       // waves of a block
 constexpr int kThreads = 64 * kWaves;
-constexpr int kMaxUnitTiles16 = 4;  // head tiles of a unit: one to four waves share the range's cache head
 constexpr int kHeadTile = 16;   // query heads of one MFMA column set
 constexpr int64_t kMaxLen = 0x7FFF0000;  // tokens of a sequence (token indexes, also a few tiles past it, are 32 bits)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -650,12 +649,15 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
   store_out(p.a, (b * p.a.q_heads + hq) * D + 4 * d4, finish(p.a, hq, top, sum, o));
 }
 
-
 }  // namespace
 
 // Head tiles of 16 per cache head; a unit takes up to four.
-static int64_t head_tiles(unsigned q_heads, const KvShape& c) { return (q_heads / c.heads + kHeadTile - 1) / kHeadTile; }
-static int64_t tile_groups(unsigned q_heads, const KvShape& c) { return (head_tiles(q_heads, c) + kMaxUnitTiles16 - 1) / kMaxUnitTiles16; }
+static int64_t head_tiles(unsigned q_heads, const KvShape& c) {
+  return (q_heads / c.heads + kHeadTile - 1) / kHeadTile;
+}
+static int64_t tile_groups(unsigned q_heads, const KvShape& c) {
+  return (head_tiles(q_heads, c) + kWaves - 1) / kWaves;
+}
 static int64_t unit_tiles16(unsigned q_heads, const KvShape& c) {
   const int64_t t = head_tiles(q_heads, c);
   return t >= 3 ? 4 : t;
@@ -673,14 +675,15 @@ static int64_t most_tiles(const KvShape& c, int64_t table_width, int64_t window)
 // (4 us of GPU time and 4 us of the host's).  A block needs about 1 us for 4
 // tiles, and the more units there are, the longer the others take anyway.  64
 // query heads over 8, D = 128, MXFP8, ranges / units on the GPU: 1 sequence of
-// 500 tokens (16 tiles, 8 units) 10.4 / 7.8 us, of 1000 9.8 / 12 (16 / 12.6
+// 500 tokens (16 tiles, 8 units) 10.4 / 7.8 us, of 1000 9.8 / 11.2 (16.2 / 11.6
 // with the launches); 8 of 700-1000 (32 tiles, 64 units) 16.5 / 12.0; 16 of
 // 1500-2000 (63 tiles, 128 units) 24.0 / 21.5, 64 53.9 / 46.5; 16 of 1000-4000
 // 27.4 / 36.2, 64 73 / 75.  (Eight waves a unit measured slower: 64 sequences
 // of 300-500 19.1 against 15.1.)
 static bool attend_ranges(int64_t units, int64_t tiles) { return tiles > (units >= 128 ? 64 : 32); }
 
-int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp4, int64_t table_width, int64_t window) {
+int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp4, int64_t table_width,
+                      int64_t window) {
   const int64_t units = batch * c.heads * tile_groups(q_heads, c), tiles = most_tiles(c, table_width, window);
   // flattened tile indexes are 32 bits, with room for one range more
   if (units > (0x7FFFFFFF - 4096) / tiles) return -1;

@@ -327,7 +327,8 @@ mxq_status mxq_kv_read(const uint8_t* kq, const uint8_t* ks, const uint8_t* vq, 
   if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 7u)) return MXQ_ERROR_MISALIGNED;
   e = check_device();
   if (e != MXQ_SUCCESS) return e;
-  return launched(mxq::launch_kv_read(kq, ks, vq, vs, slots, tokens, c, fmt == MXQ_MXFP4, k, v, dt == MXQ_BF16, stream));
+  return launched(
+      mxq::launch_kv_read(kq, ks, vq, vs, slots, tokens, c, fmt == MXQ_MXFP4, k, v, dt == MXQ_BF16, stream));
 }
 
 // Sizes of an attention call over a cache of shape c.

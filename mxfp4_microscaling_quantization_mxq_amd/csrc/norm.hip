@@ -40,9 +40,9 @@ __device__ __forceinline__ Raw8<kBf16> load_raw(const void* p, int64_t c) {
   return r;
 }
 // Streams (x, residual and r are touched once): in bf16 with the streaming
-// hint (16384 x 8192: 172 -> 164 us; the codes are stored plainly, 161 -> 155).  An fp32 lane takes its 32 bytes in two
-// instructions, and with the hint the second one fetches its line again (1003
-// x 4128: 6.2 -> 8.4 us), so those are plain.
+// hint (16384 x 8192: 172 -> 164 us; the codes are stored plainly, 161 -> 155
+// us).  An fp32 lane takes its 32 bytes in two instructions, and the hint makes
+// those slower (8192 x 8192: 162 -> 180 us), so they are plain.
 template <bool kBf16>
 __device__ __forceinline__ Raw8<kBf16> load_raw_stream(const void* p, int64_t c) {
   if constexpr (!kBf16) return load_raw<kBf16>(p, c);
@@ -226,8 +226,9 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void k_rmsnorm_mx8(const void* x
 // again.
 template <bool kBf16, bool kRes>
 __global__ __launch_bounds__(1024) void k_rmsnorm_mx8_long(const void* x, const void* residual,
-                                                           const void* __restrict__ weight, int64_t k, double inv_k, float eps,
-                                                           void* r, u32x2* __restrict__ q, uint8_t* __restrict__ s) {
+                                                           const void* __restrict__ weight, int64_t k, double inv_k,
+                                                           float eps, void* r, u32x2* __restrict__ q,
+                                                           uint8_t* __restrict__ s) {
   __shared__ double part[16];
   const int64_t lanes = k / 8, base = (int64_t)blockIdx.x * lanes;
   double sum = 0;
@@ -274,7 +275,8 @@ void launch_norm(const void* x, const void* residual, const void* weight, int64_
   else if (lanes <= 2048) MXQ_NORM(1024, 2);
   else if (lanes <= 4096) MXQ_NORM(1024, 4);
   else
-    k_rmsnorm_mx8_long<kBf16, kRes><<<dim3((unsigned)rows), dim3(1024), 0, st>>>(x, residual, weight, k, 1.0 / (double)k, eps, r, q2, s);
+    k_rmsnorm_mx8_long<kBf16, kRes>
+        <<<dim3((unsigned)rows), dim3(1024), 0, st>>>(x, residual, weight, k, 1.0 / (double)k, eps, r, q2, s);
 #undef MXQ_NORM
 }
 

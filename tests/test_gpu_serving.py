@@ -479,3 +479,27 @@ def test_work_on_another_stream():
     for a, b in zip(results(s), want):
         assert torch.equal(a, b)
     assert torch.equal(got, want[3])
+
+
+# ------------------------------------------------------------------ the example
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_decode_layer_example(fmt):
+    """The example's decode steps agree with its prompt path on the same cache.
+
+    Both attend over the same stored values.  The prompt path forms scores and
+    weights in fp32 and both round their attention output to bf16, so these
+    differ by at most a bf16 unit (2^-8); MXFP8 codes of it may then differ by
+    one unit (2^-3 of the value) in the elements that lie near a midpoint.  Over
+    the row the difference is bounded by those two: 2^-4 of its norm."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_layer.py")
+    spec = importlib.util.spec_from_file_location("decode_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    outs, again = example.run(fmt, batch=3, prompt=100, steps=5)
+    assert len(outs) == 5 and all(torch.isfinite(o.float()).all() and o.float().abs().max() > 0 for o in outs)
+    a, b = outs[-1].float(), again.float()
+    assert ((a - b).norm(dim=1) <= 2.0 ** -4 * b.norm(dim=1)).all()
