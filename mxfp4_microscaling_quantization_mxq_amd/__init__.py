@@ -516,7 +516,8 @@ def rmsnorm_quantize_fp8(x, weight, residual=None, eps=1e-6, q=None, s=None, r=N
     good = ((code == MXQ_BF16 or dt is torch.float32) and dev >= 0 and k % 32 == 0 and eps > 0 and x.is_contiguous()
             and _same(weight, dt, (k,), dev) and (r is None or residual is not None or r is x)
             and (residual is None or _same(residual, dt, x.shape, dev))
-            and (q is None or _same(q, torch.uint8, x.shape, dev)) and (s is None or _same(s, torch.uint8, (rows, k // 32), dev))
+            and (q is None or _same(q, torch.uint8, x.shape, dev))
+            and (s is None or _same(s, torch.uint8, (rows, k // 32), dev))
             and (r is None or _same(r, dt, x.shape, dev)))
     if not good:
         _need(x, "x", _floats())

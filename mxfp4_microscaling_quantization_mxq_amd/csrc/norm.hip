@@ -13,8 +13,8 @@
 // of its value), which decides its E4M3 code unless it lies that close to the
 // midpoint of two codes; then, and where a lane's largest |y| is that close to
 // a power of two (the block scale), the lane's y are formed again in fp64 and
-// rounded to odd, so that one rounding to the code remains.  (About 1 chunk of
-// 64 lanes in 200 has such a lane.)
+// rounded to odd, so that one rounding to the code remains.  (7 of the 2^20
+// positions between two codes: about 1 chunk of 64 lanes in 300 has such a lane.)
 //
 // Memory bound: x and residual are read once, r, q and s written once (7.03
 // bytes an element in bf16); the row stays in registers between the sum and
@@ -89,8 +89,9 @@ __device__ __forceinline__ void store_raw_stream(void* p, int64_t c, const Raw8<
 template <int kCtrl>
 __device__ __forceinline__ double dpp64(double v) {
   const u32x2 w = __builtin_bit_cast(u32x2, v);
-  return __builtin_bit_cast(double, (u32x2){(unsigned)__builtin_amdgcn_update_dpp(0, (int)w.x, kCtrl, 0xF, 0xF, false),
-                                            (unsigned)__builtin_amdgcn_update_dpp(0, (int)w.y, kCtrl, 0xF, 0xF, false)});
+  const u32x2 moved = {(unsigned)__builtin_amdgcn_update_dpp(0, (int)w.x, kCtrl, 0xF, 0xF, false),
+                       (unsigned)__builtin_amdgcn_update_dpp(0, (int)w.y, kCtrl, 0xF, 0xF, false)};
+  return __builtin_bit_cast(double, moved);
 }
 __device__ __forceinline__ double lane64(double v, int lane) {
   const u32x2 w = __builtin_bit_cast(u32x2, v);
@@ -171,7 +172,7 @@ __device__ __forceinline__ u32x2 scale_quantize(const float (&v)[8], const float
 // puts four rows into a block, one a wave.  Lanes of a chunk past k hold zeros
 // and store nothing (skipping their waves measured slower where there are
 // none); k % 32 == 0 keeps the quads of a block whole.  Measured: 16384 x 8192
-// bf16 with residual 152 us (6.2 TB/s), 1 x 8192 3.2 us.
+// bf16 with residual 144 us (6.6 TB/s), 1 x 8192 2.9 us.
 template <bool kBf16, bool kRes, int T, int U>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void k_rmsnorm_mx8(const void* x, const void* residual,
                                                                    const void* __restrict__ weight, int64_t rows,
