@@ -40,9 +40,10 @@ __device__ __forceinline__ Raw8<kBf16> load_raw(const void* p, int64_t c) {
   return r;
 }
 // Streams (x, residual and r are touched once; times of variants in turn, in
-// one graph's replays): in bf16 with the streaming hint (16384 x 8192: 172 -> 164 us; the codes are stored plainly, 161 -> 155
-// us).  An fp32 lane takes its 32 bytes in two instructions, and the hint makes
-// those slower (8192 x 8192: 162 -> 180 us), so they are plain.
+// one graph's replays): in bf16 with the streaming hint (16384 x 8192: 172 ->
+// 164 us; the codes are stored plainly, 161 -> 155 us).  An fp32 lane takes
+// its 32 bytes in two instructions, and the hint makes those slower (8192 x
+// 8192: 162 -> 180 us), so they are plain.
 template <bool kBf16>
 __device__ __forceinline__ Raw8<kBf16> load_raw_stream(const void* p, int64_t c) {
   if constexpr (!kBf16) return load_raw<kBf16>(p, c);
