@@ -455,7 +455,9 @@ __global__ __launch_bounds__(kThreads, 1 << (range_shift(kFp4 ? D / 2 : D) - 8))
         top = fmaxf(m, max_groups(top));
         const float ref = top > -INFINITY ? top * to_log2 : 0.0f;  // nothing seen yet: every p is 0
         if (__builtin_amdgcn_ballot_w64(top > m) != 0) {
-          const float alpha = __builtin_amdgcn_exp2f(__builtin_fmaf(m, to_log2, -ref));
+          // the old terms are relative to the rounded m * to_log2, so that is what
+          // moves them: exactly 1 for a head whose maximum stays
+          const float alpha = __builtin_amdgcn_exp2f(m * to_log2 - ref);
           l *= alpha;
 #pragma unroll
           for (int j = 0; j < J; j++) acc[j] *= alpha;

@@ -314,6 +314,72 @@ def test_attention_large_scores():
     attend_case(23, [33, 300], 1, 8, 64, 16, "mxfp4", scale=-0.25)
 
 
+def e4m3_step(i):
+    """(code, E8M0 code) of the i-th of 1024 rising values, 8 a binade, from 2^-110."""
+    return 0x38 | (i & 7), 17 + (i >> 3)
+
+
+def e2m1_step(i):
+    """(code, E8M0 code) of the i-th of 256 rising values, 2 a binade, from 2^-110."""
+    return 2 | (i & 1), 17 + (i >> 1)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_attention_weights_survive_other_heads_rising_maxima(fmt):
+    """One query head's maximum rises tile after tile; the others have theirs
+    in the first tiles and again in the last, with V = 1 there and -1 here, so
+    their output is 0 and shows any factor by which the first weights were
+    scaled on the way.
+
+    1023 sequences of 1024 tiles of 32 tokens and a short one between them: a
+    block takes 1024 tiles, a wave 256.  Scores have one non-zero product and
+    scale 1: they are exact, and so are those below the maximum (a score 60
+    below adds nothing).  Equal scores have equal probabilities, within 2^-23
+    of their value and 2^-24 of it for P's terms.  A lane sums 16 tiles' worth
+    of them (4 additions a tile), then the groups, waves and blocks are added:
+    at most 64 + 16 roundings in the sum, and no more in O.
+    bound = 2 (2^-23 + 2^-24 + 80 u), u = 2^-24.  It has no term that grows with
+    the number of tiles or with the scores."""
+    d, page, tiles, edge = 64, 64, 1024, 8
+    n = 32 * tiles
+    row = d if fmt == "mxfp8" else d // 2
+    one = 0x38 if fmt == "mxfp8" else 2  # 1.0
+    kq, vq = (np.zeros((n, row), dtype=np.uint8) for _ in range(2))
+    ks, vs = (np.full((n, d // 32), 127, dtype=np.uint8) for _ in range(2))
+    tile = np.arange(n) // 32
+    ends = (tile < edge) | (tile >= tiles - edge)
+    sign = 0x80 if fmt == "mxfp8" else 8
+    kq[:, 0] = np.where(ends, one, one | sign)  # element 0: 1 at the ends, -1 between
+    vq[:, 0] = np.where(tile < edge, one, np.where(tile >= tiles - edge, one | sign, 0))
+    steps = [e4m3_step(t) if fmt == "mxfp8" else e2m1_step(t // 4) for t in range(tiles)]
+    kq[:, row // 2] = np.array([c for c, _ in steps], dtype=np.uint8)[tile]  # element 32: rising
+    ks[:, 1] = np.array([s for _, s in steps], dtype=np.uint8)[tile]
+    pages = lambda a: np.ascontiguousarray(a.reshape(n // page, 1, page, -1))  # noqa: E731
+    cache = [pages(kq), pages(ks), pages(vq), np.ascontiguousarray(pages(vs).transpose(0, 1, 3, 2))]
+    level = np.array([29.125, 30.25, 31.375, 27.875, 33.5, 35.75, 38.25])
+    q64 = np.zeros((8, d))
+    q64[:7, 0] = level
+    q64[7, 32] = 2.0 ** -12
+    qb, _ = stored(np.broadcast_to(q64, (1024, 8, d)), "bf16")
+    lens = np.full(1024, n, dtype=np.int32)
+    lens[512] = 100
+    table = np.broadcast_to(np.arange(n // page, dtype=np.int32), (1024, n // page))
+    y = host(mxq.paged_attention(dev(qb), on_device(cache), dev(table), dev(lens), scale=1.0,
+                                 out_dtype=torch.float32)).astype(np.float64)
+    full = np.arange(1024) != 512
+    bound = 2 * (2.0 ** -23 + 2.0 ** -24 + 80 * U)
+    worst = np.abs(y[full, :7, 0]).max()
+    assert worst <= bound, f"{worst:.3g}, bound {bound:.3g}"
+    assert np.abs(y[512, :, 0] - 1).max() <= bound  # 100 tokens, all of V = 1
+    assert not y[..., 1:].any()
+    # the rising head, with the bound of its scores' roundings
+    k = np.array([oracle.e4m3_decode(c) if fmt == "mxfp8" else 1 + (c & 1) / 2 for c, _ in steps])
+    x = (k * np.exp2(np.array([s for _, s in steps], dtype=np.float64) - 127))[tile] * 2.0 ** -12
+    p = np.exp(x - x.max())
+    v = np.where(tile < edge, 1.0, np.where(tile >= tiles - edge, -1.0, 0.0))
+    assert np.abs(y[full, 7, 0] - p @ v / p.sum()).max() <= 2 * 68 * U * x.max() + 2.0 ** -21 + (n / 8 + 64) * U
+
+
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
 @pytest.mark.parametrize("seed,batch,most,heads,group,d,page", [
     (1, 20, 400, 2, 3, 128, 16),    # ranges that end inside units, several units a range
