@@ -8,8 +8,9 @@
 // The norm is taken of the rounded r, the value that is stored and that the
 // next layer adds to, so fused and unfused programs see the same stream.
 //
-// Roundings.  Squares are summed in fp32 over a lane's 8 elements and in fp64
-// from there on; the row's factor is fp64.  y is formed in fp32 (within 2 ulp
+// Roundings.  Squares, which fp64 holds exactly, are summed in fp64, and the
+// row's factor is fp64, so neither leaves its range for finite rows (fp32 squares
+// do from 1.8e19).  y is formed in fp32 (within 2 ulp
 // of its value), which decides its E4M3 code unless it lies that close to the
 // midpoint of two codes; then, and where a lane's largest |y| is that close to
 // a power of two (the block scale), the lane's y are formed again in fp64 and
@@ -56,6 +57,17 @@ __device__ __forceinline__ void to_f32(const Raw8<kBf16>& r, float (&v)[8]) {
     if constexpr (kBf16) v[i] = __uint_as_float(i & 1 ? r.w[0][i >> 1] & 0xFFFF0000u : r.w[0][i >> 1] << 16);
     else v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
   }
+}
+
+// r again, as a value the compiler knows nothing of: it would keep the fp64
+// values of the squares in registers for the branch of scale_quantize that
+// seldom forms them again (82 registers for 51; 16384 x 8192 bf16 with residual 168 us for 155).
+template <bool kBf16>
+__device__ __forceinline__ void forget(Raw8<kBf16>& r) {
+#pragma unroll
+  for (int i = 0; i < (kBf16 ? 1 : 2); i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) asm volatile("" : "+v"(r.w[i][j]));
 }
 
 // a + b rounded to the stored type, in a.
@@ -124,20 +136,25 @@ __device__ __forceinline__ double sum_row(double v, double* part) {
   return v;
 }
 
-__device__ __forceinline__ float squares(const float (&v)[8]) {
-  float s = 0;
+// In two chains, for their latency.
+__device__ __forceinline__ double squares(const float (&v)[8]) {
+  double s0 = 0, s1 = 0;
 #pragma unroll
-  for (int i = 0; i < 8; i++) s = __builtin_fmaf(v[i], v[i], s);
-  return s;
+  for (int i = 0; i < 8; i += 2) {
+    s0 = __builtin_fma((double)v[i], (double)v[i], s0);
+    s1 = __builtin_fma((double)v[i + 1], (double)v[i + 1], s1);
+  }
+  return s0 + s1;
 }
 
-// 1 / sqrt(sum / k + eps) within 2^-40: the fp32 reciprocal root and one Newton
-// step in fp64 (the library's divide and root take over a microsecond of the
+// 1 / sqrt(sum / k + eps) within 2^-50: the fp32 reciprocal root and two Newton
+// steps in fp64 (the library's divide and root take over a microsecond of the
 // row's latency), or in full where the argument leaves fp32's range.
 __device__ __forceinline__ double row_factor(double sum, double inv_k, float eps) {
   const double m = sum * inv_k + (double)eps;
   if (!(m > 1e-30 && m < 1e30)) return 1.0 / sqrt(m);
-  const double y = (double)__builtin_amdgcn_rsqf((float)m);
+  double y = (double)__builtin_amdgcn_rsqf((float)m);
+  y = __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
   return __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
 }
 
@@ -206,13 +223,14 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void k_rmsnorm_mx8(const void* x
     }
     float v[8];
     to_f32<kBf16>(a[u], v);
-    sum += (double)squares(v);
+    sum += squares(v);
   }
   const double f = row_factor(sum_row<T>(sum, part), inv_k, eps);
 #pragma unroll
   for (int u = 0; u < U; u++) {
     const int64_t c = u * T + tid;
     float v[8], w[8];
+    forget<kBf16>(a[u]);
     to_f32<kBf16>(a[u], v);
     to_f32<kBf16>(wr[u], w);
     unsigned code;
@@ -242,7 +260,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_mx8_long(const void* x, const 
     }
     float v[8];
     to_f32<kBf16>(a, v);
-    sum += (double)squares(v);
+    sum += squares(v);
   }
   const double f = row_factor(sum_row<1024>(sum, part), inv_k, eps);
   for (int64_t c = threadIdx.x; c < lanes; c += 1024) {

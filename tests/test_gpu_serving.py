@@ -88,6 +88,71 @@ def test_norm_zero_rows_signs_and_extremes():
         assert not host(s)[0].any() and not (host(q)[0] & 0x7F).any()
 
 
+def norm_y(r64, w64, eps):
+    """The normalised rows in extended precision (eps as the fp32 the call takes), as float64."""
+    r = r64.astype(np.longdouble)
+    mean = (r * r).sum(axis=-1, keepdims=True) / r.shape[-1]
+    return (r / np.sqrt(mean + np.longdouble(np.float32(eps))) * w64.astype(np.longdouble)).astype(np.float64)
+
+
+# The kernel's y where it decides a code: squares of fp32 values are exact in
+# fp64, at most 64 + 22 additions of positive terms and half of that through the
+# root, a few units in the factor and two products, 2^-53 each: below 128 of them.
+DELTA64 = 2.0 ** -46
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [544, 1056, 4128, 8192, 32800])
+def test_norm_range(k, dtype):
+    """Finite rows whose squares leave fp32's range."""
+    rng = np.random.default_rng(k)
+    size = [6.6e18, 2e19, 1e25, 1e30, 2.0 ** -60, 2.0 ** -75, 2.0 ** -100, 2.0 ** -130, 1.0]
+    x = np.stack([c * np.clip(rng.standard_normal(k), -1.6, 1.6) for c in size] + [np.full(k, c) for c in size])
+    x[9, ::3] = 0
+    a, a64 = stored(x, dtype)
+    w, w64 = stored(1 + 0.3 * rng.standard_normal(k), dtype)
+    for eps in (1e-5, 1e-30, 1e-45):
+        q, s, _ = mxq.rmsnorm_quantize_fp8(dev(a), dev(w), eps=eps)
+        model.check_mx8(host(q), host(s), norm_y(a64, w64, eps), DELTA64, f"{dtype} eps {eps}")
+
+
+def near_midpoints(rng, target, f):
+    """fp32 weights that put y = f * weight 0 to 2 units to either side of target."""
+    w = (target / f).astype(np.float32)
+    return (w.view(np.int32) + rng.integers(-2, 3, size=w.shape, dtype=np.int32)).view(np.float32)
+
+
+@pytest.mark.parametrize("k,value", [(32, 3.0), (64, 0.7), (544, 1.1), (2048, -5.3), (4128, 1e-3), (8192, 0.37),
+                                     (40000, 2.9)])
+def test_norm_codes_next_to_midpoints(k, value):
+    """Rows of one value, whose squares all round alike, with weights that put y
+    next to the midpoints of normal E4M3 codes: the code is that of y to fp64's
+    accuracy."""
+    rng = np.random.default_rng(k)
+    x = np.full((1, k), value, dtype=np.float32)
+    f = norm_y(x.astype(np.float64), np.ones(k), 1e-5)[0]
+    target = (1 + (2 * rng.integers(0, 8, size=k) + 1) / 16) * np.exp2(rng.integers(-6, 6, size=k))
+    target[::32] = 96.0  # the block's largest: scale 2^-2
+    w = near_midpoints(rng, target, f)
+    q, s, _ = mxq.rmsnorm_quantize_fp8(dev(x), dev(w), eps=1e-5)
+    y = norm_y(x.astype(np.float64), w.astype(np.float64), 1e-5)
+    model.check_mx8(host(q), host(s), y, DELTA64, f"{k} x {value}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_codes_of_many_rows(dtype):
+    """A few million elements, compared as closely."""
+    rng = np.random.default_rng(8)
+    rows, k = 1024, 4096
+    a, a64 = stored(rng.standard_normal((rows, k)), dtype)
+    p, p64 = stored(rng.standard_normal((rows, k)), dtype)
+    w, w64 = stored(1 + 0.1 * rng.standard_normal(k), dtype)
+    q, s, r = mxq.rmsnorm_quantize_fp8(dev(a), dev(w), dev(p), eps=1e-5)
+    r64, _ = model.norm_rows(a64, p64, w64, 1e-5, dtype == "bf16")
+    assert np.array_equal(oracle.to_f64(host(r)), r64)
+    model.check_mx8(host(q), host(s), norm_y(r64, w64, 1e-5), DELTA64, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("k", [96, 4128, 40000])
 def test_norm_in_place(dtype, k):
