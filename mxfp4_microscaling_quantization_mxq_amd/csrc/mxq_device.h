@@ -239,28 +239,40 @@ __device__ __forceinline__ unsigned mx_quantize_quad_f32(const float (&v)[8], un
   return out;
 }
 
-// MXFP8 of one lane's 8 consecutive fp32 values of a quad's block, every
-// magnitude clamped to 448 * 2^e ahead of the convert (as mx8_encode8_bf16;
-// fp32 bits of the limit: exponent field code + 8, mantissa .11).
-__device__ __forceinline__ u32x2 mx8_quantize_quad_f32(const float (&v)[8], unsigned* code) {
-  typedef short s16x2 __attribute__((ext_vector_type(2)));
-  unsigned m = f32x8_absmax_bits(v);
+// Largest magnitude bits over a quad of lanes.
+__device__ __forceinline__ unsigned quad_max(unsigned m) {
   m = max(m, dpp_quad_xor1(m));
-  m = max(m, dpp_quad_xor2(m));
-  const unsigned c = e8m0_code_e4m3(m >> 23);
+  return max(m, dpp_quad_xor2(m));
+}
+
+// fp32 bits of 448 * 2^e for block code c (exponent field c + 8, mantissa .11):
+// what the magnitudes of a block are clamped to ahead of the convert (as in
+// mx8_encode8_bf16).
+__device__ __forceinline__ unsigned mx8_limit_bits(unsigned c) { return ((c + 8u) << 23) | 0x600000u; }
+
+// E4M3 codes of 8 fp32 values, clamped already, under block code c.
+__device__ __forceinline__ u32x2 mx8_convert8_f32(const float (&v)[8], unsigned c) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
   const float scale = e8m0_as_scale(c);
-  const unsigned lim = ((c + 8u) << 23) | 0x600000u;
-  auto clamp = [&](float f) {
-    const unsigned w = __float_as_uint(f);
-    return __uint_as_float(min(w & 0x7FFFFFFFu, lim) | (w & 0x80000000u));
-  };
   s16x2 lo = {0, 0}, hi = {0, 0};
-  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, clamp(v[0]), clamp(v[1]), scale, false);
-  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, clamp(v[2]), clamp(v[3]), scale, true);
-  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, clamp(v[4]), clamp(v[5]), scale, false);
-  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, clamp(v[6]), clamp(v[7]), scale, true);
-  *code = c;
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[0], v[1], scale, false);
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[2], v[3], scale, true);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[4], v[5], scale, false);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[6], v[7], scale, true);
   return (u32x2){__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
+}
+
+// MXFP8 of one lane's 8 consecutive fp32 values of a quad's block.
+__device__ __forceinline__ u32x2 mx8_quantize_quad_f32(const float (&v)[8], unsigned* code) {
+  const unsigned c = e8m0_code_e4m3(quad_max(f32x8_absmax_bits(v)) >> 23), lim = mx8_limit_bits(c);
+  float cl[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const unsigned w = __float_as_uint(v[i]);
+    cl[i] = __uint_as_float(min(w & 0x7FFFFFFFu, lim) | (w & 0x80000000u));
+  }
+  *code = c;
+  return mx8_convert8_f32(cl, c);
 }
 
 // MXFP8 of one lane's 8 consecutive bf16 values of a quad's block.

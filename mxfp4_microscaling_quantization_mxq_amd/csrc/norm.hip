@@ -10,12 +10,11 @@
 //
 // Roundings.  Squares, which fp64 holds exactly, are summed in fp64, and the
 // row's factor is fp64, so neither leaves its range for finite rows (fp32 squares
-// do from 1.8e19).  y is formed in fp32 (within 2 ulp
-// of its value), which decides its E4M3 code unless it lies that close to the
-// midpoint of two codes; then, and where a lane's largest |y| is that close to
-// a power of two (the block scale), the lane's y are formed again in fp64 and
-// rounded to odd, so that one rounding to the code remains.  (7 of the 2^20
-// positions between two codes: about 1 chunk of 64 lanes in 300 has such a lane.)
+// do from 1.8e19).  y is formed in fp32, which decides its E4M3 code unless the
+// midpoint of two codes lies within 3 * 2^-23 of it; then, and where a block's
+// largest |y| is that close to a power of two (its scale), the wave's y are
+// formed again in fp64 and rounded to odd, so that one rounding to the code
+// remains.  (About 1 chunk of 64 lanes in 300 has such a lane.)
 //
 // Memory bound: x and residual are read once, r, q and s written once (7.03
 // bytes an element in bf16); the row stays in registers between the sum and
@@ -61,7 +60,7 @@ __device__ __forceinline__ void to_f32(const Raw8<kBf16>& r, float (&v)[8]) {
 
 // r again, as a value the compiler knows nothing of: it would keep the fp64
 // values of the squares in registers for the branch of scale_quantize that
-// seldom forms them again (82 registers for 51; 16384 x 8192 bf16 with residual 168 us for 155).
+// seldom forms them again.
 template <bool kBf16>
 __device__ __forceinline__ void forget(Raw8<kBf16>& r) {
 #pragma unroll
@@ -147,41 +146,65 @@ __device__ __forceinline__ double squares(const float (&v)[8]) {
   return s0 + s1;
 }
 
-// 1 / sqrt(sum / k + eps) within 2^-50: the fp32 reciprocal root and two Newton
-// steps in fp64 (the library's divide and root take over a microsecond of the
-// row's latency), or in full where the argument leaves fp32's range.
-__device__ __forceinline__ double row_factor(double sum, double inv_k, float eps) {
+// 1 / sqrt(m), m = sum / k + eps: f within 2^-40, the fp32 reciprocal root and
+// one Newton step in fp64 (the library's divide and root take over a microsecond
+// of the row's latency), or in full where m leaves fp32's range.
+struct Factor {
+  double f, m;
+};
+__device__ __forceinline__ bool in_range(double m) { return m > 1e-30 && m < 1e30; }
+__device__ __forceinline__ Factor row_factor(double sum, double inv_k, float eps) {
   const double m = sum * inv_k + (double)eps;
-  if (!(m > 1e-30 && m < 1e30)) return 1.0 / sqrt(m);
-  double y = (double)__builtin_amdgcn_rsqf((float)m);
-  y = __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
-  return __builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y);
+  if (!in_range(m)) return {1.0 / sqrt(m), m};
+  const double y = (double)__builtin_amdgcn_rsqf((float)m);
+  return {__builtin_fma(0.5 * y, __builtin_fma(-m * y, y, 1.0), y), m};
+}
+// f within 2^-50: one step more, where y is formed in fp64.
+__device__ __forceinline__ double refined(const Factor& f) {
+  return in_range(f.m) ? __builtin_fma(0.5 * f.f, __builtin_fma(-f.m * f.f, f.f, 1.0), f.f) : f.f;
 }
 
-// The MXFP8 block codes of y = v * f * w (see the top of the file).
-__device__ __forceinline__ u32x2 scale_quantize(const float (&v)[8], const float (&w)[8], double f, unsigned* code) {
-  const float f32 = (float)f;
-  float y[8];
-  unsigned near = ~0u;
+// The MXFP8 block codes of y = r * f * w (see the top of the file): the codes
+// of 1 - d and 1 + d times the fp32 y, d = 3 * 2^-23, are the same unless the
+// midpoint of two codes, normal or subnormal, lies between them.  Three
+// roundings put y within 3 * 2^-24 of its value, the two factors add 2^-24.
+template <bool kBf16>
+__device__ __forceinline__ u32x2 scale_quantize(Raw8<kBf16> r, Raw8<kBf16> weight, const Factor& factor,
+                                                unsigned* code) {
+  const float f32 = (float)factor.f;
+  float v[8], w[8], y[8];
+  to_f32<kBf16>(r, v);
+  to_f32<kBf16>(weight, w);
+#pragma unroll
+  for (int i = 0; i < 8; i++) y[i] = v[i] * f32 * w[i];
+  const unsigned top = quad_max(f32x8_absmax_bits(y)), c = e8m0_code_e4m3(top >> 23);
+  // clamped to 8 units below 448 * 2^e, so that 1 + d times it is below that
+  const float lim = __uint_as_float(mx8_limit_bits(c) - 8u);
+  float lo[8], hi[8];
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    y[i] = v[i] * f32 * w[i];
-    // 20 bits of the significand lie below E4M3's; their distance to one half,
-    // shifted to the top: within 3 units gives at most 6 << 12
-    near = min(near, (__float_as_uint(y[i]) << 12) + 0x80003000u);
+    const float z = __builtin_amdgcn_fmed3f(y[i], -lim, lim);
+    lo[i] = z * (1 - 0x3p-23f);
+    hi[i] = z * (1 + 0x3p-23f);
   }
-  const unsigned top = f32x8_absmax_bits(y);
-  if (near <= 0x6000u || (top > 0x800000u && ((top + 3u) & 0x7FFFFFu) <= 6u)) {
+  const u32x2 out = mx8_convert8_f32(lo, c), other = mx8_convert8_f32(hi, c);
+  *code = c;
+  const bool again = ((out.x ^ other.x) | (out.y ^ other.y)) != 0 || (top > 0x800000u && ((top + 3u) & 0x7FFFFFu) <= 6u);
+  if (__builtin_amdgcn_ballot_w64(again) == 0) return out;
+  const double f = refined(factor);
+  forget<kBf16>(r);
+  forget<kBf16>(weight);
+  to_f32<kBf16>(r, v);
+  to_f32<kBf16>(weight, w);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const double d = (double)v[i] * f * (double)w[i];
-      const float n = (float)d;
-      // rounded to odd: an inexact result with an even significand moves one
-      // unit towards d
-      unsigned b = __float_as_uint(n);
-      if ((double)n != d && (b & 1u) == 0) b += (fabs(d) > fabs((double)n)) ? 1u : ~0u;
-      y[i] = __uint_as_float(b);
-    }
+  for (int i = 0; i < 8; i++) {
+    const double d = (double)v[i] * f * (double)w[i];
+    const float n = (float)d;
+    // rounded to odd: an inexact result with an even significand moves one
+    // unit towards d
+    unsigned b = __float_as_uint(n);
+    if ((double)n != d && (b & 1u) == 0) b += (fabs(d) > fabs((double)n)) ? 1u : ~0u;
+    y[i] = __uint_as_float(b);
   }
   return mx8_quantize_quad_f32(y, code);
 }
@@ -225,16 +248,13 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void k_rmsnorm_mx8(const void* x
     to_f32<kBf16>(a[u], v);
     sum += squares(v);
   }
-  const double f = row_factor(sum_row<T>(sum, part), inv_k, eps);
+  const Factor f = row_factor(sum_row<T>(sum, part), inv_k, eps);
 #pragma unroll
   for (int u = 0; u < U; u++) {
     const int64_t c = u * T + tid;
-    float v[8], w[8];
-    forget<kBf16>(a[u]);
-    to_f32<kBf16>(a[u], v);
-    to_f32<kBf16>(wr[u], w);
     unsigned code;
-    const u32x2 out = scale_quantize(v, w, f, &code);
+    forget<kBf16>(a[u]);
+    const u32x2 out = scale_quantize<kBf16>(a[u], wr[u], f, &code);
     if (c < lanes) {
       q[base + c] = out;
       if ((c & 3) == 0) s[(base + c) >> 2] = (uint8_t)code;
@@ -262,13 +282,11 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_mx8_long(const void* x, const 
     to_f32<kBf16>(a, v);
     sum += squares(v);
   }
-  const double f = row_factor(sum_row<1024>(sum, part), inv_k, eps);
+  const Factor f = row_factor(sum_row<1024>(sum, part), inv_k, eps);
   for (int64_t c = threadIdx.x; c < lanes; c += 1024) {
-    float v[8], w[8];
-    to_f32<kBf16>(load_raw<kBf16>(kRes ? r : x, base + c), v);  // what this thread itself stored
-    to_f32<kBf16>(load_raw<kBf16>(weight, c), w);
     unsigned code;
-    const u32x2 out = scale_quantize(v, w, f, &code);
+    const u32x2 out = scale_quantize<kBf16>(load_raw<kBf16>(kRes ? r : x, base + c),  // what this thread itself stored
+                                            load_raw<kBf16>(weight, c), f, &code);
     q[base + c] = out;
     if ((c & 3) == 0) s[(base + c) >> 2] = (uint8_t)code;
   }

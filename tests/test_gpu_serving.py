@@ -139,6 +139,24 @@ def test_norm_codes_next_to_midpoints(k, value):
     model.check_mx8(host(q), host(s), y, DELTA64, f"{k} x {value}")
 
 
+@pytest.mark.parametrize("k,value", [(32, 3.0), (64, 0.7), (544, 1.1), (2048, -5.3), (4128, 1e-3), (8192, 0.37),
+                                     (40000, 2.9)])
+def test_norm_codes_next_to_subnormal_midpoints(k, value):
+    """As above, at the midpoints (n + 1/2) 2^-9 of the codes below E4M3's normal
+    range, in blocks whose largest is well inside a binade or next to a power of
+    two (the scale then moves them by a binade)."""
+    rng = np.random.default_rng(k + 1)
+    x = np.full((1, k), value, dtype=np.float32)
+    f = norm_y(x.astype(np.float64), np.ones(k), 1e-5)[0]
+    target = (rng.integers(0, 8, size=k) + 0.5) * np.exp2(rng.choice([-11, -11, -12], size=k))
+    target *= rng.choice([1.0, -1.0], size=k)
+    target[::32] = np.where(np.arange(k // 32) % 2 == 0, 96.0, 64.0)  # scale 2^-2 or 2^-3
+    w = near_midpoints(rng, target, f)
+    q, s, _ = mxq.rmsnorm_quantize_fp8(dev(x), dev(w), eps=1e-5)
+    y = norm_y(x.astype(np.float64), w.astype(np.float64), 1e-5)
+    model.check_mx8(host(q), host(s), y, DELTA64, f"{k} x {value}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_norm_codes_of_many_rows(dtype):
     """A few million elements, compared as closely."""
