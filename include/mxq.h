@@ -345,7 +345,8 @@ MXQ_API mxq_status mxq_transfp4_dequantize(const uint8_t *q, const uint8_t *s,
  *   (q, s) = MXFP8 of y, scales and codes by the rule of mxq_quantize_fp8.
  * Squares and their sum are fp64, and so is the row's factor.  y is fp32, and
  * fp64 where a rounding boundary of a code or scale lies within 3 * 2^-23 of its
- * fp32 value, so the codes are rounded once, from a y of fp64 accuracy.
+ * fp32 value (or fp32 may have fewer bits than that), so the codes are rounded
+ * once, from a y of fp64 accuracy.
  * x, residual, r [rows][k] and weight [k] of type xdt; q [rows][k]; s
  * [rows][k/32].  r receives the sum and may be x or residual itself (in
  * place); with residual NULL it is not written and may be NULL.  q and s must

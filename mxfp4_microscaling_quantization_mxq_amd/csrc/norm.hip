@@ -12,9 +12,10 @@
 // row's factor is fp64, so neither leaves its range for finite rows (fp32 squares
 // do from 1.8e19).  y is formed in fp32, which decides its E4M3 code unless the
 // midpoint of two codes lies within 3 * 2^-23 of it; then, and where a block's
-// largest |y| is that close to a power of two (its scale), the wave's y are
-// formed again in fp64 and rounded to odd, so that one rounding to the code
-// remains.  (About 1 chunk of 64 lanes in 300 has such a lane.)
+// largest |y| is that close to a power of two (its scale) or below 2^-64, or
+// the factor below 2^-100, the wave's y are formed again in fp64 and rounded to
+// odd, so that one rounding to the code remains.  (About 1 chunk of 64 lanes in
+// 300 has such a lane.)
 //
 // Memory bound: x and residual are read once, r, q and s written once (7.03
 // bytes an element in bf16); the row stays in registers between the sum and
@@ -189,7 +190,9 @@ __device__ __forceinline__ u32x2 scale_quantize(Raw8<kBf16> r, Raw8<kBf16> weigh
   }
   const u32x2 out = mx8_convert8_f32(lo, c), other = mx8_convert8_f32(hi, c);
   *code = c;
-  const bool again = ((out.x ^ other.x) | (out.y ^ other.y)) != 0 || (top > 0x800000u && ((top + 3u) & 0x7FFFFFu) <= 6u);
+  // (a factor or a largest this small: fp32 may have fewer bits than that)
+  const bool again = ((out.x ^ other.x) | (out.y ^ other.y)) != 0 || f32 < 0x1p-100f ||
+                     (top != 0 && (top < 0x1F800000u || ((top + 3u) & 0x7FFFFFu) <= 6u));
   if (__builtin_amdgcn_ballot_w64(again) == 0) return out;
   const double f = refined(factor);
   forget<kBf16>(r);

@@ -157,6 +157,32 @@ def test_norm_codes_next_to_subnormal_midpoints(k, value):
     model.check_mx8(host(q), host(s), y, DELTA64, f"{k} x {value}")
 
 
+@pytest.mark.parametrize("eps", [1e-5, 1e-45])
+@pytest.mark.parametrize("k", [544, 8192, 32800])
+def test_norm_codes_at_the_ends_of_the_range(k, eps):
+    """Weights that put y next to midpoints, in rows whose factor is below fp32's
+    normal numbers, and with y that are."""
+    rng = np.random.default_rng(k + 2)
+    x = np.full((1, k), 3e38, dtype=np.float32)
+    f = norm_y(x.astype(np.float64), np.ones(k), eps)[0]
+    target = (1 + (2 * rng.integers(0, 8, size=k) + 1) / 16) * np.exp2(rng.integers(-6, 6, size=k))
+    target[::32] = 96.0
+    w = near_midpoints(rng, target, f)
+    q, s, _ = mxq.rmsnorm_quantize_fp8(dev(x), dev(w), eps=eps)
+    model.check_mx8(host(q), host(s), norm_y(x.astype(np.float64), w.astype(np.float64), eps), DELTA64, "factor")
+    # the smallest scale, 2^-127: codes from 2^-6 (normal) and (n + 1/2) 2^-9 on,
+    # where fp32 has 17 bits and fewer
+    x = np.ones((1, k), dtype=np.float32)
+    x[0, 7] = 3e38
+    f = norm_y(x.astype(np.float64), np.ones(k), eps)[0]
+    target = (1 + (2 * rng.integers(0, 8, size=k) + 1) / 16) * np.exp2(rng.integers(-133, -131, size=k))
+    target[1::3] = (rng.integers(0, 8, size=target[1::3].size) + 0.5) * 2.0 ** -136
+    w = near_midpoints(rng, target, f)
+    w[7] = 1.0
+    q, s, _ = mxq.rmsnorm_quantize_fp8(dev(x), dev(w), eps=eps)
+    model.check_mx8(host(q), host(s), norm_y(x.astype(np.float64), w.astype(np.float64), eps), DELTA64, "y")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_norm_codes_of_many_rows(dtype):
     """A few million elements, compared as closely."""
