@@ -214,8 +214,8 @@ __device__ __forceinline__ float sum_groups(float v) {
 // Stores four elements of the output.
 __device__ __forceinline__ void store_out(const AttendArgs& a, int64_t at, f32x4 o) {
   if (a.bf16_out) {
-    const unsigned x0 = f32_to_bf16_rne(o[0]) | ((unsigned)f32_to_bf16_rne(o[1]) << 16);
-    const unsigned x1 = f32_to_bf16_rne(o[2]) | ((unsigned)f32_to_bf16_rne(o[3]) << 16);
+    const unsigned x0 = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)o[0], (__bf16)o[1]});
+    const unsigned x1 = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)o[2], (__bf16)o[3]});
     *(u32x2*)((uint16_t*)a.out + at) = (u32x2){x0, x1};
   } else {
     *(f32x4*)((float*)a.out + at) = o;
@@ -225,7 +225,8 @@ __device__ __forceinline__ void store_out(const AttendArgs& a, int64_t at, f32x4
 // Partial results of one unit: m is in units of the scores' log2.
 // o = sum_t 2^(x_t - m) V_t and sum likewise -> the output, with the head's sink.
 __device__ __forceinline__ f32x4 finish(const AttendArgs& a, int64_t hq, float m, float sum, f32x4 o) {
-  if (!(m > -INFINITY)) return (f32x4){0, 0, 0, 0};  // nothing visible
+  // Nothing visible.  (Scores that are all NaN leave m there too, and a NaN sum.)
+  if (!(m > -INFINITY) && sum == 0) return (f32x4){0, 0, 0, 0};
   if (a.sinks) {
     const float sk = a.sinks[hq] * kLog2e, top = fmaxf(m, sk), f = __builtin_amdgcn_exp2f(m - top);
     sum = sum * f + __builtin_amdgcn_exp2f(sk - top);

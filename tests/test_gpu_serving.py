@@ -433,6 +433,56 @@ def e2m1_step(i):
     return 2 | (i & 1), 17 + (i >> 1)
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("width,lens", [(40, [600, 0, 33]), (300, [4000, 0, 33])])  # one block a unit; ranges and join
+def test_attention_nan_is_not_hidden(width, lens, out):
+    """A NaN in a head's query, in a visible key or value, or in a head's sink
+    gives NaN where it belongs and nowhere else; a sequence with nothing visible
+    gives zeros all the same."""
+    heads, group, d, page = 2, 4, 64, 16
+    rng = np.random.default_rng(width)
+    cache = filled_cache(rng, width, page, heads, d, "mxfp8")
+    pages = rng.permutation(width).astype(np.int32)
+    table = np.stack([pages] * 3)
+    n = np.array(lens, dtype=np.int32)
+    q, _ = stored(rng.standard_normal((3, heads * group, d)), "bf16")
+    sinks = rng.standard_normal(heads * group).astype(np.float32)
+
+    def call(qb=q, c=cache, sk=None):
+        y = mxq.paged_attention(dev(qb), on_device(c), dev(table), dev(n), sinks=None if sk is None else dev(sk),
+                                out_dtype=out)
+        return oracle.to_f64(host(y))
+
+    clean, clean_sinks = call(), call(sk=sinks)
+    assert np.isfinite(clean).all() and not clean[1].any()
+    bad = q.copy()
+    bad[:, 3, :] = 0x7FC0
+    bad[:, 6, 17] = 0xFFC0
+    for y, ref in ((call(bad), clean), (call(bad, sk=sinks), clean_sinks)):
+        for h in range(heads * group):
+            for b in (0, 2):
+                assert np.isnan(y[b, h]).all() if h in (3, 6) else np.array_equal(y[b, h], ref[b, h]), (b, h)
+        assert not y[1].any()
+    last = int(table[0, 20 // page])  # token 20: visible to both sequences
+    c = [a.copy() for a in cache]
+    c[0][last, 1, 20 % page, 5] = 0x7F  # a key of cache head 1
+    y = call(c=c)
+    assert np.array_equal(y[:, :group], clean[:, :group]) and np.isnan(y[[0, 2], group:]).all() and not y[1].any()
+    c = [a.copy() for a in cache]
+    c[2][last, 0, 20 % page, 9] = 0xFF  # a value of cache head 0
+    y = call(c=c)
+    assert np.isnan(y[[0, 2], :group, 9]).all() and not y[1].any()
+    y[[0, 2], :group, 9] = clean[[0, 2], :group, 9]
+    assert np.array_equal(y, clean)
+    for bits in (0x7FC00000, 0x7FFFFFFF):
+        sk = sinks.copy()
+        sk.view(np.uint32)[2] = bits
+        y = call(sk=sk)
+        assert np.isnan(y[[0, 2], 2]).all() and not y[1].any()
+        y[[0, 2], 2] = clean_sinks[[0, 2], 2]
+        assert np.array_equal(y, clean_sinks)
+
+
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
 def test_attention_weights_survive_other_heads_rising_maxima(fmt):
     """One query head's maximum rises tile after tile; the others have theirs
