@@ -61,7 +61,6 @@ struct AttendParams {
   AttendArgs a;
   KvShape c;
   unsigned group;        // query heads per cache head
-  unsigned tiles16;      // head tiles of 16 per cache head
   unsigned tile_groups;  // units per sequence and cache head
   unsigned block_tiles;  // head tiles of a unit: 1, 2 or 4
   // Workspace: for each unit that spans blocks, {its parts, the block that
@@ -721,7 +720,6 @@ hipError_t launch_attend(const AttendArgs& a, const KvShape& c, bool fp4, void* 
   p.a = a;
   p.c = c;
   p.group = a.q_heads / c.heads;
-  p.tiles16 = (unsigned)head_tiles(a.q_heads, c);
   p.tile_groups = (unsigned)tile_groups(a.q_heads, c);
   p.block_tiles = (unsigned)unit_tiles16(a.q_heads, c);
   const int64_t blocks = attend_blocks(a.batch, a.q_heads, c, fp4, a.table_width, a.window);
