@@ -303,15 +303,20 @@ void launch_norm(const void* x, const void* residual, const void* weight, int64_
 #define MXQ_NORM(T, U)                                                                                             \
   k_rmsnorm_mx8<kBf16, kRes, T, U><<<dim3((unsigned)(T == 64 ? (rows + 3) / 4 : rows)), dim3(T == 64 ? 256 : T), 0, \
                                      st>>>(x, residual, weight, rows, k, 1.0 / (double)k, eps, r, q2, s)
-  if (lanes <= 64) MXQ_NORM(64, 1);
-  else if (lanes <= 128) MXQ_NORM(64, 2);
-  else if (lanes <= 256) MXQ_NORM(256, 1);
-  else if (lanes <= 512) MXQ_NORM(256, 2);
   // Without a residual a block of 512 has half the bytes on their way, and
   // twice the blocks of 256 do better once there are enough rows: 16384 x 8192
   // bf16 83 -> 77 us (with a residual even, 152 us; 64 rows 4.0 us with 512
   // threads, 4.4 with 256).
-  else if (lanes <= 1024 && !kRes && rows >= 1024) MXQ_NORM(256, 4);
+  if constexpr (!kRes) {
+    if (lanes > 512 && lanes <= 1024 && rows >= 1024) {
+      MXQ_NORM(256, 4);
+      return;
+    }
+  }
+  if (lanes <= 64) MXQ_NORM(64, 1);
+  else if (lanes <= 128) MXQ_NORM(64, 2);
+  else if (lanes <= 256) MXQ_NORM(256, 1);
+  else if (lanes <= 512) MXQ_NORM(256, 2);
   else if (lanes <= 1024) MXQ_NORM(512, 2);
   else if (lanes <= 2048) MXQ_NORM(1024, 2);
   else if (lanes <= 4096) MXQ_NORM(1024, 4);
