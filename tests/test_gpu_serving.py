@@ -198,6 +198,20 @@ def test_norm_codes_of_many_rows(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_nan_and_infinity_reach_the_product(dtype):
+    """Outside the contract, but not hidden: a NaN in a row gives NaN codes in all of
+    it, an infinity a NaN code of its element, and gemm_w4a8 of them is NaN."""
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((4, 512))
+    x[1, 7], x[2, 9] = np.nan, np.inf
+    a, _ = stored(x, dtype)
+    q, s, _ = mxq.rmsnorm_quantize_fp8(dev(a), dev(stored(np.ones(512), dtype)[0]))
+    assert ((host(q)[1] & 0x7F) == 0x7F).all() and host(q)[2, 9] & 0x7F == 0x7F
+    c = mxq.gemm_w4a8(q, s, *mxq.quantize(dev(rng.standard_normal((64, 512)).astype(np.float32))), torch.float32)
+    assert torch.isnan(c[1:3]).all() and torch.isfinite(c[[0, 3]]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("k", [96, 4128, 40000])
 def test_norm_in_place(dtype, k):
     rng = np.random.default_rng(k)
@@ -560,6 +574,114 @@ def test_attention_ranges(seed, batch, most, heads, group, d, page, fmt):
     for sinks in (False, True):
         attend_case(seed, lens, heads, group, d, page, fmt, torch.bfloat16 if seed % 2 else torch.float32,
                     sinks=sinks, extra_width=4096 // page)
+
+
+def uneven(rng, batch, tiles):
+    """Lengths of `batch` sequences, `tiles` tiles of 32 tokens together, the first,
+    a middle and the last one empty."""
+    n = rng.multinomial(tiles, rng.dirichlet(np.full(batch - 3, 2.0)))
+    lens = [int(t) * 32 - int(rng.integers(0, 32)) if t else 0 for t in n]
+    return [0] + lens[:batch // 2] + [0] + lens[batch // 2:] + [0]
+
+
+def long_case(seed, lens, heads, group, d, page, fmt, out, per, window=0, sinks=False, check=8):
+    """A batch whose blocks take ranges of `per` tiles.  Sequences share pages of a
+    pool; the pages where the visible positions begin and end are a sequence's own,
+    with NaN around them, and the entries before name a page of NaN."""
+    rng = np.random.default_rng(seed)
+    batch, pool = len(lens), 48
+    starts = [max(0, n - window) if window else 0 for n in lens]
+    total = sum(-(-n // 32) - a // 32 for n, a in zip(lens, starts)) * heads * -(-group // 64)
+    blocks = 512 if (d if fmt == "mxfp8" else d // 2) >= 128 else 1024
+    assert max(-(-total // blocks), 4) == per, (total, blocks)
+    cache = filled_cache(rng, pool + 1 + 2 * batch, page, heads, d, fmt)
+    table = np.full((batch, max(-(-n // page) for n in lens) + 1), -1, dtype=np.int32)
+    dead = np.zeros((cache[0].shape[0], page), dtype=bool)
+    dead[pool] = True
+    for b, (n, a) in enumerate(zip(lens, starts)):
+        if n == 0:
+            continue
+        first, last = a // page, (n - 1) // page
+        table[b, :first] = pool
+        table[b, first:last + 1] = rng.integers(0, pool, size=last + 1 - first)
+        for own, p in ((pool + 1 + 2 * b, first), (pool + 2 + 2 * b, last)):
+            table[b, p] = own
+            t = p * page + np.arange(page)
+            dead[own] = (t < a) | (t >= n)
+        table[b, last + 1:] = pool
+    kq, ks, vq, vs = cache
+    for c in (kq, vq):
+        c.transpose(0, 2, 1, 3)[dead] = NAN_BYTES[fmt]
+    ks.transpose(0, 2, 1, 3)[dead] = 255
+    vs.transpose(0, 3, 1, 2)[dead] = 255
+    qb, q64 = stored(rng.standard_normal((batch, heads * group, d)), "bf16")
+    sk = rng.standard_normal(heads * group).astype(np.float32) * 2 if sinks else None
+    y = mxq.paged_attention(dev(qb), on_device(cache), dev(table), dev(np.array(lens, dtype=np.int32)), window=window,
+                            sinks=dev(sk) if sinks else None, out_dtype=out)
+    got = oracle.to_f64(host(y))
+    rows = lambda q, s: model.dequantize_rows(np.ascontiguousarray(q).reshape(-1, q.shape[-1]),  # noqa: E731
+                                              np.ascontiguousarray(s).reshape(-1, d // 32), fmt).reshape(
+                                                  -1, heads, page, d)
+    kd, vd = rows(kq, ks), rows(vq, vs.transpose(0, 1, 3, 2))
+    for b in sorted({0, batch - 1, int(np.argmax(lens)), *rng.choice(batch, size=min(check, batch), replace=False)}):
+        n, a = lens[b], starts[b]
+        if n == 0:
+            assert not got[b].any(), b
+            continue
+        t = np.arange(a, n)
+        at = table[b, t // page], slice(None), t % page
+        k, v = kd[at], vd[at]  # [tokens, heads, d]
+        for h in range(heads):
+            q = q64[b, h * group:(h + 1) * group]
+            x = k[:, h] @ q.T / np.sqrt(d)
+            mag = (np.abs(k[:, h]) @ np.abs(q).T / np.sqrt(d)).max(axis=0)
+            top = x.max(axis=0)
+            extra = 0.0
+            if sinks:
+                sh = sk[h * group:(h + 1) * group].astype(np.float64)
+                top = np.maximum(top, sh)
+                extra = np.exp(sh - top)
+            p = np.exp(x - top)
+            den = (p.sum(axis=0) + extra)[:, None]
+            ref, size = p.T @ v[:, h] / den, p.T @ np.abs(v[:, h]) / den
+            bound = size * (2 * (d + 4) * U * mag[:, None] + 2.0 ** -21 + ((n - a) / 8 + 64) * U)
+            if out == torch.bfloat16:
+                bound = bound + size * 2.0 ** -16
+                bound = bound + (np.abs(ref) + bound) * 2.0 ** -8
+            bad = ~(np.abs(got[b, h * group:(h + 1) * group] - ref) <= bound)
+            assert not bad.any(), (b, n, h, int(bad.sum()))
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt,d,per,heads,group,batch,page", [
+    ("mxfp8", 128, 37, 2, 8, 40, 64),
+    ("mxfp4", 128, 41, 8, 8, 23, 32),   # 1024 ranges, three terms of P with fp32 output
+    ("mxfp4", 64, 101, 4, 4, 9, 16),
+    ("mxfp8", 64, 45, 2, 70, 30, 128),  # two units a cache head, one wave a head tile
+    ("mxfp8", 256, 37, 1, 16, 300, 16),  # more sequences than threads of a block
+    ("mxfp4", 256, 53, 3, 20, 12, 64)])  # two head tiles a unit
+def test_attention_long_ranges(fmt, d, per, heads, group, batch, page, out):
+    """Ranges of many tiles a wave, with cuts inside sequences of uneven lengths."""
+    rng = np.random.default_rng(per)
+    blocks = 512 if (d if fmt == "mxfp8" else d // 2) >= 128 else 1024
+    lens = uneven(rng, batch, per * blocks // (heads * -(-group // 64)) - 3)
+    long_case(per, lens, heads, group, d, page, fmt, out, per)
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("fmt,d,window,most,heads,group,batch,page,per", [
+    ("mxfp8", 128, 3000, 20000, 4, 8, 40, 64, 28),
+    ("mxfp4", 64, 1500, 9000, 2, 4, 5, 16, 4),
+    ("mxfp8", 64, 5001, 30000, 8, 2, 32, 32, 38),
+    ("mxfp4", 256, 2111, 4000, 1, 16, 3, 128, 4)])
+def test_attention_window_over_ranges(fmt, d, window, most, heads, group, batch, page, per, sinks):
+    """Windows past 1024 positions on longer sequences: the ranges begin inside a
+    sequence's pages and are cut and joined."""
+    rng = np.random.default_rng(window)
+    lens = [int(n) for n in rng.integers(window // 2, most, size=batch)]
+    lens[0], lens[-1] = most, window + 1
+    lens[batch // 2] = 0
+    long_case(window, lens, heads, group, d, page, fmt, torch.bfloat16 if sinks else torch.float32, per, window, sinks)
 
 
 @pytest.mark.parametrize("seed", range(16))
