@@ -41,10 +41,10 @@ __device__ __forceinline__ Raw8<kBf16> load_raw(const void* p, int64_t c) {
   return r;
 }
 // Streams (x, residual and r are touched once; times of variants in turn, in
-// one graph's replays): in bf16 with the streaming hint (16384 x 8192: 172 ->
-// 164 us; the codes are stored plainly, 161 -> 155 us).  An fp32 lane takes
+// one graph's replays): in bf16 with the streaming hint (16384 x 8192: 168 ->
+// 156 us; the codes are stored plainly, 161 with the hint).  An fp32 lane takes
 // its 32 bytes in two instructions, and the hint makes those slower (8192 x
-// 8192: 162 -> 180 us), so they are plain.
+// 8192: 163 -> 181 us), so they are plain.
 template <bool kBf16>
 __device__ __forceinline__ Raw8<kBf16> load_raw_stream(const void* p, int64_t c) {
   if constexpr (!kBf16) return load_raw<kBf16>(p, c);
@@ -148,8 +148,8 @@ __device__ __forceinline__ double squares(const float (&v)[8]) {
 }
 
 // 1 / sqrt(m), m = sum / k + eps: f within 2^-40, the fp32 reciprocal root and
-// one Newton step in fp64 (the library's divide and root take over a microsecond
-// of the row's latency), or in full where m leaves fp32's range.
+// one Newton step in fp64 (1 x 8192 3.23 us, 3.29 with the library's root and
+// divide), or in full where m leaves fp32's range.
 struct Factor {
   double f, m;
 };
@@ -178,7 +178,10 @@ __device__ __forceinline__ u32x2 scale_quantize(Raw8<kBf16> r, Raw8<kBf16> weigh
   to_f32<kBf16>(weight, w);
 #pragma unroll
   for (int i = 0; i < 8; i++) y[i] = v[i] * f32 * w[i];
-  const unsigned top = quad_max(f32x8_absmax_bits(y)), c = e8m0_code_e4m3(top >> 23);
+  float big = 0;  // (in fp32: the instruction takes magnitudes of three; a NaN stays)
+#pragma unroll
+  for (int i = 0; i < 8; i++) big = __builtin_elementwise_maximum(big, __builtin_fabsf(y[i]));
+  const unsigned top = quad_max(__float_as_uint(big)), c = e8m0_code_e4m3(top >> 23);
   // clamped to 8 units below 448 * 2^e, so that 1 + d times it is below that
   const float lim = __uint_as_float(mx8_limit_bits(c) - 8u);
   float lo[8], hi[8];
@@ -215,8 +218,11 @@ __device__ __forceinline__ u32x2 scale_quantize(Raw8<kBf16> r, Raw8<kBf16> weigh
 // One row by T threads with U chunks of 8 elements each (k <= 8 T U): T = 64
 // puts four rows into a block, one a wave.  Lanes of a chunk past k hold zeros
 // and store nothing (skipping their waves measured slower where there are
-// none); k % 32 == 0 keeps the quads of a block whole.  Measured: 16384 x 8192
-// bf16 with residual 144 us (6.6 TB/s), 1 x 8192 2.9 us.
+// none); k % 32 == 0 keeps the quads of a block whole.  Measured (medians of a
+// kernel trace): 16384 x 8192 bf16 with residual 148 us (6.4 TB/s), 8192 x 8192
+// fp32 159, 1 x 8192 3.1.  The fp64 squares and the interval of y cost 2 % of the
+// first and 0.2 us of the last (156 against 153 and 3.23 against 3.05 us in one
+// graph's replays, fp32 even).
 template <bool kBf16, bool kRes, int T, int U>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void k_rmsnorm_mx8(const void* x, const void* residual,
                                                                    const void* __restrict__ weight, int64_t rows,
@@ -305,8 +311,8 @@ void launch_norm(const void* x, const void* residual, const void* weight, int64_
                                      st>>>(x, residual, weight, rows, k, 1.0 / (double)k, eps, r, q2, s)
   // Without a residual a block of 512 has half the bytes on their way, and
   // twice the blocks of 256 do better once there are enough rows: 16384 x 8192
-  // bf16 83 -> 77 us (with a residual even, 152 us; 64 rows 4.0 us with 512
-  // threads, 4.4 with 256).
+  // bf16 85 -> 77 us, 1024 rows even (8.4 and 8.5), 64 rows 3.5 us with 512
+  // threads, 3.8 with 256.  (With a residual even, 156 and 155 us.)
   if constexpr (!kRes) {
     if (lanes > 512 && lanes <= 1024 && rows >= 1024) {
       MXQ_NORM(256, 4);
