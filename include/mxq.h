@@ -404,7 +404,8 @@ MXQ_API mxq_status mxq_kv_read(const uint8_t *kq, const uint8_t *ks, const uint8
  * [q_heads] or NULL; out [batch][q_heads][head_dim] of type odt.  head_dim
  * 64, 128 or 256; q_heads a multiple of kv_heads; scale finite.  Scores,
  * probabilities and sums are fp32 (probabilities enter their product as two
- * bf16 terms).
+ * bf16 terms for bf16 output, 2^-17 of them, and three for fp32 output, 2^-25).
+ * A NaN among a head's visible scores gives NaN.
  * The length is split over blocks whose partial results go to `workspace`
  * (16-byte aligned, at least the bytes that mxq_paged_attention_workspace
  * gives for the same sizes; may be NULL for 0).  Its content need not be

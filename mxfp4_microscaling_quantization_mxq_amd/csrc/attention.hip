@@ -30,8 +30,8 @@
 // Memory bound: the cache is read once (2 x 1.03 bytes a token, head and
 // element in MXFP8, 2 x 0.53 in MXFP4).  64 query heads over 8, D = 128, medians
 // of a kernel trace, without the join's 4 to 7 us: 64 sequences of 8192 tokens
-// in MXFP8 174 us (6.4 TB/s), 1 of 131072 47 (5.9), 32 of 24000 in MXFP4 168
-// (5.0).
+// in MXFP8 177 us (6.3 TB/s; 181 with fp32 output), 1 of 131072 47 (5.9), 32 of
+// 24000 in MXFP4 159 (5.3; 176).
 //
 // Split.  A unit is one sequence and one cache head (and up to 64 of its query
 // heads); its work is its visible tiles.  The tiles of all units, in order,
@@ -79,9 +79,10 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // The arguments of a kernel whose only argument is p.  With kAgain they are read
 // again at each call: what only one phase of the kernel uses then occupies no
 // scalar register in the others (the tile loop's resources take most of them,
-// and scalars that do not fit are kept in vector registers).  The kernel of
-// ranges is 3 % faster with it on MXFP4, that of units, which has fewer phases,
-// 8-25 % slower (the loop waits for scalar loads it would have kept).
+// and scalars that do not fit are kept in vector registers).  The kernels of
+// ranges keep 15 such scalars for 57 to 66 without it (their times differ by less
+// than two runs of one build do); that of units, which has fewer phases, is 4-29 %
+// slower with it (the loop waits for scalar loads it would have kept).
 template <bool kAgain>
 __device__ __forceinline__ const AttendParams& args(const AttendParams& p) {
   if constexpr (!kAgain) return p;
@@ -679,12 +680,12 @@ static int64_t most_tiles(const KvShape& c, int64_t table_width, int64_t window)
 // one block longer than the join of its parts takes, which is a second launch
 // (4 us of GPU time and 4 us of the host's).  A block needs about 1 us for 4
 // tiles, and the more units there are, the longer the others take anyway.  64
-// query heads over 8, D = 128, MXFP8, ranges / units in a graph's replays: 1 sequence of
-// 500 tokens (16 tiles, 8 units) 10.4 / 7.8 us, of 1000 9.8 / 11.2 (16.2 / 11.6
-// with the launches); 8 of 700-1000 (32 tiles, 64 units) 16.5 / 12.0; 16 of
-// 1500-2000 (63 tiles, 128 units) 24.0 / 21.5, 64 53.9 / 46.5; 16 of 1000-4000
-// 27.4 / 36.2, 64 73 / 75.  (Eight waves a unit measured slower: 64 sequences
-// of 300-500 19.1 against 15.1.)
+// query heads over 8, D = 128, MXFP8, ranges / units in a graph's replays: 1
+// sequence of 500 tokens (16 tiles, 8 units) 9.2 / 7.7 us, of 1000 9.7 / 11.8
+// (but two launches); 8 of 700-1000 (32 tiles, 64 units) 15.5 / 11.8; 16 of
+// 1500-2000 (63 tiles, 128 units) 23.0 / 21.4, 64 53.5 / 45.7; 16 of 1000-4000
+// 27.1 / 35.4, 64 72 / 75; D = 64, 97 of 0-3999 with a window of 128 16.5 / 8.7,
+// in MXFP4 16.3 / 8.3.
 static bool attend_ranges(int64_t units, int64_t tiles) { return tiles > (units >= 128 ? 64 : 32); }
 
 int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp4, int64_t table_width,

@@ -38,11 +38,11 @@ __device__ __forceinline__ KvBlock kv_block(const KvShape& c) {
 // block, quantized by the functions the quantizers use, so the codes are those
 // of mxq_quantize / mxq_quantize_fp8.  A quad's lanes share the token, so
 // skipping a slot keeps quads whole.  Measured: 16384 tokens x 8 heads x 128
-// from a fused projection of 10240 bf16 into MXFP8 pages of 64: 23.0 us (4.4
+// from a fused projection of 10240 bf16 into MXFP8 pages of 64: 23.1 us (4.4
 // TB/s, median of a kernel trace).  Variants in turn, in one graph's replays:
-// 20.8 as it is, 26.1 with a token's heads side by side in a block, 22.0 with
-// four chunks a block, 21.0 without any scale store, so the scattered bytes of
-// vs cost nothing.
+// 23.5 as it is, 26.6 with a token's heads side by side in a block, 22.5 with
+// four chunks a block, 23.2 without any scale store, so the scattered
+// bytes of vs cost next to nothing.
 template <bool kBf16, bool kFp4>
 __global__ __launch_bounds__(256) void k_kv_append(const void* __restrict__ k, int64_t k_stride,
                                                    const void* __restrict__ v, int64_t v_stride,
@@ -82,10 +82,10 @@ __global__ __launch_bounds__(256) void k_kv_append(const void* __restrict__ k, i
 }
 
 // One lane = 8 elements of one token's head.  A slot outside the cache reads
-// as zeros.  32768 tokens x 8 heads x 128 to bf16: MXFP8 31.2 us (6.5 TB/s),
-// MXFP4 26.2 (medians of a kernel trace).  Variants in turn, in one graph's
-// replays: 34.3 and 29.6 as it is, one chunk a block 37.4 and 33.8, plain
-// output stores 47.2 and 34.2.
+// as zeros.  32768 tokens x 8 heads x 128 to bf16: MXFP8 31.0 us (6.5 TB/s),
+// MXFP4 26.5 (medians of a kernel trace).  Variants in turn, in one graph's
+// replays: 35.3 and 30.1 as it is, one chunk a block 38.5 and 34.3, plain
+// output stores 49.0 and 30.7.
 template <bool kBf16, bool kFp4, int U>
 __global__ __launch_bounds__(256) void k_kv_read(const uint8_t* __restrict__ kq, const uint8_t* __restrict__ ks,
                                                  const uint8_t* __restrict__ vq, const uint8_t* __restrict__ vs,

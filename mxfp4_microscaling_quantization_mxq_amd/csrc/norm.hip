@@ -220,7 +220,7 @@ __device__ __forceinline__ u32x2 scale_quantize(Raw8<kBf16> r, Raw8<kBf16> weigh
 // and store nothing (skipping their waves measured slower where there are
 // none); k % 32 == 0 keeps the quads of a block whole.  Measured (medians of a
 // kernel trace): 16384 x 8192 bf16 with residual 148 us (6.4 TB/s), 8192 x 8192
-// fp32 159, 1 x 8192 3.1.  The fp64 squares and the interval of y cost 2 % of the
+// fp32 158, 1 x 8192 3.0.  The fp64 squares and the interval of y cost 2 % of the
 // first and 0.2 us of the last (156 against 153 and 3.23 against 3.05 us in one
 // graph's replays, fp32 even).
 template <bool kBf16, bool kRes, int T, int U>
