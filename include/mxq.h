@@ -387,6 +387,34 @@ MXQ_API mxq_status mxq_kv_read(const uint8_t *kq, const uint8_t *ks, const uint8
                        mxq_dtype dt, hipStream_t stream);
 
 /*
+ * Rotation of new queries and keys by their positions, with the write of keys
+ * and values into the paged cache.  A head's first 2 * pairs elements are
+ * `pairs` pairs, (i, pairs + i), or (2 i, 2 i + 1) with interleaved != 0; pair i
+ * of token t turns by angle = p * freqs[i] (radians):
+ *   (a, b) -> (a cos - b sin, b cos + a sin).
+ * The other elements stay.  p is positions[t], or, with position_axes > 1
+ * axes (positions [position_axes][tokens]), positions[axes[i] * tokens + t]; an
+ * entry of axes past the last axis names the last one.  axes is NULL for one axis.
+ * q_out receives the rotated queries, rounded to bf16; keys are quantized into
+ * their slots from the rotated values (cos, sin and keys in fp64, so the codes
+ * are rounded once), values as mxq_kv_append writes them.  Queries of tokens
+ * whose slot is skipped are rotated all the same.
+ * q, k, v of type dt: row t at q + t * q_stride elements, [q_heads][head_dim]
+ * contiguous inside a row, k and v likewise with kv_heads (strides multiples of
+ * 8, at least a row); positions int64, freqs fp32 [pairs], axes u8 [pairs];
+ * slots and the cache as mxq_kv_append; q_out bf16 [tokens][q_heads][head_dim],
+ * which must not overlap q, k or v (refused).  pairs a multiple of 8, 2 * pairs
+ * <= head_dim <= 512; q_heads * head_dim <= 2^20; tokens <= 2^22; position_axes
+ * 1 to 256.  An angle of 2^40 or more, or not finite, gives NaN.
+ */
+MXQ_API mxq_status mxq_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, mxq_dtype dt, const int64_t *positions, int64_t position_axes,
+                           const uint8_t *axes, const float *freqs, int64_t pairs, int interleaved,
+                           const int64_t *slots, int64_t tokens, int64_t q_heads, int64_t pages, int64_t kv_heads,
+                           int64_t page_size, int64_t head_dim, mxq_format fmt, uint8_t *kq, uint8_t *ks,
+                           uint8_t *vq, uint8_t *vs, void *q_out, hipStream_t stream);
+
+/*
  * Attention of one new token per sequence over the paged cache (which holds
  * that token already).  For each sequence b and query head h, with cache head
  * h / (q_heads / kv_heads) and t over the visible positions

@@ -22,6 +22,10 @@ and, between the products of a served model's decode step:
     o = paged_attention(q, cache, table, lens)       # one new token per sequence
     k, v = kv_read(cache, slots)                     # read slots back
 
+or, for tokens with positions and for drafted tokens that one step checks:
+
+    q = rope_append(cache, q, k, v, slots, positions, freqs)   # rotate, quantize new tokens into their slots
+
 Every tensor argument is checked before anything is enqueued: dtype, shape
 (scales and caller-supplied outputs must match the operands exactly),
 contiguity, and that it lives on the operands' device; the NVFP4 tensor
@@ -53,6 +57,7 @@ API = (
     "mxq_dequantize", "mxq_gemv_w4a16", "mxq_gemm_w4a4", "mxq_gemm_w4a4_quant", "mxq_gemm_w4a4_dynamic",
     "mxq_gemm_w4a8", "mxq_gemm_w4a8_dynamic", "nvq_quantize", "nvq_dequantize", "nvq_gemm", "mxq_transfp4_quantize", "mxq_transfp4_dequantize",
     "mxq_rmsnorm_quantize_fp8", "mxq_kv_append", "mxq_kv_read", "mxq_paged_attention_workspace", "mxq_paged_attention",
+    "mxq_rope_append",
 )
 
 
@@ -103,6 +108,8 @@ def capi() -> ctypes.CDLL:
     lib.mxq_paged_attention_workspace.argtypes = [I64, I64, I64, I64, I64, I64, I64, ctypes.POINTER(I64)]
     lib.mxq_paged_attention.argtypes = [P, I64, P, P, P, P, P, I64, I64, P, P, I64, I64, I64, I64, I64, I64, I, F,
                                         I64, P, I64, P, I, P]
+    lib.mxq_rope_append.argtypes = [P, I64, P, I64, P, I64, I, P, I64, P, P, I64, I, P, I64, I64, I64, I64, I64, I64, I,
+                                    P, P, P, P, P, P]
     for name in API[2:]:
         getattr(lib, name).restype = I
     _lib = lib
@@ -648,6 +655,61 @@ def kv_append(cache, k, v, slots):
     _check(capi().mxq_kv_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, _dtype_code(k.dtype),
                                 slots.data_ptr(), n, pages, heads, page, d, fmt, kq.data_ptr(), ks.data_ptr(),
                                 vq.data_ptr(), vs.data_ptr(), _stream(dev)), "mxq_kv_append")
+
+
+def rope_append(cache, q, k, v, slots, positions, freqs, axes=None, interleaved=False, out=None):
+    """Rotate new queries and keys by their positions and quantize keys and
+    values into their slots (as kv_append, from the rotated keys, rounded once).
+    Returns the rotated queries, bf16 [tokens, q_heads, head_dim].
+
+    q [tokens, q_heads, head_dim], k, v [tokens, kv_heads, head_dim], all bf16 or
+    all fp32, row strides free; slots int64 [tokens] (outside the cache, e.g. -1:
+    not written); positions int64 [tokens]; freqs fp32 [n], radians a position: a
+    head's first 2 n elements turn in pairs (i, n + i), or (2 i, 2 i + 1) if
+    interleaved; n % 8 == 0.  With several position axes (time, height, width),
+    positions is [axes, tokens] and axes uint8 [n] names the axis of each pair.
+    out must not overlap q, k or v."""
+    torch = _torch()
+    dev = _index(cache[0])
+    pages, heads, page, d, fmt = _cache(cache, dev)
+    q_stride = _rows(q, "q", _floats(), None, d)
+    k_stride = _rows(k, "k", (q.dtype,), heads, d)
+    v_stride = _rows(v, "v", (q.dtype,), heads, d)
+    n, q_heads, _ = q.shape
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ValueError(f"q has {n} tokens, k {k.shape[0]}, v {v.shape[0]}")
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1 or not _same(freqs, torch.float32, freqs.shape, dev):
+        _need(freqs, "freqs", torch.float32, ndim=1)
+    pairs = freqs.shape[0]
+    if axes is None:
+        count = 1
+        if not _same(positions, torch.int64, (n,), dev):
+            _need(positions, "positions", torch.int64, (n,))
+    else:
+        if not isinstance(positions, torch.Tensor) or positions.dim() != 2 or positions.shape[0] < 2:
+            raise ValueError("with axes, positions must have shape [2 or more axes, tokens]")
+        count = positions.shape[0]
+        if not _same(positions, torch.int64, (count, n), dev) or not _same(axes, torch.uint8, (pairs,), dev):
+            _need(positions, "positions", torch.int64, (count, n))
+            _need(axes, "axes", torch.uint8, (pairs,))
+    if not _same(slots, torch.int64, (n,), dev):
+        _need(slots, "slots", torch.int64, (n,))
+    if out is None:
+        out = q.new_empty((n, q_heads, d), dtype=torch.bfloat16)
+    else:
+        _need(out, "out", torch.bfloat16, (n, q_heads, d))
+    on = (q, k, v, slots, positions, freqs, out) if axes is None else (q, k, v, slots, positions, freqs, out, axes)
+    if dev < 0 or any(t.get_device() != dev for t in on):
+        names = ("q", "k", "v", "slots", "positions", "freqs", "out", "axes")
+        _on_device(kq=cache[0], **dict(zip(names, on)))
+    kq, ks, vq, vs = cache
+    _check(capi().mxq_rope_append(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                                  _dtype_code(q.dtype), positions.data_ptr(), count,
+                                  None if axes is None else axes.data_ptr(), freqs.data_ptr(), pairs,
+                                  int(bool(interleaved)), slots.data_ptr(), n, q_heads, pages, heads, page, d, fmt,
+                                  kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), out.data_ptr(),
+                                  _stream(dev)), "mxq_rope_append")
+    return out
 
 
 def kv_read(cache, slots, dtype=None, k=None, v=None):

@@ -331,6 +331,59 @@ mxq_status mxq_kv_read(const uint8_t* kq, const uint8_t* ks, const uint8_t* vq, 
       mxq::launch_kv_read(kq, ks, vq, vs, slots, tokens, c, fmt == MXQ_MXFP4, k, v, dt == MXQ_BF16, stream));
 }
 
+// Whether the n bytes at p and the m bytes at q have one in common.
+static bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  return (uintptr_t)p < (uintptr_t)q + (uintptr_t)m && (uintptr_t)q < (uintptr_t)p + (uintptr_t)n;
+}
+
+mxq_status mxq_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, mxq_dtype dt, const int64_t* positions, int64_t position_axes,
+                           const uint8_t* axes, const float* freqs, int64_t pairs, int interleaved,
+                           const int64_t* slots, int64_t tokens, int64_t q_heads, int64_t pages, int64_t kv_heads,
+                           int64_t page_size, int64_t head_dim, mxq_format fmt, uint8_t* kq, uint8_t* ks, uint8_t* vq,
+                           uint8_t* vs, void* q_out, hipStream_t stream) {
+  mxq::KvShape c;
+  if (!cache_shape(pages, kv_heads, page_size, head_dim, &c) || !valid_dtype(dt) || !valid_format(fmt))
+    return MXQ_ERROR_INVALID_VALUE;
+  if (head_dim > 512 || q_heads < 1 || q_heads > (1 << 20) / head_dim) return MXQ_ERROR_INVALID_VALUE;
+  if (pairs < 8 || pairs % 8 != 0 || pairs > head_dim / 2 || position_axes < 1 || position_axes > 256)
+    return MXQ_ERROR_INVALID_VALUE;
+  const int64_t q_row = q_heads * head_dim, row = kv_heads * head_dim;
+  if (tokens < 1 || tokens > (1 << 22) || q_stride < q_row || k_stride < row || v_stride < row || q_stride % 8 != 0 ||
+      k_stride % 8 != 0 || v_stride % 8 != 0)
+    return MXQ_ERROR_INVALID_VALUE;
+  if (tokens > kMaxElems / q_stride || tokens > kMaxElems / k_stride || tokens > kMaxElems / v_stride)
+    return MXQ_ERROR_INVALID_VALUE;
+  if (!q || !k || !v || !positions || !freqs || !slots || !q_out || (position_axes > 1) != (axes != nullptr))
+    return MXQ_ERROR_INVALID_VALUE;
+  const int64_t e = dt == MXQ_BF16 ? 2 : 4, out_bytes = 2 * tokens * q_row;
+  if (overlap(q_out, out_bytes, q, e * ((tokens - 1) * q_stride + q_row)) ||
+      overlap(q_out, out_bytes, k, e * ((tokens - 1) * k_stride + row)) ||
+      overlap(q_out, out_bytes, v, e * ((tokens - 1) * v_stride + row)))
+    return MXQ_ERROR_INVALID_VALUE;
+  mxq_status st = cache_pointers(kq, ks, vq, vs);
+  if (st != MXQ_SUCCESS) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || ((uintptr_t)slots & 7u) ||
+      ((uintptr_t)positions & 7u) || ((uintptr_t)freqs & 3u))
+    return MXQ_ERROR_MISALIGNED;
+  st = check_device();
+  if (st != MXQ_SUCCESS) return st;
+  mxq::RopeArgs a;
+  a.q = q, a.k = k, a.v = v;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.positions = positions;
+  a.axes = axes;
+  a.freqs = freqs;
+  a.slots = slots;
+  a.tokens = tokens;
+  a.position_axes = position_axes;
+  a.q_heads = (unsigned)q_heads;
+  a.pairs = (unsigned)pairs;
+  a.kq = kq, a.ks = ks, a.vq = vq, a.vs = vs;
+  a.q_out = (uint16_t*)q_out;
+  return launched(mxq::launch_rope_append(a, c, dt == MXQ_BF16, interleaved != 0, fmt == MXQ_MXFP4, stream));
+}
+
 // Sizes of an attention call over a cache of shape c.
 static bool attend_sizes(int64_t batch, int64_t q_heads, const mxq::KvShape& c, int64_t table_width, int64_t window) {
   if (batch < 1 || q_heads < 1 || q_heads % c.heads != 0 || (c.dim != 64 && c.dim != 128 && c.dim != 256)) return false;

@@ -262,6 +262,15 @@ __device__ __forceinline__ u32x2 mx8_convert8_f32(const float (&v)[8], unsigned 
   return (u32x2){__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
 }
 
+// d rounded to odd in fp32: an inexact result with an even significand moves one
+// unit towards d, so that one more rounding (to a code) is that of d itself.
+__device__ __forceinline__ float round_odd(double d) {
+  const float n = (float)d;
+  unsigned b = __float_as_uint(n);
+  if ((double)n != d && (b & 1u) == 0) b += (fabs(d) > fabs((double)n)) ? 1u : ~0u;
+  return __uint_as_float(b);
+}
+
 // MXFP8 of one lane's 8 consecutive fp32 values of a quad's block.
 __device__ __forceinline__ u32x2 mx8_quantize_quad_f32(const float (&v)[8], unsigned* code) {
   const unsigned c = e8m0_code_e4m3(quad_max(f32x8_absmax_bits(v)) >> 23), lim = mx8_limit_bits(c);

@@ -29,6 +29,23 @@ hipError_t launch_kv_read(const uint8_t* kq, const uint8_t* ks, const uint8_t* v
                           const int64_t* slots, int64_t tokens, const KvShape& c, bool fp4, void* k, void* v,
                           bool bf16, hipStream_t st);
 
+// New tokens' queries and keys rotated by their positions: queries to q_out,
+// keys and the values as they are quantized into their slots.
+struct RopeArgs {
+  const void *q, *k, *v;  // rows of whole heads, strides in elements
+  int64_t q_stride, k_stride, v_stride;
+  const int64_t* positions;  // [position_axes][tokens]
+  const uint8_t* axes;       // [pairs], or null: axis 0
+  const float* freqs;        // [pairs]
+  const int64_t* slots;      // [tokens]
+  int64_t tokens, position_axes;
+  unsigned q_heads, pairs;
+  uint8_t *kq, *ks, *vq, *vs;
+  uint16_t* q_out;  // bf16 [tokens][q_heads][dim]
+};
+hipError_t launch_rope_append(const RopeArgs& a, const KvShape& c, bool bf16, bool interleaved, bool fp4,
+                              hipStream_t st);
+
 // Attention of one new token per sequence over the paged cache.
 struct AttendArgs {
   const uint16_t* q;  // bf16 [batch][q_heads][dim], rows q_stride elements apart

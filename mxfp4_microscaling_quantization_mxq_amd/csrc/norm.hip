@@ -203,15 +203,7 @@ __device__ __forceinline__ u32x2 scale_quantize(Raw8<kBf16> r, Raw8<kBf16> weigh
   to_f32<kBf16>(r, v);
   to_f32<kBf16>(weight, w);
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const double d = (double)v[i] * f * (double)w[i];
-    const float n = (float)d;
-    // rounded to odd: an inexact result with an even significand moves one
-    // unit towards d
-    unsigned b = __float_as_uint(n);
-    if ((double)n != d && (b & 1u) == 0) b += (fabs(d) > fabs((double)n)) ? 1u : ~0u;
-    y[i] = __uint_as_float(b);
-  }
+  for (int i = 0; i < 8; i++) y[i] = round_odd((double)v[i] * f * (double)w[i]);
   return mx8_quantize_quad_f32(y, code);
 }
 
