@@ -452,6 +452,45 @@ MXQ_API mxq_status mxq_paged_attention(const void *q, int64_t q_stride, const ui
                                float scale, int64_t window, void *workspace, int64_t workspace_bytes,
                                void *out, mxq_dtype odt, hipStream_t stream);
 
+/*
+ * Attention of drafted tokens over the paged cache (which holds them already):
+ * `drafts` tokens per sequence, of which each sees the sequence's context and
+ * the drafted tokens that its mask names (the ancestors in a tree of drafts, or
+ * all before it in a chain, and itself).  Drafted token i of sequence b is at
+ * cache position context[b] + i; bit j % 64 of mask[b][i][j / 64] says that it
+ * sees drafted token j (words = ceil(drafts / 64) a token; bits from `drafts` on
+ * have no meaning).  For each query head h, with cache head h / (q_heads /
+ * kv_heads) and t over what token i sees:
+ *   o_i = sum_t p_t V_t / (sum_t p_t + [sinks] exp(sinks[h])), p_t = exp(scale * q_i . K_t).
+ * A window > 0 hides what lies `window` positions or more before the token, but
+ * not the first `first` positions of the sequence: the distance to context
+ * token t is context[b] + depth_i - t, to drafted token j depth_i - depth_j, with
+ * depth_i the number of drafted tokens before i (j < i) that i sees; a drafted
+ * token's position is context[b] + depth.  With drafts 1 this is a decode step
+ * whose first tokens stay visible.
+ * A token that sees nothing gives zeros (a mask of 0 and a context of 0 mark
+ * padding).  What the cache holds in positions that a token does not see has no
+ * effect on it.  Contexts below 0 count as 0, above table_width * P as that;
+ * positions past the table, or whose table entry is outside [0, pages), are not
+ * visible.  The table, contexts and masks are device memory, and the host does
+ * not read them.
+ * q bf16 [batch * drafts] rows at q + r * q_stride elements (row b * drafts + i
+ * is token i of sequence b); context int32 [batch]; mask uint64 [batch][drafts]
+ * [words]; out [batch * drafts][q_heads][head_dim] of type odt; 1 <= drafts <=
+ * 256; window, first >= 0.  The table, sinks, head_dim, scale, accuracy, NaN,
+ * workspace (mxq_tree_attention_workspace) and split as mxq_paged_attention.
+ */
+MXQ_API mxq_status mxq_tree_attention_workspace(int64_t batch, int64_t drafts, int64_t q_heads, int64_t kv_heads,
+                                        int64_t page_size, int64_t head_dim, int64_t table_width, int64_t window,
+                                        int64_t first, int64_t *bytes);
+MXQ_API mxq_status mxq_tree_attention(const void *q, int64_t q_stride, const uint8_t *kq, const uint8_t *ks,
+                              const uint8_t *vq, const uint8_t *vs, const int32_t *table, int64_t table_width,
+                              int64_t table_stride, const int32_t *context, const uint64_t *mask,
+                              const float *sinks, int64_t batch, int64_t drafts, int64_t q_heads, int64_t pages,
+                              int64_t kv_heads, int64_t page_size, int64_t head_dim, mxq_format fmt, float scale,
+                              int64_t window, int64_t first, void *workspace, int64_t workspace_bytes, void *out,
+                              mxq_dtype odt, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,7 @@ and, between the products of a served model's decode step:
 or, for tokens with positions and for drafted tokens that one step checks:
 
     q = rope_append(cache, q, k, v, slots, positions, freqs)   # rotate, quantize new tokens into their slots
+    o = tree_attention(q, cache, table, context, mask)         # several drafted tokens per sequence
 
 Every tensor argument is checked before anything is enqueued: dtype, shape
 (scales and caller-supplied outputs must match the operands exactly),
@@ -57,7 +58,7 @@ API = (
     "mxq_dequantize", "mxq_gemv_w4a16", "mxq_gemm_w4a4", "mxq_gemm_w4a4_quant", "mxq_gemm_w4a4_dynamic",
     "mxq_gemm_w4a8", "mxq_gemm_w4a8_dynamic", "nvq_quantize", "nvq_dequantize", "nvq_gemm", "mxq_transfp4_quantize", "mxq_transfp4_dequantize",
     "mxq_rmsnorm_quantize_fp8", "mxq_kv_append", "mxq_kv_read", "mxq_paged_attention_workspace", "mxq_paged_attention",
-    "mxq_rope_append",
+    "mxq_rope_append", "mxq_tree_attention_workspace", "mxq_tree_attention",
 )
 
 
@@ -110,6 +111,9 @@ def capi() -> ctypes.CDLL:
                                         I64, P, I64, P, I, P]
     lib.mxq_rope_append.argtypes = [P, I64, P, I64, P, I64, I, P, I64, P, P, I64, I, P, I64, I64, I64, I64, I64, I64, I,
                                     P, P, P, P, P, P]
+    lib.mxq_tree_attention_workspace.argtypes = [I64, I64, I64, I64, I64, I64, I64, I64, I64, ctypes.POINTER(I64)]
+    lib.mxq_tree_attention.argtypes = [P, I64, P, P, P, P, P, I64, I64, P, P, P, I64, I64, I64, I64, I64, I64, I64, I, F,
+                                       I64, I64, P, I64, P, I, P]
     for name in API[2:]:
         getattr(lib, name).restype = I
     _lib = lib
@@ -795,6 +799,113 @@ def paged_attention(q, cache, table, lens, scale=None, window=0, sinks=None, out
                                    out.data_ptr(), _dtype_code(out_dtype), _stream(dev))
     if code != 0:
         _check(code, "mxq_paged_attention")
+    return out
+
+
+def tree_mask(parents, device="cuda"):
+    """The masks of tree_attention, int64 [batch, drafts, words], of trees of
+    drafted tokens: parents is a list of lists (one list: a batch of one), where
+    parents[b][i] is the index of the drafted token that i follows, below i, or -1
+    where it follows the context.  A token sees its ancestors and itself.  Trees
+    shorter than the longest are padded with tokens that see no drafted token and
+    that none sees."""
+    torch = _torch()
+    trees = parents.tolist() if isinstance(parents, torch.Tensor) else list(parents)
+    if not trees or not hasattr(trees[0], "__len__"):
+        trees = [trees]
+    drafts = max(len(t) for t in trees)
+    if drafts < 1:
+        raise ValueError("a tree needs a drafted token")
+    words = (drafts + 63) // 64
+    masks = torch.zeros(len(trees), drafts, words, dtype=torch.int64)
+    for b, tree in enumerate(trees):
+        seen = []
+        for i, p in enumerate(tree):
+            if not -1 <= p < i:
+                raise ValueError(f"parents[{b}][{i}] is {p}: a drafted token follows one before it, or -1")
+            seen.append((seen[p] if p >= 0 else 0) | 1 << i)
+            for w in range(words):
+                v = seen[i] >> (64 * w) & 0xFFFFFFFFFFFFFFFF
+                masks[b, i, w] = v - (1 << 64) if v >> 63 else v
+    return masks.to(device)
+
+
+def tree_attention(q, cache, table, context, mask, scale=None, window=0, first=0, sinks=None, out_dtype=None, out=None,
+                   workspace=None):
+    """Attention of several drafted tokens per sequence over the cache, which
+    holds them already: out[batch * drafts, q_heads, D].
+
+    q [batch * drafts, q_heads, D] bf16 (row stride free), row b * drafts + i the
+    i-th drafted token of sequence b, at cache position context[b] + i; context
+    [batch] int32, tokens before the drafted ones; mask [batch, drafts, words]
+    int64, bit j of token i's words (64 a word): it sees drafted token j
+    (tree_mask makes them of a tree); table [batch, width] int32 page ids (row
+    stride free).  window > 0 hides positions that far back or further, but not
+    the `first` first positions of the sequence; a drafted token's position is
+    context + the drafted tokens before it that it sees.  scale, sinks and
+    workspace as in paged_attention.  A token that sees nothing gives zeros."""
+    torch = _torch()
+    dev = _index(cache[0])
+    pages, heads, page, d, fmt = _cache(cache, dev)
+    q_stride = _rows(q, "q", (torch.bfloat16,), None, d)
+    rows, q_heads, _ = q.shape
+    if q_heads % heads != 0:
+        raise ValueError(f"{q_heads} query heads over {heads} cache heads")
+    if not isinstance(mask, torch.Tensor) or mask.dim() != 3 or not _same(mask, torch.int64, mask.shape, dev):
+        _need(mask, "mask", torch.int64, ndim=3)
+    batch, drafts, words = mask.shape
+    if words != (drafts + 63) // 64:
+        raise ValueError(f"mask must have {(drafts + 63) // 64} words for {drafts} drafted tokens, got {words}")
+    if rows != batch * drafts:
+        raise ValueError(f"q has {rows} rows for {batch} sequences of {drafts} drafted tokens")
+    if not isinstance(table, torch.Tensor) or table.dtype is not torch.int32:
+        raise TypeError("table must be an int32 tensor")
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must have shape [{batch}, width] with contiguous rows, got {tuple(shape)}")
+    width = shape[1]
+    table_stride = table.stride(0) if batch > 1 else max(width, table.stride(0))
+    if not _same(context, torch.int32, (batch,), dev):
+        _need(context, "context", torch.int32, (batch,))
+    kq, ks, vq, vs = cache
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    if out is None and out_dtype is torch.bfloat16:
+        out = q.new_empty((rows, q_heads, d))
+    else:
+        out = _out(out, "out", (rows, q_heads, d), out_dtype, kq.device, real=True)
+    if sinks is not None and not _same(sinks, torch.float32, (q_heads,), dev):
+        _need(sinks, "sinks", torch.float32, (q_heads,))
+    lib = capi()
+    need = ctypes.c_int64()
+    code = lib.mxq_tree_attention_workspace(batch, drafts, q_heads, heads, page, d, width, window, first,
+                                            ctypes.byref(need))
+    if code != 0:
+        _check(code, "mxq_tree_attention_workspace")
+    need = need.value
+    if workspace is None:
+        wp = None
+        if need:
+            workspace = kq.new_empty(need)
+            wp = workspace.data_ptr()
+    else:
+        _need(workspace, "workspace", torch.uint8, ndim=1)
+        need, least = workspace.shape[0], need
+        if need < least:
+            raise ValueError(f"workspace has {need} bytes, {least} are needed")
+        wp = workspace.data_ptr()
+    if (dev < 0 or q.get_device() != dev or table.get_device() != dev or context.get_device() != dev
+            or mask.get_device() != dev or out.get_device() != dev or (sinks is not None and sinks.get_device() != dev)
+            or (workspace is not None and workspace.get_device() != dev)):
+        on = {"kq": kq, "q": q, "table": table, "context": context, "mask": mask, "out": out, "sinks": sinks,
+              "workspace": workspace}
+        _on_device(**{name: t for name, t in on.items() if t is not None})
+    code = lib.mxq_tree_attention(q.data_ptr(), q_stride, kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(),
+                                  table.data_ptr(), width, table_stride, context.data_ptr(), mask.data_ptr(),
+                                  None if sinks is None else sinks.data_ptr(), batch, drafts, q_heads, pages, heads,
+                                  page, d, fmt, 1.0 / math.sqrt(d) if scale is None else scale, window, first, wp, need,
+                                  out.data_ptr(), _dtype_code(out_dtype), _stream(dev))
+    if code != 0:
+        _check(code, "mxq_tree_attention")
     return out
 
 

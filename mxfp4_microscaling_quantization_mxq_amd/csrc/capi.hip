@@ -444,4 +444,71 @@ mxq_status mxq_paged_attention(const void* q, int64_t q_stride, const uint8_t* k
   return launched(mxq::launch_attend(a, c, fmt == MXQ_MXFP4, workspace, stream));
 }
 
+// Sizes of a tree's attention over a cache of shape c.
+static bool tree_sizes(int64_t batch, int64_t drafts, int64_t q_heads, const mxq::KvShape& c, int64_t table_width,
+                       int64_t window, int64_t first) {
+  if (batch < 1 || q_heads < 1 || q_heads % c.heads != 0 || (c.dim != 64 && c.dim != 128 && c.dim != 256)) return false;
+  if (drafts < 1 || drafts > 256 || table_width < 1 || table_width > 0x7FFFFFFF || window < 0 || first < 0) return false;
+  // blocks of 256 threads of both launches: below 2^32 threads
+  if (q_heads > (1 << 20) || batch > (1 << 24) / q_heads) return false;
+  const int64_t blocks = mxq::tree_attend_blocks(batch, drafts, (unsigned)q_heads, c, table_width, window, first);
+  return blocks > 0 && blocks < (1 << 24);
+}
+
+mxq_status mxq_tree_attention_workspace(int64_t batch, int64_t drafts, int64_t q_heads, int64_t kv_heads,
+                                        int64_t page_size, int64_t head_dim, int64_t table_width, int64_t window,
+                                        int64_t first, int64_t* bytes) {
+  mxq::KvShape c;
+  if (!bytes || !cache_shape(1, kv_heads, page_size, head_dim, &c) ||
+      !tree_sizes(batch, drafts, q_heads, c, table_width, window, first))
+    return MXQ_ERROR_INVALID_VALUE;
+  *bytes = mxq::tree_attend_workspace(batch, drafts, (unsigned)q_heads, c, table_width, window, first);
+  return MXQ_SUCCESS;
+}
+
+mxq_status mxq_tree_attention(const void* q, int64_t q_stride, const uint8_t* kq, const uint8_t* ks, const uint8_t* vq,
+                              const uint8_t* vs, const int32_t* table, int64_t table_width, int64_t table_stride,
+                              const int32_t* context, const uint64_t* mask, const float* sinks, int64_t batch,
+                              int64_t drafts, int64_t q_heads, int64_t pages, int64_t kv_heads, int64_t page_size,
+                              int64_t head_dim, mxq_format fmt, float scale, int64_t window, int64_t first,
+                              void* workspace, int64_t workspace_bytes, void* out, mxq_dtype odt, hipStream_t stream) {
+  mxq::KvShape c;
+  if (!cache_shape(pages, kv_heads, page_size, head_dim, &c) || !valid_dtype(odt) || !valid_format(fmt) ||
+      !tree_sizes(batch, drafts, q_heads, c, table_width, window, first))
+    return MXQ_ERROR_INVALID_VALUE;
+  if (q_stride < q_heads * head_dim || q_stride % 8 != 0 || q_stride > kMaxElems / (batch * drafts) ||
+      table_stride < table_width || table_stride > kMaxElems / batch || !std::isfinite(scale))
+    return MXQ_ERROR_INVALID_VALUE;
+  if (!q || !table || !context || !mask || !out) return MXQ_ERROR_INVALID_VALUE;
+  const int64_t need = mxq::tree_attend_workspace(batch, drafts, (unsigned)q_heads, c, table_width, window, first);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERROR_INVALID_VALUE;
+  mxq_status e = cache_pointers(kq, ks, vq, vs);
+  if (e != MXQ_SUCCESS) return e;
+  if (!aligned16(q) || !aligned16(out) || (need > 0 && !aligned16(workspace))) return MXQ_ERROR_MISALIGNED;
+  if (((uintptr_t)table & 3u) || ((uintptr_t)context & 3u) || ((uintptr_t)sinks & 3u) || ((uintptr_t)mask & 7u))
+    return MXQ_ERROR_MISALIGNED;
+  e = check_device();
+  if (e != MXQ_SUCCESS) return e;
+  mxq::TreeArgs a;
+  a.q = (const uint16_t*)q;
+  a.q_stride = q_stride;
+  a.kq = kq, a.ks = ks, a.vq = vq, a.vs = vs;
+  a.table = table;
+  a.table_width = table_width;
+  a.table_stride = table_stride;
+  a.context = context;
+  a.mask = mask;
+  a.words = (unsigned)((drafts + 63) / 64);
+  a.sinks = sinks;
+  a.batch = batch;
+  a.drafts = drafts;
+  a.window = window;
+  a.first = first;
+  a.q_heads = (unsigned)q_heads;
+  a.scale = scale;
+  a.out = out;
+  a.bf16_out = odt == MXQ_BF16;
+  return launched(mxq::launch_tree_attend(a, c, fmt == MXQ_MXFP4, workspace, stream));
+}
+
 }  // extern "C"

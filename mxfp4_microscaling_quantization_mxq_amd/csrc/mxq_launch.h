@@ -68,6 +68,30 @@ int64_t attend_blocks(int64_t batch, unsigned q_heads, const KvShape& c, bool fp
 int64_t attend_workspace(int64_t batch, unsigned q_heads, const KvShape& c, int64_t table_width, int64_t window);
 hipError_t launch_attend(const AttendArgs& a, const KvShape& c, bool fp4, void* workspace, hipStream_t st);
 
+// Attention of `drafts` drafted tokens per sequence over the paged cache.
+struct TreeArgs {
+  const uint16_t* q;  // bf16 [batch * drafts][q_heads][dim], rows q_stride elements apart
+  int64_t q_stride;
+  const uint8_t *kq, *ks, *vq, *vs;
+  const int32_t* table;  // [batch][table_width], rows table_stride apart
+  int64_t table_width, table_stride;
+  const int32_t* context;  // [batch]
+  const uint64_t* mask;    // [batch][drafts][words]
+  unsigned words;          // (drafts + 63) / 64
+  const float* sinks;      // [q_heads] or null
+  int64_t batch, drafts, window, first;
+  unsigned q_heads;
+  float scale;
+  void* out;  // [batch * drafts][q_heads][dim]
+  bool bf16_out;
+};
+// As attend_blocks and attend_workspace.
+int64_t tree_attend_blocks(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
+                           int64_t window, int64_t first);
+int64_t tree_attend_workspace(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
+                              int64_t window, int64_t first);
+hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, void* workspace, hipStream_t st);
+
 hipError_t launch_mx_quantize(const void* x, bool bf16, int64_t rows, int64_t k, uint8_t* q, uint8_t* s,
                               hipStream_t st);
 // MXFP8: q[rows][k] E4M3 codes, s[rows][k/32] E8M0 codes.

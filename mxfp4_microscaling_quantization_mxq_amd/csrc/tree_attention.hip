@@ -1,0 +1,671 @@
+// tree_attention.hip -- attention of several drafted tokens per sequence over a
+// paged MXFP8 / MXFP4 cache, each of which sees the context and the drafted
+// tokens that its mask names (gfx950).
+//
+//   o_i = sum_t p_t V_t / (sum_t p_t [+ exp(sink - m)]),  p_t = exp(scale q_i . K_t - m),
+//   t over the context and over context + j for the bits j of mask i
+//
+// Rows.  The query heads that share a cache head, of all drafted tokens, are the
+// rows of one product with the cache: row r is head r % group of token r / group.
+// A wave takes N sets of 16 rows (the columns of the 16x16x32 bf16 MFMA) and
+// walks over tiles of 32 tokens as the attention of one token does: S^T = K Q^T,
+// whose results are the B operand of O^T += V^T P^T without leaving their lanes,
+// with the transpose of V as byte selects.  A tile is loaded and decoded once for
+// the wave's sets.
+//
+// Masks.  A tile that some row of the wave does not see whole (the context's
+// end, a window's edge, the drafted tokens) forms a word of 32 bits a row, from
+// two ranges and the row's mask in LDS; all others have no mask at all.
+//
+// Split.  As for one token: a unit is one sequence, one cache head and a group
+// of its rows; the tiles of all units in order are cut into equal ranges, one a
+// block, and ranges that end inside a unit leave partial results to be joined.
+#include "mxq_attend.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kSet = 16;            // rows of one MFMA column set
+constexpr int kMaskRow = 2 * 4 + 2;  // 32-bit words of a token's mask in LDS, an empty one before and after
+
+struct TreeParams {
+  TreeArgs a;
+  KvShape c;
+  unsigned group;       // query heads per cache head
+  unsigned rows;        // group * drafts
+  unsigned row_groups;  // units per sequence and cache head
+  unsigned row_shift;   // 2^row_shift waves of a block take rows of their own, the others tiles
+  // Workspace, as for one token: records {parts, the block that opened the
+  // unit, the unit} by opening block (by_block) or by unit, and two slots of
+  // partial results a block.
+  bool by_block;
+  int* parts;
+  float *part_o, *part_ml;
+};
+
+// What a sequence's rows may see: tiles [0, a) and [b, b + n - a) of 32 tokens.
+struct TreeSpan {
+  int context, end, a, b, n;
+};
+__device__ __forceinline__ TreeSpan tree_span(const TreeParams& p, int64_t seq) {
+  const int64_t most = min(p.a.table_width << p.c.page_shift, kMaxLen);
+  const int64_t context = min((int64_t)max(p.a.context[seq], 0), most), end = min(context + p.a.drafts, most);
+  TreeSpan s = {(int)context, (int)end, 0, 0, 0};
+  if (p.a.window > 0) {
+    s.a = (int)((min(p.a.first, end) + kTile - 1) / kTile);
+    s.b = max(s.a, (int)(max((int64_t)0, context - p.a.window + 1) / kTile));
+  }
+  const int tiles = (int)((end + kTile - 1) / kTile);
+  s.n = s.a + max(0, tiles - s.b);
+  if (s.n == 0) s.b = tiles - 1, s.n = 1;  // nothing to see: a tile that is masked, for the zeros
+  return s;
+}
+
+__device__ __forceinline__ unsigned below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+
+// Tiles of a range.
+__device__ __forceinline__ unsigned range_tiles(unsigned sum, unsigned blocks, unsigned least) {
+  return max((sum + blocks - 1) / blocks, least);
+}
+
+template <int D, bool kFp4, int kTerms, int N, bool kRanges>
+__global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
+  typedef Tile<D, kFp4> T;
+  constexpr int kSteps = D / 32;  // QK products of half a tile
+  constexpr int J = D / 16;       // PV products of a tile; elements of V per lane and token
+  constexpr int kPad = D + 4;
+  __shared__ float lds_o[kWaves][kSet][kPad];
+  __shared__ float lds_m[kWaves][kSet], lds_l[kWaves][kSet], lds_top[kWaves][kSet];
+  __shared__ unsigned lds_mask[kWaves * N * kSet][kMaskRow];
+  __shared__ int lds_depth[kThreads];
+  __shared__ unsigned lds_sum[kWaves];
+  __shared__ int lds_at[3];
+
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned per_shift = 2 - p.row_shift, per_tile = 1u << per_shift;  // waves that share tiles
+  const int sub = wave & (per_tile - 1), row_wave = wave >> per_shift;
+  const unsigned unit_rows = (unsigned)(N * kSet) << p.row_shift;
+
+  unsigned x, end, u_first, head, rg, per = 0;
+  int64_t b;
+  TreeSpan s;
+  if constexpr (!kRanges) {
+    unsigned id = blockIdx.x;
+    rg = id % p.row_groups;
+    id /= p.row_groups;
+    head = id % p.c.heads;
+    b = id / p.c.heads;
+    s = tree_span(p, b);
+    x = u_first = 0;
+    end = s.n;
+  } else {
+    // each thread sums the tiles of a run of sequences; scan over the block
+    const unsigned units = p.c.heads * p.row_groups;  // of a sequence
+    const unsigned batch = (unsigned)p.a.batch, each = (batch + kThreads - 1) / kThreads;
+    const unsigned b0 = min(threadIdx.x * each, batch), b1 = min(b0 + each, batch);
+    unsigned own = 0;
+    for (unsigned k = b0; k < b1; k++) own += tree_span(p, k).n * units;
+    unsigned incl = own;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const unsigned o = __shfl_up(incl, m, 64);
+      if (lane >= m) incl += o;
+    }
+    if (lane == 63) lds_sum[wave] = incl;
+    __syncthreads();
+    unsigned sum = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) {
+      if (w < wave) before += lds_sum[w];
+      sum += lds_sum[w];
+    }
+    sum = uniform(sum);
+    per = range_tiles(sum, gridDim.x, per_tile);
+    x = blockIdx.x * per;
+    end = min(x + per, sum);
+    unsigned at = before + incl - own;  // first tile of this thread's sequences
+    if (x >= at && x < at + own) {
+      unsigned k = b0, n = tree_span(p, k).n;
+      while (x >= at + n * units) {
+        at += n * units;
+        n = tree_span(p, ++k).n;
+      }
+      const unsigned u = (x - at) / n;
+      lds_at[0] = (int)k, lds_at[1] = (int)u, lds_at[2] = (int)(at + u * n);
+    }
+    if (p.by_block && threadIdx.x == 0) p.parts[4 * blockIdx.x] = 0;
+    if (x >= end) return;
+    __syncthreads();
+    b = uniform(lds_at[0]);
+    const unsigned u = uniform(lds_at[1]);
+    u_first = uniform(lds_at[2]);
+    s = tree_span(p, b);
+    head = u / p.row_groups, rg = u % p.row_groups;
+  }
+
+  while (true) {
+    // tiles [first, last) of the unit, counted from its first
+    const int first = (int)(x - u_first), last = min(s.n, (int)(end - u_first));
+    const unsigned row0 = rg * unit_rows, token0 = row0 / p.group;
+    const unsigned tokens = (min(row0 + unit_rows, p.rows) - 1) / p.group - token0 + 1;
+    const unsigned words = p.a.words, drafts = (unsigned)p.a.drafts;
+
+    // the masks of the unit's tokens, less what the window hides, and all depths
+    if (threadIdx.x < drafts) {
+      const uint32_t* m = (const uint32_t*)(p.a.mask + (b * drafts + threadIdx.x) * words);
+      int depth = 0;
+      for (unsigned w = 0; w <= threadIdx.x / 32; w++) depth += __popc(m[w] & below((int)(threadIdx.x - 32 * w)));
+      lds_depth[threadIdx.x] = depth;
+    }
+    __syncthreads();
+    for (unsigned t = threadIdx.x; t < tokens; t += kThreads) {
+      const uint32_t* m = (const uint32_t*)(p.a.mask + (b * drafts + token0 + t) * words);
+      const int depth = lds_depth[token0 + t];
+      lds_mask[t][0] = 0;
+      for (unsigned w = 0; w < 2 * words; w++) {
+        unsigned v = m[w] & below((int)drafts - (int)(32 * w));
+        if (p.a.window > 0 && p.a.window < p.a.drafts) {
+          unsigned left = v;
+          while (left) {
+            const int bit = __builtin_ctz(left), d = lds_depth[32 * w + bit];
+            left &= left - 1;
+            if (depth - d >= p.a.window && s.context + d >= p.a.first) v &= ~(1u << bit);
+          }
+        }
+        lds_mask[t][1 + w] = v;
+      }
+      lds_mask[t][1 + 2 * words] = 0;
+    }
+    __syncthreads();
+
+    // rows: scores are scaled by |scale| (its sign is in q), never by less than
+    // what keeps a masked score at -inf
+    const float to_log2 = fmaxf(fabsf(p.a.scale) * kLog2e, 0x1p-100f);
+    const unsigned q_sign = p.a.scale < 0 ? 0x80008000u : 0u;
+    float m[N], l[N];  // of the unscaled scores, and of this lane's tokens
+    f32x4 acc[N][J];
+    bf16x8 qf[N][kSteps];
+    int lo[N];  // context tokens from here on are inside the row's window
+    unsigned mask_at[N];
+    bool live[N];
+    int lo_most = 0;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      m[n] = -INFINITY, l[n] = 0;
+#pragma unroll
+      for (int j = 0; j < J; j++) acc[n][j] = (f32x4){0, 0, 0, 0};
+      const unsigned r = row0 + (row_wave * N + n) * kSet + i;
+      live[n] = r < p.rows;
+      const unsigned token = live[n] ? r / p.group : token0, qh = head * p.group + (live[n] ? r - token * p.group : 0);
+      mask_at[n] = token - token0;
+      lo[n] = 0;
+      if (p.a.window > 0) lo[n] = (int)max((int64_t)0, s.context + lds_depth[token] - p.a.window + 1);
+      lo_most = live[n] ? max(lo_most, lo[n]) : lo_most;
+#pragma unroll
+      for (int st = 0; st < kSteps; st++) {
+        const int d = D == 64 ? 16 * g + 8 * st : 128 * (st / 4) + 32 * g + 8 * (st & 3);
+        u32x4 w = {0, 0, 0, 0};
+        if (live[n]) w = *(const u32x4*)(p.a.q + (b * drafts + token) * p.a.q_stride + (int64_t)qh * D + d);
+        qf[n][st] = __builtin_bit_cast(bf16x8, w ^ q_sign);
+      }
+    }
+#pragma unroll
+    for (int k = 1; k < 16; k <<= 1) lo_most = max(lo_most, __shfl_xor(lo_most, k, 64));
+    lo_most = uniform(lo_most);
+    const int seen_first = p.a.window > 0 ? (int)min(p.a.first, (int64_t)s.context) : 0;
+
+    {
+      const unsigned shift = p.c.page_shift, pmask = (1u << shift) - 1;
+      // This wave's tiles are first + sub + per_tile j, j < count.  The page ids
+      // of the tile to load next are scalars, read from the table one tile
+      // earlier; -1 where the table names no page of the cache.
+      const __attribute__((address_space(4))) int32_t* row =
+          (const __attribute__((address_space(4))) int32_t*)(p.a.table + b * p.a.table_stride);
+      const bool any_row = row0 + row_wave * N * kSet < p.rows;
+      const int count = any_row && first + sub < last ? (last - first - sub + (int)per_tile - 1) >> per_shift : 0;
+      auto token_of = [&](int j) {
+        const int k = first + sub + (j << per_shift);
+        return (k < s.a ? k : k - s.a + s.b) * kTile;
+      };
+      auto id_of = [&](int token) { return uniform(row[(unsigned)min(token, s.end - 1) >> shift]); };
+      int id0 = -1, id1 = -1, fetched = 0;  // tiles whose K is on its way
+
+      T t;
+      Half half[2];  // of the tile in t
+      auto fetch_k = [&]() {
+        const int tok = token_of(fetched);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int id = h ? id1 : id0, th = tok + 16 * h;
+          half[h].on = fetched < count && th < s.end && id >= 0 && id < p.c.pages;
+          half[h].row = (((int64_t)(half[h].on ? id : 0) * p.c.heads + head) << shift) + (th & pmask);
+          load_k<D, kFp4>(p, half[h], h, i, g, t);
+        }
+        fetched++;
+        const int next = token_of(min(fetched, count - 1));
+        id0 = id_of(next);
+        id1 = id_of(next + 16);
+      };
+      auto fetch_v = [&](int j) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) load_v<D, kFp4>(p, half[h], (token_of(j) + 16 * h) & pmask, h, i, g, t);
+      };
+      if (count > 0) {
+        id0 = id_of(token_of(0));
+        id1 = id_of(token_of(0) + 16);
+        fetch_k();
+        fetch_v(0);
+      }
+      for (int j = 0; j < count; j++) {
+        const int t0 = token_of(j);
+        const bool on0 = half[0].on, on1 = half[1].on;
+        // S^T
+        f32x4 sc[N][2];
+#pragma unroll
+        for (int n = 0; n < N; n++) sc[n][0] = sc[n][1] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+        for (int st = 0; st < kSteps; st++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const float scale = e8m0_as_scale(t.ks[h][D == 64 ? 0 : st / 4]);
+            u32x4 a;
+#pragma unroll
+            for (int e = 0; e < 4; e++) a[e] = decode2<kFp4>(t.k[h], 4 * st + e, scale);
+#pragma unroll
+            for (int n = 0; n < N; n++)
+              sc[n][h] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), qf[n][st], sc[n][h], 0, 0, 0);
+          }
+        fetch_k();
+        const bool whole = t0 + kTile <= s.context && (t0 >= lo_most || t0 + kTile <= seen_first) && on0 && on1;
+        unsigned seen[N];
+        if (!whole) {
+          unsigned any = 0;
+#pragma unroll
+          for (int n = 0; n < N; n++) {
+            // context tokens in the window or among the first, then the drafted ones
+            const int to = s.context - t0;
+            unsigned w = (below(to) & ~below(lo[n] - t0)) | below(seen_first - t0);
+            const int at = (-to) >> 5;  // drafted token -to is the tile's first
+            if (at >= -1 && at <= 2 * (int)words - 1) {
+              const unsigned* mk = &lds_mask[mask_at[n]][1 + at];
+              w |= (unsigned)((((uint64_t)mk[1] << 32) | mk[0]) >> ((unsigned)-to & 31u));
+            }
+            w &= (on0 ? 0xFFFFu : 0u) | (on1 ? 0xFFFF0000u : 0u);
+            seen[n] = live[n] ? w : 0u;
+            any |= seen[n];
+          }
+#pragma unroll
+          for (int k = 1; k < 16; k <<= 1) any |= (unsigned)__shfl_xor((int)any, k, 64);
+          // a token that no row sees: its V bytes are whatever the page holds, so
+          // its codes and scale are cleared
+#pragma unroll
+          for (int r = 0; r < 8; r++) {
+            const bool kept = (any >> (16 * (r >> 2) + 4 * g + (r & 3))) & 1;
+#pragma unroll
+            for (int w = 0; w < (int)(sizeof(t.v[r]) / 4); w++) t.v[r][w] = kept ? t.v[r][w] : 0u;
+            t.vs[r >> 2] = kept ? t.vs[r >> 2] : t.vs[r >> 2] & ~(0xFFu << (8 * (r & 3)));
+          }
+        }
+        // softmax over the tile; y[4 h + r]: row i, token t0 + 16 h + 4 g + r
+        u32x4 pt[N][kTerms];
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+          float y[8];
+#pragma unroll
+          for (int r = 0; r < 8; r++) y[r] = sc[n][r >> 2][r & 3];
+          if (!whole) {
+#pragma unroll
+            for (int r = 0; r < 8; r++)
+              y[r] = (seen[n] >> (16 * (r >> 2) + 4 * g + (r & 3))) & 1 ? y[r] : -INFINITY;
+          }
+          float top = y[0];
+#pragma unroll
+          for (int r = 1; r < 8; r++) top = fmaxf(top, y[r]);
+          top = fmaxf(m[n], max_groups(top));
+          const float ref = top > -INFINITY ? top * to_log2 : 0.0f;  // nothing seen yet: every p is 0
+          if (__builtin_amdgcn_ballot_w64(top > m[n]) != 0) {
+            // the old terms are relative to the rounded m * to_log2, so that is what
+            // moves them: exactly 1 for a row whose maximum stays
+            const float alpha = __builtin_amdgcn_exp2f(m[n] * to_log2 - ref);
+            l[n] *= alpha;
+#pragma unroll
+            for (int k = 0; k < J; k++) acc[n][k] *= alpha;
+            m[n] = top;
+          }
+          // P in bf16 terms: each takes the upper half of what the ones before
+          // it left (truncated; the last one rounded)
+#pragma unroll
+          for (int r = 0; r < 8; r += 2) {
+            float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r], to_log2, -ref));
+            float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(y[r + 1], to_log2, -ref));
+            l[n] += p0 + p1;
+#pragma unroll
+            for (int k = 0; k < kTerms; k++) {
+              if (k + 1 == kTerms) {
+                pt[n][k][r >> 1] = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)p0, (__bf16)p1});
+              } else {
+                const unsigned w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+                pt[n][k][r >> 1] = perm(w1, w0, 0x07060302u);
+                p0 -= __uint_as_float(w0 & 0xFFFF0000u);  // exact
+                p1 -= __uint_as_float(w1 & 0xFFFF0000u);
+              }
+            }
+          }
+        }
+        // O^T
+        float vscale[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++) vscale[r] = e8m0_as_scale((t.vs[r >> 2] >> (8 * (r & 3))) & 0xFFu);
+#pragma unroll
+        for (int j2 = 0; j2 < J / 2; j2++) {
+          unsigned d[8];
+#pragma unroll
+          for (int r = 0; r < 8; r++) d[r] = decode2<kFp4>(t.v[r], j2, vscale[r]);
+          u32x4 va[2];
+#pragma unroll
+          for (int r = 0; r < 4; r++) {
+            va[0][r] = perm(d[2 * r + 1], d[2 * r], 0x05040100u);
+            va[1][r] = perm(d[2 * r + 1], d[2 * r], 0x07060302u);
+          }
+          if (!whole) {
+            // A NaN (or an infinity) of a token that some rows see must not reach
+            // the others as NaN times 0: it leaves the product, and a product of
+            // ones counts, for each row and element, the seen tokens that had one
+            u32x4 odd[2];
+            unsigned found = 0;
+#pragma unroll
+            for (int o = 0; o < 2; o++)
+#pragma unroll
+              for (int r = 0; r < 4; r++) {
+                unsigned one = 0;
+                if ((va[o][r] & 0x7F80u) == 0x7F80u) one |= 0x3F80u, va[o][r] &= 0xFFFF0000u;
+                if ((va[o][r] & 0x7F800000u) == 0x7F800000u) one |= 0x3F800000u, va[o][r] &= 0xFFFFu;
+                odd[o][r] = one;
+                found |= one;
+              }
+            if (__builtin_amdgcn_ballot_w64(found != 0) != 0) {
+#pragma unroll
+              for (int n = 0; n < N; n++) {
+                u32x4 is;
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                  const unsigned at = 16 * (r >> 1) + 4 * g + 2 * (r & 1);
+                  is[r] = ((seen[n] >> at) & 1 ? 0x3F80u : 0u) | ((seen[n] >> (at + 1)) & 1 ? 0x3F800000u : 0u);
+                }
+#pragma unroll
+                for (int o = 0; o < 2; o++) {
+                  const f32x4 hits = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                      __builtin_bit_cast(bf16x8, odd[o]), __builtin_bit_cast(bf16x8, is), (f32x4){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                  for (int r = 0; r < 4; r++)
+                    acc[n][2 * j2 + o][r] = hits[r] > 0 ? __builtin_nanf("") : acc[n][2 * j2 + o][r];
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < N; n++)
+#pragma unroll
+            for (int k = 0; k < kTerms; k++)
+#pragma unroll
+              for (int o = 0; o < 2; o++)
+                acc[n][2 * j2 + o] =
+                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, va[o]),
+                                                            __builtin_bit_cast(bf16x8, pt[n][k]), acc[n][2 * j2 + o], 0, 0, 0);
+        }
+        fetch_v(j + 1);
+      }
+    }
+
+    // join the waves that shared tiles, a set at a time (maxima in log2 units from here on)
+    const bool opens = first == 0, closes = last == s.n;  // of the unit
+    if (kRanges && opens && threadIdx.x == 0 && !(p.by_block && closes)) {
+      const unsigned unit = ((unsigned)b * p.c.heads + head) * p.row_groups + rg;
+      int* w = p.parts + 4 * (p.by_block ? blockIdx.x : unit);
+      w[0] = (int)((u_first + (unsigned)s.n - 1) / per - blockIdx.x) + 1;
+      w[1] = (int)blockIdx.x, w[2] = (int)unit;
+    }
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const float ln = sum_groups(l[n]), mn = m[n] * to_log2;
+      if (g == 0) lds_m[wave][i] = mn;
+      __syncthreads();
+      float mt = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWaves; w++) {
+        const float mw = lds_m[w][i];
+        mt = w >> per_shift == row_wave ? fmaxf(mt, mw) : mt;
+      }
+      const float f = mn > -INFINITY ? __builtin_amdgcn_exp2f(mn - mt) : 0.0f;
+      if (g == 0) lds_l[wave][i] = ln * f;  // (no maximum: 0, or NaN if all its scores were)
+      if (g == 0 && sub == 0) lds_top[wave][i] = mt;
+#pragma unroll
+      for (int j = 0; j < J; j++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) lds_o[wave][i][(4 * g + r) * J + j] = acc[n][j][r] * f;
+      __syncthreads();
+
+      // out: threads over (row of the set, 4 elements)
+      constexpr int kQuads = D / 4;
+      for (unsigned e = threadIdx.x; e < ((unsigned)kSet << p.row_shift) * kQuads; e += kThreads) {
+        const unsigned rr = e / kQuads, d4 = e % kQuads, wb = rr / kSet << per_shift;
+        const unsigned in_unit = (rr / kSet * N + n) * kSet + rr % kSet, r = row0 + in_unit;
+        if (r >= p.rows) continue;
+        const float mx = lds_top[wb][rr % kSet];
+        float sum = 0;
+        f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+        for (unsigned w = 0; w < kWaves; w++) {
+          if (w >= per_tile) break;
+          sum += lds_l[wb + w][rr % kSet];
+          o += *(const f32x4*)&lds_o[wb + w][rr % kSet][4 * d4];
+        }
+        if (!kRanges || (opens && closes)) {
+          const unsigned token = r / p.group;
+          const int64_t hq = (int64_t)head * p.group + (r - token * p.group);
+          store_out(p.a, ((b * drafts + token) * p.a.q_heads + hq) * D + 4 * d4, finish(p.a, hq, mx, sum, o));
+        } else {
+          // a block has at most one part of a unit that a block before it
+          // opened (slot 0) and one of a unit that it opens itself (slot 1)
+          const int64_t slot = (2 * (int64_t)blockIdx.x + (opens ? 1 : 0)) * unit_rows + in_unit;
+          *(f32x4*)(p.part_o + slot * D + 4 * d4) = o;
+          if (d4 == 0) {
+            p.part_ml[2 * slot] = mx;
+            p.part_ml[2 * slot + 1] = sum;
+          }
+        }
+      }
+      if (n + 1 < N) __syncthreads();
+    }
+    // the next unit: the next row group, cache head or sequence
+    if constexpr (!kRanges) break;
+    x = u_first + (unsigned)last;
+    if (x >= end) break;
+    u_first = x;
+    if (++rg == p.row_groups) {
+      rg = 0;
+      if (++head == p.c.heads) {
+        head = 0;
+        s = tree_span(p, ++b);
+      }
+    }
+    x = uniform(x), u_first = uniform(u_first), head = uniform(head), rg = uniform(rg), b = uniform((int)b);
+    __syncthreads();  // it writes the same LDS
+  }
+}
+
+// Adds the parts of the unit of record blockIdx.x, kRowsEach rows a block (grid
+// y), each by kLines lines of D / 4 threads: a line adds every kLines-th part in
+// order, then the lines are added in order.
+template <int D, int kRowsEach>
+__global__ __launch_bounds__(256) void k_tree_join(TreeParams p, unsigned unit_rows) {
+  constexpr int kQuads = D / 4, kLines = 256 / kQuads / kRowsEach;
+  __shared__ f32x4 lo[256 / kQuads][kQuads];
+  __shared__ float ll[256 / kQuads], lm[256 / kQuads];
+  const int* w = p.parts + 4 * blockIdx.x;
+  const int parts = w[0];
+  if (parts < 2) return;
+  const unsigned k0 = w[1], unit = w[2];
+  const unsigned head = unit / p.row_groups % p.c.heads;
+  const int64_t b = unit / (p.row_groups * p.c.heads);
+  const int d4 = threadIdx.x % kQuads, at = threadIdx.x / kQuads, line = at % kLines;
+  const unsigned in_unit = blockIdx.y * kRowsEach + at / kLines, r = unit % p.row_groups * unit_rows + in_unit;
+  const bool live = in_unit < unit_rows && r < p.rows;
+  auto slot = [&](int part) { return (int64_t)(2 * (k0 + part) + (part == 0 ? 1 : 0)) * unit_rows + in_unit; };
+  float top = -INFINITY, sum = 0;
+  f32x4 o = {0, 0, 0, 0};
+  if (live) {
+    // a line's parts four at a time, all loads first
+    constexpr int kN = 4;
+    for (int k = line; k < parts; k += kN * kLines) {
+      f32x2 ml[kN];
+      f32x4 po[kN];
+#pragma unroll
+      for (int c = 0; c < kN; c++) {
+        const int64_t sl = slot(min(k + c * kLines, parts - 1));
+        ml[c] = *(const f32x2*)(p.part_ml + 2 * sl);
+        po[c] = *(const f32x4*)(p.part_o + sl * D + 4 * d4);
+      }
+      float m = top;
+#pragma unroll
+      for (int c = 0; c < kN; c++) m = fmaxf(m, ml[c].x);
+      const float ref = m > -INFINITY ? m : 0.0f, f0 = __builtin_amdgcn_exp2f(top - ref);
+      sum *= f0;
+      o *= f0;
+      top = m;
+#pragma unroll
+      for (int c = 0; c < kN; c++) {
+        if (k + c * kLines >= parts) continue;
+        const float f = __builtin_amdgcn_exp2f(ml[c].x - ref);
+        sum += f * ml[c].y;
+        o += po[c] * f;
+      }
+    }
+  }
+  if constexpr (kLines > 1) {
+    lo[at][d4] = o;
+    if (d4 == 0) ll[at] = sum, lm[at] = top;
+    __syncthreads();
+    if (line != 0) return;
+#pragma unroll
+    for (int k = 1; k < kLines; k++) top = fmaxf(top, lm[at + k]);
+    const float ref = top > -INFINITY ? top : 0.0f;
+    o = (f32x4){0, 0, 0, 0};
+    sum = 0;
+#pragma unroll
+    for (int k = 0; k < kLines; k++) {
+      const float f = __builtin_amdgcn_exp2f(lm[at + k] - ref);
+      o += lo[at + k][d4] * f;
+      sum += ll[at + k] * f;
+    }
+  }
+  if (!live) return;
+  const unsigned token = r / p.group;
+  const int64_t hq = (int64_t)head * p.group + (r - token * p.group);
+  store_out(p.a, ((b * p.a.drafts + token) * p.a.q_heads + hq) * D + 4 * d4, finish(p.a, hq, top, sum, o));
+}
+
+}  // namespace
+
+// Shape of a call's units: N sets of 16 rows a wave, 2^row_shift waves with rows
+// of their own.
+struct TreeUnits {
+  int sets;
+  unsigned row_shift, rows, row_groups;  // rows of a unit; units per sequence and cache head
+};
+static TreeUnits tree_units(int64_t drafts, unsigned q_heads, const KvShape& c) {
+  const int64_t rows = (int64_t)(q_heads / c.heads) * drafts;
+  const int sets = rows <= kSet ? 1 : 256 / (int)c.dim;
+  const int64_t waves = (rows + sets * kSet - 1) / (sets * kSet);
+  const unsigned shift = waves >= 3 ? 2 : waves - 1;
+  const unsigned unit = (unsigned)(sets * kSet) << shift;
+  return {sets, shift, unit, (unsigned)((rows + unit - 1) / unit)};
+}
+
+// Tiles of the longest sequence that the table can name.
+static int64_t tree_tiles(int64_t drafts, const KvShape& c, int64_t table_width, int64_t window, int64_t first) {
+  int64_t most = std::min<int64_t>(table_width << c.page_shift, kMaxLen);
+  int64_t tiles = (most + kTile - 1) / kTile;
+  if (window > 0 && window < most && first < most)
+    tiles = std::min(tiles, (first + kTile - 1) / kTile + (window + drafts) / kTile + 2);
+  return tiles;
+}
+
+// Whether blocks take ranges of the flattened tiles (and a second launch joins
+// the parts), or a unit each.
+static bool tree_ranges(int64_t units, int64_t tiles) { return tiles > (units >= 128 ? 64 : 32); }
+
+constexpr int64_t kRangeBlocks = 512;
+
+int64_t tree_attend_blocks(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
+                           int64_t window, int64_t first) {
+  const TreeUnits u = tree_units(drafts, q_heads, c);
+  const int64_t units = batch * c.heads * u.row_groups, tiles = tree_tiles(drafts, c, table_width, window, first);
+  // flattened tile indexes are 32 bits, with room for one range more
+  if (units > (0x7FFFFFFF - 4096) / tiles) return -1;
+  if (!tree_ranges(units, tiles)) return units;
+  const int64_t waves = kWaves >> u.row_shift;
+  return std::min<int64_t>(kRangeBlocks, units * ((tiles + waves - 1) / waves));
+}
+
+int64_t tree_attend_workspace(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
+                              int64_t window, int64_t first) {
+  const TreeUnits u = tree_units(drafts, q_heads, c);
+  if (!tree_ranges(batch * c.heads * u.row_groups, tree_tiles(drafts, c, table_width, window, first))) return 0;
+  const int64_t blocks = tree_attend_blocks(batch, drafts, q_heads, c, table_width, window, first);
+  return blocks * (16 + 2 * (int64_t)u.rows * (c.dim + 2) * 4);
+}
+
+template <int D>
+static void launch_join(const TreeParams& p, unsigned unit_rows, int64_t records, hipStream_t st) {
+  constexpr int kLines = 256 / (D / 4), kFew = kLines > 8 ? kLines / 8 : 1;
+  const unsigned rows = std::min(p.rows, unit_rows);
+  if (p.by_block)
+    k_tree_join<D, kLines><<<dim3((unsigned)records, (rows + kLines - 1) / kLines), dim3(256), 0, st>>>(p, unit_rows);
+  else
+    k_tree_join<D, kFew><<<dim3((unsigned)records, (rows + kFew - 1) / kFew), dim3(256), 0, st>>>(p, unit_rows);
+}
+
+hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, void* workspace, hipStream_t st) {
+  const TreeUnits u = tree_units(a.drafts, a.q_heads, c);
+  TreeParams p;
+  p.a = a;
+  p.c = c;
+  p.group = a.q_heads / c.heads;
+  p.rows = p.group * (unsigned)a.drafts;
+  p.row_groups = u.row_groups;
+  p.row_shift = u.row_shift;
+  const int64_t units = a.batch * c.heads * u.row_groups;
+  const int64_t blocks = tree_attend_blocks(a.batch, a.drafts, a.q_heads, c, a.table_width, a.window, a.first);
+  const bool ranges = tree_ranges(units, tree_tiles(a.drafts, c, a.table_width, a.window, a.first));
+  p.by_block = units >= blocks / 2;
+  p.parts = (int*)workspace;  // at most a record a block, in either case
+  p.part_o = (float*)((uint8_t*)workspace + blocks * 16);
+  p.part_ml = p.part_o + 2 * blocks * u.rows * c.dim;
+  const dim3 grid((unsigned)blocks), block(kThreads);
+#define MXQ_TREE_R(D, F, T, N) \
+  ranges ? k_tree_attend<D, F, T, N, true><<<grid, block, 0, st>>>(p) : k_tree_attend<D, F, T, N, false><<<grid, block, 0, st>>>(p)
+#define MXQ_TREE_N(D, N)                                                      \
+  do {                                                                        \
+    if (a.bf16_out && fp4) MXQ_TREE_R(D, true, 2, N);                         \
+    else if (a.bf16_out) MXQ_TREE_R(D, false, 2, N);                          \
+    else if (fp4) MXQ_TREE_R(D, true, 3, N);                                  \
+    else MXQ_TREE_R(D, false, 3, N);                                          \
+    if (ranges) launch_join<D>(p, u.rows, p.by_block ? blocks : units, st);   \
+  } while (0)
+  if (c.dim == 64 && u.sets == 1) MXQ_TREE_N(64, 1);
+  else if (c.dim == 64) MXQ_TREE_N(64, 4);
+  else if (c.dim == 128 && u.sets == 1) MXQ_TREE_N(128, 1);
+  else if (c.dim == 128) MXQ_TREE_N(128, 2);
+  else MXQ_TREE_N(256, 1);
+#undef MXQ_TREE_N
+#undef MXQ_TREE_R
+  return hipGetLastError();
+}
+
+}  // namespace mxq

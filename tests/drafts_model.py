@@ -71,3 +71,77 @@ def check_codes(q, s, y, span, fmt, what=""):
     rnd = model.e4m3_round if fmt == "mxfp8" else e2m1_round
     bad = ~((got >= rnd((b - w) * scale)) & (got <= rnd((b + w) * scale)))
     assert not bad.any(), f"{what}: {int(bad.sum())} codes off, first at {np.argwhere(bad)[0]}"
+
+
+# ------------------------------------------------------------------ attention of a tree
+
+def bits_of(mask):
+    """Truth values [batch, drafts, drafts] of masks [batch, drafts, words] of 64 bits."""
+    m = np.ascontiguousarray(mask).view(np.uint64)
+    drafts = m.shape[1]
+    at = np.arange(drafts)
+    return (m[:, :, at // 64] >> (at % 64).astype(np.uint64)) & np.uint64(1) != 0
+
+
+def mask_of(bits):
+    """The reverse: int64 words."""
+    bits = np.asarray(bits, dtype=bool)
+    batch, drafts = bits.shape[:2]
+    words = -(-drafts // 64)
+    wide = np.zeros((batch, drafts, 64 * words), dtype=np.uint64)
+    wide[:, :, :drafts] = bits
+    return (wide.reshape(batch, drafts, words, 64) << np.arange(64, dtype=np.uint64)).sum(-1, dtype=np.uint64).view(np.int64)
+
+
+def visible(context, bits, table_row, pages, page, window=0, first=0):
+    """What the tokens of one sequence see: truth values [drafts, n] over cache positions."""
+    drafts = len(bits)
+    most = len(table_row) * page
+    n = min(max(int(context), 0), most)
+    end = min(n + drafts, most)
+    depth = np.array([bits[i, :i].sum() for i in range(drafts)])
+    see = np.zeros((drafts, end), dtype=bool)
+    place = np.concatenate((np.arange(n), n + depth))[:end]
+    see[:, :n] = True
+    see[:, n:] = bits[:, :end - n]
+    if window:
+        see &= ((n + depth)[:, None] - place[None] < window) | (place[None] < first)
+    named = (table_row >= 0) & (table_row < pages)
+    return see & named[np.arange(end) // page][None]
+
+
+def tree_attention(q, cache, table, context, bits, fmt, scale, window=0, first=0, sinks=None):
+    """(out, size, mag) in float64 as serving_model.attention, for q [batch, drafts, heads, D]."""
+    q = np.asarray(q, dtype=np.float64)
+    batch, drafts, heads, d = q.shape
+    pages, hkv, page = cache[0].shape[:3]
+    out, size, mag = np.zeros_like(q), np.zeros_like(q), np.zeros(q.shape[:3])
+    group = heads // hkv
+    for b in range(batch):
+        see = visible(context[b], bits[b], table[b], pages, page, window, first)
+        at = np.flatnonzero(see.any(0))
+        if not len(at):
+            continue
+        see = see[:, at]
+        pg, pos = table[b, at // page], at % page
+        kq, ks, vq, vs = cache
+        vst = vs.transpose(0, 3, 1, 2)
+        rows = []
+        for c, s in ((kq[pg, :, pos], ks[pg, :, pos]), (vq[pg, :, pos], vst[pg, pos])):
+            x = model.dequantize_rows(np.ascontiguousarray(c).reshape(-1, c.shape[-1]),
+                                      np.ascontiguousarray(s).reshape(-1, s.shape[-1]), fmt)
+            rows.append(np.asarray(x, dtype=np.float64).reshape(len(at), hkv, d))
+        for h in range(heads):
+            k, v = (r[:, h // group] for r in rows)
+            s = np.where(see, (q[b, :, h] @ k.T) * scale, -np.inf)
+            mag[b, :, h] = np.where(see, np.abs(q[b, :, h]) @ np.abs(k).T, 0).max(1) * abs(scale)
+            some = see.any(1)
+            top = np.where(some, s.max(1), 0.0)
+            if sinks is not None:
+                top = np.where(some, np.maximum(top, sinks[h]), 0.0)
+            p = np.exp(s - top[:, None])
+            total = p.sum(1) + (np.exp(sinks[h] - top) if sinks is not None else 0.0)
+            total = np.where(some, total, 1.0)
+            out[b, :, h] = p @ v / total[:, None]
+            size[b, :, h] = p @ np.abs(v) / total[:, None]
+    return out, size, mag

@@ -75,3 +75,85 @@ def test_binding_rope():
                      ((q, k, k, n, p, f), dict(out=torch.zeros(5, 4, 64)))):
         with pytest.raises(TypeError):
             mxq.rope_append(c, *args, **kw)
+
+
+# ------------------------------------------------------------------ attention of a tree
+
+def tree(lib, q=A, qs=1024, kq=A, ks=B, vq=C, vs=D, table=E, width=4, stride=4, context=A, mask=B, sinks=NULL, batch=2,
+         drafts=5, qh=8, pages=9, heads=2, page=16, dim=128, fmt=0, scale=0.1, window=0, first=0, ws=A,
+         ws_bytes=1 << 30, out=B, dt=1):
+    return lib.mxq_tree_attention(q, qs, kq, ks, vq, vs, table, width, stride, context, mask, sinks, batch, drafts, qh,
+                                  pages, heads, page, dim, fmt, scale, window, first, ws, ws_bytes, out, dt, NULL)
+
+
+def test_tree_refusals(lib):
+    for bad in (dict(q=NULL), dict(table=NULL), dict(context=NULL), dict(mask=NULL), dict(out=NULL), dict(kq=NULL),
+                dict(vs=NULL), dict(batch=0), dict(drafts=0), dict(drafts=-1), dict(drafts=257), dict(qh=7), dict(qh=0),
+                dict(heads=3), dict(dim=96), dict(dim=32), dict(dim=512), dict(page=20), dict(width=0), dict(stride=3),
+                dict(qs=1016), dict(qs=1028), dict(window=-1), dict(first=-1), dict(scale=float("nan")),
+                dict(scale=float("inf")), dict(dt=2), dict(fmt=2), dict(batch=2 ** 40), dict(qs=1 << 60),
+                dict(width=2 ** 31, stride=2 ** 31), dict(batch=1 << 24), dict(batch=1 << 21, width=1 << 24, stride=1 << 24)):
+        assert tree(lib, **bad) == INVALID, bad
+    for bad in (dict(q=MIS), dict(out=MIS), dict(kq=MIS), dict(vs=MIS), dict(table=MIS2), dict(context=MIS2),
+                dict(sinks=MIS2), dict(mask=MIS4)):
+        assert tree(lib, **bad) == MISALIGNED, bad
+
+
+def tree_workspace(lib, batch, drafts, qh, heads, page, dim, width, window=0, first=0):
+    n = ctypes.c_int64(-1)
+    code = lib.mxq_tree_attention_workspace(batch, drafts, qh, heads, page, dim, width, window, first, ctypes.byref(n))
+    return code, n.value
+
+
+def test_tree_workspace(lib):
+    code, need = tree_workspace(lib, 1, 5, 8, 2, 16, 128, 4096)
+    assert code == 0 and need > 0 and need % 4 == 0
+    big = dict(batch=1, width=4096, stride=4096, qs=1024)
+    assert tree(lib, ws_bytes=need - 1, **big) == INVALID
+    assert tree(lib, ws=NULL, ws_bytes=need, **big) == INVALID
+    assert tree(lib, ws=MIS, ws_bytes=need, **big) == MISALIGNED
+    assert tree_workspace(lib, 1, 5, 8, 2, 16, 128, 1) == (0, 0)  # nothing to split
+    assert tree_workspace(lib, 1, 5, 8, 2, 16, 128, 4096, 64)[1] < need  # a window bounds what is split
+    assert tree_workspace(lib, 1, 5, 8, 2, 16, 128, 4096, 64, 1 << 40)[1] == need  # first tokens that reach all
+    assert tree_workspace(lib, 1, 5, 8, 3, 16, 128, 4096)[0] == INVALID
+    assert tree_workspace(lib, 1, 0, 8, 2, 16, 128, 4096)[0] == INVALID
+    assert lib.mxq_tree_attention_workspace(1, 5, 8, 2, 16, 128, 4, 0, 0, None) == INVALID
+
+
+def test_tree_no_device(lib):
+    if torch.cuda.device_count() > 0:
+        pytest.skip("a GPU is present: this case is only safe without one")
+    assert tree(lib) == NOT_SUPPORTED
+
+
+def test_binding_tree():
+    c = mxq.kv_cache(3, 16, 2, 64, device="cpu")
+    q, table = torch.zeros(6, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32)
+    n, m = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, 1, dtype=torch.int64)
+    for a, t, x, k, kw in ((q[:, :3], table, n, m, {}), (q[:5], table, n, m, {}), (q, table[:1], n, m, {}),
+                           (q, table, n[:1], m, {}), (q, table.t().contiguous().t(), n, m, {}),
+                           (q[..., :32], table, n, m, {}), (q, table, n, m[..., 0], {}),
+                           (q, table, n, torch.zeros(2, 3, 2, dtype=torch.int64), {}),
+                           (q, table, n, m, dict(sinks=torch.zeros(3))), (q, table, n, m, {}),
+                           (q, table, n, m, dict(out=torch.zeros(6, 4, 32, dtype=torch.bfloat16)))):
+        with pytest.raises(ValueError):
+            mxq.tree_attention(a, c, t, x, k, **kw)
+    for a, t, x, k, kw in ((q.float(), table, n, m, {}), (q, table.long(), n, m, {}), (q, table, n.long(), m, {}),
+                           (q, table, n, m.int(), {}), (q, table, n, m, dict(out_dtype=torch.float16)),
+                           (q, table, n, m, dict(sinks=torch.zeros(4, dtype=torch.bfloat16)))):
+        with pytest.raises(TypeError):
+            mxq.tree_attention(a, c, t, x, k, **kw)
+    for kw in (dict(window=-1), dict(first=-1)):
+        with pytest.raises(mxq.MXQError):
+            mxq.tree_attention(q, c, table, n, m, **kw)
+
+
+def test_tree_mask():
+    assert mxq.tree_mask([-1, 0, 0, 1], device="cpu").tolist() == [[[1], [3], [5], [11]]]
+    assert mxq.tree_mask(torch.tensor([[-1, 0], [-1, -1]]), device="cpu").tolist() == [[[1], [3]], [[1], [2]]]
+    wide = mxq.tree_mask(list(range(-1, 65)), device="cpu")
+    assert wide.shape == (1, 66, 2) and wide[0, 63].tolist() == [-1, 0] and wide[0, 65].tolist() == [-1, 3]
+    assert mxq.tree_mask([[-1], []], device="cpu").tolist() == [[[1]], [[0]]]
+    for bad in ([0], [-1, 1], [-2], [[-1, 0, 5]], []):
+        with pytest.raises(ValueError):
+            mxq.tree_mask(bad, device="cpu")

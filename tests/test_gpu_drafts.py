@@ -160,3 +160,302 @@ def test_rope_no_finite_angle_gives_nan():
     want = torch.zeros(2, 64, dtype=torch.bool)
     want[:, [3, 35, 9, 41, 20, 52]] = True
     assert torch.equal(nan, want)
+
+
+# ------------------------------------------------------------------ attention of a tree
+
+NAN_BYTES = {"mxfp8": 0x7F, "mxfp4": 0x77}
+
+
+def random_trees(rng, batch, drafts, short=True):
+    """Bits [batch, drafts, drafts] of random trees, some shorter and padded."""
+    bits = np.zeros((batch, drafts, drafts), dtype=bool)
+    for b in range(batch):
+        n = int(rng.integers(0, drafts + 1)) if short and b % 3 == 2 else drafts
+        for i in range(n):
+            p = int(rng.integers(-1, i))if i and rng.random() < 0.4 else i - 1
+            if p >= 0:
+                bits[b, i] = bits[b, p]
+            bits[b, i, i] = True
+    return bits
+
+
+def tree_bound(ref, size, mag, n, d, out):
+    bound = size * (2 * (d + 4) * U * mag[..., None] + 2.0 ** -21 + (n / 8 + 64) * U)
+    if out == torch.bfloat16:
+        bound = bound + size * 2.0 ** -16
+        bound = bound + (np.abs(ref) + bound) * 2.0 ** -8
+    return bound
+
+
+def tree_inputs(seed, context, bits, heads, group, d, page, fmt, window=0, first=0, holes=(), extra_width=2):
+    """(cache, table, stored q, q64): a cache that is NaN wherever no token of the call looks."""
+    rng = np.random.default_rng(seed)
+    batch, drafts = bits.shape[:2]
+    counts = [-(-(max(n, 0) + drafts) // page) for n in context]
+    pages = sum(counts) + 2
+    cache = filled_cache(rng, pages, page, heads, d, fmt)
+    order = rng.permutation(pages).astype(np.int32)
+    table = np.full((batch, max(counts) + extra_width), -7, dtype=np.int32)
+    at = 0
+    for b, c in enumerate(counts):
+        table[b, :c] = order[at:at + c]
+        table[b, c:] = 2 ** 31 - 1 if b % 2 else -1  # names no page
+        at += c
+    for b, p in holes:
+        table[b, p] = pages if p % 2 else -1
+    seen = np.zeros((pages, page), dtype=bool)
+    for b in range(batch):
+        t = np.flatnonzero(visible_any(context[b], bits[b], table[b], pages, page, window, first))
+        seen[table[b, t // page], t % page] = True
+    kq, ks, vq, vs = cache
+    for a in (kq, vq):
+        a.transpose(0, 2, 1, 3)[~seen] = NAN_BYTES[fmt]
+    ks.transpose(0, 2, 1, 3)[~seen] = 255
+    vs.transpose(0, 3, 1, 2)[~seen] = 255
+    q, q64 = stored(rng.standard_normal((batch * drafts, heads * group * d + 3 * d)), "bf16")
+    return cache, table, q, q64[:, d:d + heads * group * d].reshape(batch, drafts, heads * group, d)
+
+
+def visible_any(*args):
+    return dm.visible(*args).any(0)
+
+
+def tree_case(seed, context, drafts, heads, group, d, page, fmt, out=torch.float32, window=0, first=0, sinks=False,
+              scale=None, bits=None, holes=(), extra_width=2):
+    rng = np.random.default_rng(seed + 1000)
+    if bits is None:
+        bits = random_trees(rng, len(context), drafts)
+    cache, table, q, q64 = tree_inputs(seed, context, bits, heads, group, d, page, fmt, window, first, holes, extra_width)
+    qd = dev(q)[:, d:d + heads * group * d].unflatten(1, (heads * group, d))
+    sk = rng.standard_normal(heads * group).astype(np.float32) * 2 if sinks else None
+    y = mxq.tree_attention(qd, on_device(cache), dev(table), dev(np.array(context, dtype=np.int32)),
+                           dev(dm.mask_of(bits)), scale=scale, window=window, first=first,
+                           sinks=dev(sk) if sinks else None, out_dtype=out)
+    torch.cuda.synchronize()
+    ref, size, mag = dm.tree_attention(q64, cache, table, context, bits, fmt, d ** -0.5 if scale is None else scale,
+                                       window, first, sk)
+    got = oracle.to_f64(host(y)).reshape(ref.shape)
+    bound = tree_bound(ref, size, mag, max(context) + drafts, d, out)
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), (f"{int(bad.sum())} of {bad.size} off, first {np.argwhere(bad)[0]}: "
+                           f"{got[bad][0]} for {ref[bad][0]}, bound {bound[bad][0]}")
+    return got
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("drafts", [1, 6])
+def test_tree_formats_and_lengths(drafts, page, d, fmt, out):
+    """Contexts around tile and page ends, one of nothing among them."""
+    tree_case(d + page, [0, 1, 15, 16, 17, 31, 32, 33, 63, 65, 127, 129, 300], drafts, 2, 3, d, page, fmt, out)
+
+
+@pytest.mark.parametrize("drafts", [1, 2, 3, 7, 15, 16, 17, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 200, 256])
+def test_tree_drafts(drafts):
+    """Trees below, at and past 32 and 64 tokens, at contexts that put them anywhere in a tile."""
+    tree_case(drafts, [0, 5, 47, 100], drafts, 1, 2, 64, 16, "mxfp8")
+    tree_case(drafts, [31, 64], drafts, 2, 1, 128, 32, "mxfp4", torch.bfloat16)
+
+
+@pytest.mark.parametrize("heads,group", [(1, 1), (3, 1), (2, 8), (1, 15), (2, 16), (1, 17), (1, 24), (1, 40), (1, 64),
+                                         (1, 71), (1, 128)])
+@pytest.mark.parametrize("drafts", [1, 3, 11])
+def test_tree_head_layouts(heads, group, drafts):
+    """Rows of one, several and many sets and units."""
+    tree_case(group, [5, 97, 261], drafts, heads, group, 64, 16, "mxfp8")
+    tree_case(group, [130], drafts, heads, group, 128, 32, "mxfp4", torch.bfloat16)
+    tree_case(group, [70], drafts, heads, group, 256, 64, "mxfp8")
+
+
+@pytest.mark.parametrize("window", [1, 2, 5, 16, 31, 33, 100, 128, 5000])
+@pytest.mark.parametrize("first", [0, 1, 4, 31, 32, 33, 100, 1000])
+def test_tree_window_and_first(window, first):
+    """Windows within the drafted tokens, within a tile and past the sequence, with
+    first tokens that lie before, at and inside the window."""
+    tree_case(window, [0, 1, 33, 100, 128, 129, 517], 9, 2, 4, 64, 16, "mxfp8", window=window, first=first,
+              sinks=first % 2 == 0)
+
+
+def test_tree_sinks():
+    tree_case(11, [1500, 3, 0, 700], 5, 2, 8, 128, 16, "mxfp8", sinks=True)
+    tree_case(12, [1500], 12, 2, 8, 128, 64, "mxfp4", torch.bfloat16, sinks=True)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_tree_any_masks(seed):
+    """Masks that are no trees: bits ahead, no bit for the token itself, nothing at all."""
+    rng = np.random.default_rng(seed)
+    drafts = [3, 40, 70, 256][seed]
+    bits = rng.random((5, drafts, drafts)) < np.array([0.5, 0.02, 0.95, 0.0, 1.0])[:, None, None]
+    tree_case(seed, [0, 0, 77, 0, 31], drafts, 1, 4, 64, 16, "mxfp8", bits=bits)
+    tree_case(seed, [0, 9, 77, 40, 31], drafts, 1, 4, 64, 16, "mxfp4", bits=bits, window=7, first=3, sinks=True)
+
+
+def test_tree_rows_that_see_nothing():
+    """Zeros, with and without a sink, beside rows that see something."""
+    bits = np.zeros((3, 5, 5), dtype=bool)
+    bits[0, 2, 2] = bits[2, 4, 1] = True
+    for sinks in (False, True):
+        y = tree_case(1, [0, 0, 0], 5, 2, 3, 64, 16, "mxfp8", bits=bits, sinks=sinks)
+        some = np.abs(y).sum((2, 3)) > 0
+        assert some.tolist() == [[False, False, True, False, False], [False] * 5, [False] * 4 + [True]]
+    tree_case(2, [100, 64, 0], 5, 1, 2, 64, 16, "mxfp8", bits=bits, window=1)  # nothing but what the mask names
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_tree_pages_the_table_does_not_name(fmt):
+    """Entries outside the cache hide their positions, a whole sequence's and the drafted tokens' among them."""
+    tree_case(5, [100, 40, 70, 16], 4, 2, 2, 64, 16, fmt,
+              holes=[(0, 0), (0, 3), (1, 2), (2, 1), (2, 4), (3, 0), (3, 1)])
+
+
+def test_tree_contexts_past_the_table():
+    """Contexts at, past and just below what the table names: drafted tokens beyond it are not there."""
+    rng = np.random.default_rng(0)
+    cache = filled_cache(rng, 3, 16, 1, 64, "mxfp8")
+    table = np.array([[2, 0]] * 5, dtype=np.int32)
+    context = [2 ** 31 - 1, -5, 32, 30, 31]
+    bits = np.repeat(np.tril(np.ones((1, 3, 3), dtype=bool)), 5, axis=0)
+    qb, q64 = stored(rng.standard_normal((15, 2, 64)), "bf16")
+    for window in (0, 1, 2, 20):
+        y = mxq.tree_attention(dev(qb), on_device(cache), dev(table), dev(np.array(context, dtype=np.int32)),
+                               dev(dm.mask_of(bits)), window=window, out_dtype=torch.float32)
+        ref, size, mag = dm.tree_attention(q64.reshape(5, 3, 2, 64), cache, table, context, bits, "mxfp8", 0.125, window)
+        assert (np.abs(host(y).reshape(ref.shape) - ref) <= tree_bound(ref, size, mag, 35, 64, torch.float32)).all()
+
+
+@pytest.mark.parametrize("seed,context,drafts,heads,group,d,page,fmt,out", [
+    (1, [3000, 5, 1200, 0], 5, 2, 4, 64, 16, "mxfp8", torch.float32),
+    (2, [2500, 2500], 16, 2, 8, 128, 64, "mxfp8", torch.bfloat16),       # rows of one unit
+    (3, [4100], 64, 1, 8, 128, 16, "mxfp8", torch.float32),              # several row groups
+    (4, [1500, 900], 3, 1, 2, 256, 32, "mxfp4", torch.float32),
+    (5, [2000, 1999], 100, 1, 3, 64, 128, "mxfp4", torch.bfloat16),
+    (6, [1400] * 70, 2, 2, 2, 64, 16, "mxfp8", torch.float32),           # several units a range
+    (7, [1200, 40] * 150, 1, 1, 3, 64, 16, "mxfp4", torch.float32),      # more sequences than threads of a block
+])
+def test_tree_ranges(seed, context, drafts, heads, group, d, page, fmt, out):
+    """Ranges that end inside units, and the join of their parts."""
+    tree_case(seed, context, drafts, heads, group, d, page, fmt, out, sinks=seed % 2 == 0)
+
+
+@pytest.mark.parametrize("window,first", [(1500, 0), (1500, 40), (1100, 1100)])
+def test_tree_window_over_ranges(window, first):
+    tree_case(window, [4000, 100, 1600], 6, 2, 4, 64, 16, "mxfp8", window=window, first=first)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_tree_random(seed):
+    rng = np.random.default_rng(seed + 500)
+    drafts = int(np.exp(rng.uniform(0, np.log(257))))
+    heads, group = int(rng.integers(1, 4)), int(rng.integers(1, 10))
+    context = [int(np.exp(rng.uniform(0, np.log(2500)))) - 1 for _ in range(int(rng.integers(1, 6)))]
+    windowed = rng.random() < 0.5
+    tree_case(seed, context, drafts, heads, group, int(rng.choice([64, 128, 256])), int(rng.choice([16, 32, 128, 1024])),
+              str(rng.choice(["mxfp8", "mxfp4"])), torch.bfloat16 if seed % 2 else torch.float32,
+              window=int(np.exp(rng.uniform(0, np.log(2000)))) if windowed else 0,
+              first=int(rng.integers(0, 200)) if windowed else 0, sinks=bool(rng.random() < 0.3),
+              scale=[None, None, -0.2, 0.0][seed % 4])
+
+
+def test_tree_of_one_token_is_paged_attention():
+    """A tree of one token and the attention of one new token, each within its bound."""
+    context = np.array([0, 70, 1033, 2500], dtype=np.int32)
+    bits = np.ones((4, 1, 1), dtype=bool)
+    cache, table, q, q64 = tree_inputs(3, context, bits, 2, 8, 128, 64, "mxfp8")
+    qd, c = dev(q)[:, 128:128 * 17].unflatten(1, (16, 128)), on_device(cache)
+    a = mxq.tree_attention(qd, c, dev(table), dev(context), dev(dm.mask_of(bits)), out_dtype=torch.float32)
+    b = mxq.paged_attention(qd, c, dev(table), dev(context + 1), out_dtype=torch.float32)
+    ref, size, mag = dm.tree_attention(q64, cache, table, context, bits, "mxfp8", 128 ** -0.5)
+    bound = tree_bound(ref, size, mag, 2501, 128, torch.float32)
+    for y in (a, b):
+        assert (np.abs(host(y).reshape(ref.shape) - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("context,group,drafts", [([40, 0, 33], 4, 6), ([4000, 0, 33], 4, 6), ([70, 0, 5], 8, 40)])
+def test_tree_nan_reaches_who_sees_it(context, group, drafts, out):
+    """A NaN in a token's query, or in a key or value that it sees, gives NaN there
+    and nowhere else: the same key and value are masked for other rows of the
+    same product."""
+    heads, d, page = 2, 64, 16
+    rng = np.random.default_rng(drafts)
+    bits = random_trees(rng, 3, drafts, short=False)
+    bits[:, 1, 0] = False  # token 1 does not see token 0
+    cache, table, q, _ = tree_inputs(9, context, bits, heads, group, d, page, "mxfp8")
+    n, mask = dev(np.array(context, dtype=np.int32)), dev(dm.mask_of(bits))
+
+    def call(qb=q, c=cache, **kw):
+        qd = dev(qb)[:, d:d + heads * group * d].unflatten(1, (heads * group, d))
+        y = mxq.tree_attention(qd, on_device(c), dev(table), n, mask, out_dtype=out, **kw)
+        return oracle.to_f64(host(y)).reshape(3, drafts, heads * group, d)
+
+    clean = call()
+    assert np.isfinite(clean).all()
+    bad = q.copy()
+    row = 2 * drafts + 1
+    bad[row, d + 3 * d + 5] = 0x7FC0  # head 3 of token 1 of the last sequence
+    y = call(bad)
+    assert np.isnan(y[2, 1, 3]).all()
+    y[2, 1, 3] = clean[2, 1, 3]
+    assert np.array_equal(y, clean)
+    for b in range(3):
+        for j in (0, drafts // 2, drafts - 1):
+            at = context[b] + j
+            pg, pos = table[b, at // page], at % page
+            sees = bits[b, :, j]
+            for kind in range(3):  # a key of head 1, a value and a value's scale of head 0
+                c = [a.copy() for a in cache]
+                if kind == 0:
+                    c[0][pg, 1, pos, 7] = 0xFF
+                    where = np.zeros(clean.shape, dtype=bool)
+                    where[b, sees, group:] = True
+                elif kind == 1:
+                    c[2][pg, 0, pos, 9] = 0x7F
+                    where = np.zeros(clean.shape, dtype=bool)
+                    where[b, sees, :group, 9] = True
+                else:
+                    c[3][pg, 0, 1, pos] = 255
+                    where = None
+                y = call(c=c)
+                if where is None:  # an infinite scale: infinite or NaN where it is seen
+                    where = ~np.isfinite(y)
+                    assert not where[b, ~sees].any() and not np.delete(where, b, 0).any()
+                    assert where[b, sees, :group, 32:].any() == sees.any() and not where[..., :32].any()
+                    assert not where[:, :, group:].any()
+                else:
+                    assert np.array_equal(np.isnan(y), where), (b, j, kind)
+                assert np.array_equal(y[~where], clean[~where])
+
+
+def test_tree_workspace_table_slice_and_repeat():
+    """A caller's workspace (of arbitrary content), a sliced table and a repeated
+    call give the same bits, and nothing past the output is written."""
+    rng = np.random.default_rng(9)
+    bits = random_trees(rng, 2, 20)
+    context = np.array([3000, 1700], dtype=np.int32)
+    cache, table, q, _ = tree_inputs(1, context, bits, 2, 4, 64, 16, "mxfp8")
+    c, t, n, m = on_device(cache), dev(table), dev(context), dev(dm.mask_of(bits))
+    qd = dev(q)[:, 64:64 * 9].unflatten(1, (8, 64))
+    a = mxq.tree_attention(qd, c, t, n, m)
+    wide = torch.cat((t, t[:, :5]), 1)
+    b = mxq.tree_attention(qd, c, wide[:, :t.shape[1]], n, m)
+    ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")
+    e = mxq.tree_attention(qd, c, t, n, m, workspace=ws)
+    room = torch.full((42, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = room[1:41]
+    assert mxq.tree_attention(qd, c, t, n, m, workspace=ws, out=out) is out
+    assert torch.equal(a, b) and torch.equal(a, e) and torch.equal(a, out)
+    assert (room[0] == 7).all() and (room[41] == 7).all()
+
+
+def test_tree_mask_of_parents():
+    """The helper's masks, and a ragged batch of trees through the operator."""
+    m = mxq.tree_mask([[-1, 0, 0, 2], [-1, -1]])
+    assert m.cpu().tolist() == [[[1], [3], [5], [13]], [[1], [2], [0], [0]]]
+    chain = mxq.tree_mask(list(range(-1, 69)))
+    assert np.array_equal(dm.bits_of(host(chain)), np.tril(np.ones((1, 70, 70), dtype=bool)))
+    bits = dm.bits_of(host(m))
+    tree_case(3, [20, 0], 4, 1, 2, 64, 16, "mxfp8", bits=bits)
