@@ -491,6 +491,37 @@ MXQ_API mxq_status mxq_tree_attention(const void *q, int64_t q_stride, const uin
                               int64_t window, int64_t first, void *workspace, int64_t workspace_bytes, void *out,
                               mxq_dtype odt, hipStream_t stream);
 
+/*
+ * A token of each row of logits.  With weights w_i = exp((x_i - max x) /
+ * temperature), and the tokens ordered by logit, the largest first, equal ones
+ * by index, what may be drawn is the shortest of three prefixes of that order:
+ * the first top_k tokens; of them the fewest whose weights reach top_p of
+ * theirs; those of weight min_p and more.  tokens[r] is the first token by index
+ * for which the running sum of the weights that may be drawn passes u[r] times
+ * their sum, and shares[r] its weight's share of that sum.
+ * temperature not above 0: the largest logit (the first of equal ones), share 1.
+ * top_k <= 0 or >= vocab, top_p >= 1 and min_p <= 0 leave all tokens; top_p <= 0
+ * leaves one, min_p >= 1 the largest.  u is cut to [0, 1]; at 1 the last token
+ * that may be drawn is taken.  A row that holds a NaN or +inf, or nothing but
+ * -inf, gives token -1 and a share of NaN.
+ * Weights are fp64 and are summed as whole multiples of 2^-43 of the largest, so
+ * results do not depend on the order of summing; weights below 2^-44 of the
+ * largest count as 0.
+ * logits of type dt, row r at logits + r * stride elements (stride >= vocab, any
+ * alignment of its type); u fp32 [rows].  Each setting is an array [rows], or one
+ * value for all rows where its array is NULL (top_k int32, the others fp32; the
+ * value must not be NaN).  tokens int32 [rows], shares fp32 [rows].  vocab <=
+ * 2^20, rows <= 2^20.  workspace: 16-byte aligned, at least the bytes that
+ * mxq_sample_workspace gives (may be NULL for 0); its content need not be
+ * prepared, and it may be reused by any later call on the same stream.
+ */
+MXQ_API mxq_status mxq_sample_workspace(int64_t rows, int64_t vocab, int64_t *bytes);
+MXQ_API mxq_status mxq_sample(const void *logits, mxq_dtype dt, int64_t stride, int64_t rows, int64_t vocab,
+                      const float *u, const float *temperature_of, float temperature, const int32_t *top_k_of,
+                      int64_t top_k, const float *top_p_of, float top_p, const float *min_p_of, float min_p,
+                      void *workspace, int64_t workspace_bytes, int32_t *tokens, float *shares,
+                      hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

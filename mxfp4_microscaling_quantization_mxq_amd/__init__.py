@@ -26,6 +26,7 @@ or, for tokens with positions and for drafted tokens that one step checks:
 
     q = rope_append(cache, q, k, v, slots, positions, freqs)   # rotate, quantize new tokens into their slots
     o = tree_attention(q, cache, table, context, mask)         # several drafted tokens per sequence
+    tokens, shares = sample(logits, u, temperature=0.8, top_p=0.95)   # draw a token of each row
 
 Every tensor argument is checked before anything is enqueued: dtype, shape
 (scales and caller-supplied outputs must match the operands exactly),
@@ -59,6 +60,7 @@ API = (
     "mxq_gemm_w4a8", "mxq_gemm_w4a8_dynamic", "nvq_quantize", "nvq_dequantize", "nvq_gemm", "mxq_transfp4_quantize", "mxq_transfp4_dequantize",
     "mxq_rmsnorm_quantize_fp8", "mxq_kv_append", "mxq_kv_read", "mxq_paged_attention_workspace", "mxq_paged_attention",
     "mxq_rope_append", "mxq_tree_attention_workspace", "mxq_tree_attention",
+    "mxq_sample_workspace", "mxq_sample",
 )
 
 
@@ -114,6 +116,8 @@ def capi() -> ctypes.CDLL:
     lib.mxq_tree_attention_workspace.argtypes = [I64, I64, I64, I64, I64, I64, I64, I64, I64, ctypes.POINTER(I64)]
     lib.mxq_tree_attention.argtypes = [P, I64, P, P, P, P, P, I64, I64, P, P, P, I64, I64, I64, I64, I64, I64, I64, I, F,
                                        I64, I64, P, I64, P, I, P]
+    lib.mxq_sample_workspace.argtypes = [I64, I64, ctypes.POINTER(I64)]
+    lib.mxq_sample.argtypes = [P, I, I64, I64, I64, P, P, F, P, I64, P, F, P, F, P, I64, P, P, P]
     for name in API[2:]:
         getattr(lib, name).restype = I
     _lib = lib
@@ -907,6 +911,75 @@ def tree_attention(q, cache, table, context, mask, scale=None, window=0, first=0
     if code != 0:
         _check(code, "mxq_tree_attention")
     return out
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, shares=None, workspace=None):
+    """Draw a token of each row: (tokens int32 [rows], shares fp32 [rows]).
+
+    logits [rows, vocab] bf16 or fp32 (row stride free); u [rows] fp32 random
+    numbers in [0, 1).  Weights are exp((logit - largest) / temperature), ordered
+    by logit, equal ones by index; what may be drawn is the shortest of three
+    prefixes of that order: top_k tokens, of them the fewest whose weights reach
+    top_p of theirs, and those of weight min_p and more (of the largest).  The
+    token is the first by index where the running sum of these weights passes u
+    times their sum; its share is its weight over that sum.  temperature 0: the
+    largest.  top_k 0, top_p 1 and min_p 0 leave all.  Each setting is a number or
+    a tensor [rows] (top_k int32, the others fp32).  A row with a NaN or +inf, or
+    nothing but -inf, gives token -1 and share NaN."""
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError(f"logits must be a torch.Tensor, got {type(logits).__name__}")
+    code = _dtype_code(logits.dtype)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must have shape [rows, vocab] with contiguous rows, got {tuple(logits.shape)}")
+    dev = logits.get_device()
+    rows, vocab = logits.shape
+    stride = logits.stride(0) if rows > 1 else vocab
+    if not _same(u, torch.float32, (rows,), dev):
+        _need(u, "u", torch.float32, (rows,))
+    on = {"logits": logits, "u": u}
+    given = []
+    for name, v, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            if not _same(v, dt, (rows,), dev):
+                _need(v, name, dt, (rows,))
+            on[name] = v
+            given += [v.data_ptr(), 0]
+        else:
+            given += [None, v]
+    if tokens is None:
+        tokens = logits.new_empty(rows, dtype=torch.int32)
+    elif not _same(tokens, torch.int32, (rows,), dev):
+        _need(tokens, "tokens", torch.int32, (rows,))
+    if shares is None:
+        shares = logits.new_empty(rows, dtype=torch.float32)
+    elif not _same(shares, torch.float32, (rows,), dev):
+        _need(shares, "shares", torch.float32, (rows,))
+    on["tokens"], on["shares"] = tokens, shares
+    lib = capi()
+    need = ctypes.c_int64()
+    status = lib.mxq_sample_workspace(rows, vocab, ctypes.byref(need))
+    if status != 0:
+        _check(status, "mxq_sample_workspace")
+    need, wp = need.value, None
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, ndim=1)
+        on["workspace"] = workspace
+        need, least = workspace.shape[0], need
+        if need < least:
+            raise ValueError(f"workspace has {need} bytes, {least} are needed")
+        wp = workspace.data_ptr()
+    elif need:
+        workspace = logits.new_empty(need, dtype=torch.uint8)
+        wp = workspace.data_ptr()
+    if dev < 0 or any(t.get_device() != dev for t in on.values()):
+        _on_device(**on)
+    status = lib.mxq_sample(logits.data_ptr(), code, stride, rows, vocab, u.data_ptr(), *given, wp, need,
+                            tokens.data_ptr(), shares.data_ptr(), _stream(dev))
+    if status != 0:
+        _check(status, "mxq_sample")
+    return tokens, shares
 
 
 from . import nvq  # noqa: E402  (the NVFP4 names: nvq.quantize / nvq.dequantize / nvq.gemm)

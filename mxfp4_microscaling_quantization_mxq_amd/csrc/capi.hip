@@ -511,4 +511,46 @@ mxq_status mxq_tree_attention(const void* q, int64_t q_stride, const uint8_t* kq
   return launched(mxq::launch_tree_attend(a, c, fmt == MXQ_MXFP4, workspace, stream));
 }
 
+static bool sample_sizes(int64_t rows, int64_t vocab) {
+  return rows >= 1 && rows <= (1 << 20) && vocab >= 1 && vocab <= (1 << 20);
+}
+
+mxq_status mxq_sample_workspace(int64_t rows, int64_t vocab, int64_t* bytes) {
+  if (!bytes || !sample_sizes(rows, vocab)) return MXQ_ERROR_INVALID_VALUE;
+  *bytes = mxq::sample_workspace(rows, vocab);
+  return MXQ_SUCCESS;
+}
+
+mxq_status mxq_sample(const void* logits, mxq_dtype dt, int64_t stride, int64_t rows, int64_t vocab, const float* u,
+                      const float* temperature_of, float temperature, const int32_t* top_k_of, int64_t top_k,
+                      const float* top_p_of, float top_p, const float* min_p_of, float min_p, void* workspace,
+                      int64_t workspace_bytes, int32_t* tokens, float* shares, hipStream_t stream) {
+  if (!sample_sizes(rows, vocab) || !valid_dtype(dt) || stride < vocab || stride > kMaxElems / rows)
+    return MXQ_ERROR_INVALID_VALUE;
+  if (!logits || !u || !tokens || !shares) return MXQ_ERROR_INVALID_VALUE;
+  if ((!temperature_of && std::isnan(temperature)) || (!top_p_of && std::isnan(top_p)) ||
+      (!min_p_of && std::isnan(min_p)))
+    return MXQ_ERROR_INVALID_VALUE;
+  const int64_t need = mxq::sample_workspace(rows, vocab);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERROR_INVALID_VALUE;
+  if (((uintptr_t)logits & (dt == MXQ_BF16 ? 1u : 3u)) || (need > 0 && !aligned16(workspace)))
+    return MXQ_ERROR_MISALIGNED;
+  for (const void* p : {(const void*)u, (const void*)temperature_of, (const void*)top_k_of, (const void*)top_p_of,
+                        (const void*)min_p_of, (const void*)tokens, (const void*)shares})
+    if ((uintptr_t)p & 3u) return MXQ_ERROR_MISALIGNED;
+  mxq_status e = check_device();
+  if (e != MXQ_SUCCESS) return e;
+  mxq::SampleArgs a;
+  a.logits = logits;
+  a.stride = stride, a.rows = rows, a.vocab = vocab;
+  a.u = u;
+  a.temperature_of = temperature_of, a.top_p_of = top_p_of, a.min_p_of = min_p_of;
+  a.top_k_of = top_k_of;
+  a.temperature = temperature, a.top_p = top_p, a.min_p = min_p;
+  a.top_k = top_k;
+  a.tokens = tokens;
+  a.shares = shares;
+  return launched(mxq::launch_sample(a, dt == MXQ_BF16, workspace, stream));
+}
+
 }  // extern "C"

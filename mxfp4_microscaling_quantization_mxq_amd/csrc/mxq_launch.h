@@ -92,6 +92,22 @@ int64_t tree_attend_workspace(int64_t batch, int64_t drafts, unsigned q_heads, c
                               int64_t window, int64_t first);
 hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, void* workspace, hipStream_t st);
 
+// A token of each row of logits.  A setting is an array of one value a row, or
+// (null) one value for all.
+struct SampleArgs {
+  const void* logits;  // [rows][vocab], rows `stride` elements apart
+  int64_t stride, rows, vocab;
+  const float* u;  // [rows]
+  const float *temperature_of, *top_p_of, *min_p_of;
+  const int32_t* top_k_of;
+  float temperature, top_p, min_p;
+  int64_t top_k;
+  int32_t* tokens;  // [rows]
+  float* shares;    // [rows]
+};
+int64_t sample_workspace(int64_t rows, int64_t vocab);
+hipError_t launch_sample(const SampleArgs& a, bool bf16, void* workspace, hipStream_t st);
+
 hipError_t launch_mx_quantize(const void* x, bool bf16, int64_t rows, int64_t k, uint8_t* q, uint8_t* s,
                               hipStream_t st);
 // MXFP8: q[rows][k] E4M3 codes, s[rows][k/32] E8M0 codes.

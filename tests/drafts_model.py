@@ -145,3 +145,51 @@ def tree_attention(q, cache, table, context, bits, fmt, scale, window=0, first=0
             out[b, :, h] = p @ v / total[:, None]
             size[b, :, h] = p @ np.abs(v) / total[:, None]
     return out, size, mag
+
+
+# ------------------------------------------------------------------ the draw of a token
+
+def draw_check(x, u, temperature, top_k, top_p, min_p, token, share, what=""):
+    """(token, share) is a right answer for one row of float64 logits.
+
+    The weights are formed in extended precision.  The library's are whole
+    multiples of 2^-43 of the largest (half of one off at most), from fp64 values
+    within 2^-48: a sum over n of them is within n 2^-44 + 2^-48 of the sum, in
+    units of the largest weight.  Where a threshold lies that close to a prefix's
+    weight, either prefix is right, and either token where u's product lies that
+    close to a running sum."""
+    x = np.asarray(x, dtype=np.float64)
+    n = len(x)
+    if np.isnan(x).any() or x.max() == np.inf or x.max() == -np.inf:
+        assert token == -1 and np.isnan(share), what
+        return
+    if not temperature > 0:
+        assert token == int(np.argmax(x)) and share == 1, f"{what}: {token} for the largest {int(np.argmax(x))}"
+        return
+    with np.errstate(invalid="ignore"):
+        z = (x - x.max()).astype(np.longdouble) / np.longdouble(np.float32(temperature))
+    w = np.exp(np.where(np.isnan(z), -np.inf, z))
+    order = np.lexsort((np.arange(n), -x))
+    k = top_k if 0 < top_k < n else n
+    sums = np.cumsum(w[order])
+    off = n * 2.0 ** -44 + 2.0 ** -48 * float(sums[-1])
+    lengths = {k}
+    if np.float32(top_p) < 1:
+        goal = np.longdouble(np.float32(top_p)) * sums[k - 1]
+        lengths = {max(1, min(k, int(np.searchsorted(sums[:k], goal + d, side="left")) + 1)) for d in (-off, 0, off)}
+    least = np.longdouble(min(np.float32(min_p), np.float32(1)))
+    sizes = {max(1, int((w >= least + d).sum())) for d in (-2.0 ** -48, 0, 2.0 ** -48)}
+    u = min(max(float(np.float32(u)), 0.0), 1.0)
+    for length in lengths:
+        for size in sizes:
+            kept = np.zeros(n, dtype=bool)
+            kept[order[:min(length, size)]] = True
+            run = np.cumsum(np.where(kept, w, 0))
+            total = run[-1]
+            if 0 <= token < n and kept[token] and w[token] > 0:
+                before = run[token] - w[token]
+                if before - off <= u * total <= run[token] + off and (u < 1 or total - run[token] <= off):
+                    # the share: fp64 weight, the sum off by `off`, one rounding
+                    assert abs(share - w[token] / total) <= w[token] / total * (2.0 ** -23 + 2 * off / total), what
+                    return
+    raise AssertionError(f"{what}: token {token} (share {share}) is not the draw for u {u}, lengths {sorted(lengths)}")

@@ -157,3 +157,44 @@ def test_tree_mask():
     for bad in ([0], [-1, 1], [-2], [[-1, 0, 5]], []):
         with pytest.raises(ValueError):
             mxq.tree_mask(bad, device="cpu")
+
+
+# ------------------------------------------------------------------ the draw of a token
+
+def draw(lib, x=A, dt=1, stride=100, rows=3, vocab=100, u=B, t_of=NULL, t=1.0, k_of=NULL, k=0, p_of=NULL, p=1.0, m_of=NULL,
+         m=0.0, ws=A, ws_bytes=1 << 40, tokens=C, shares=D):
+    return lib.mxq_sample(x, dt, stride, rows, vocab, u, t_of, t, k_of, k, p_of, p, m_of, m, ws, ws_bytes, tokens, shares,
+                          NULL)
+
+
+def test_sample_refusals(lib):
+    nan = float("nan")
+    for bad in (dict(x=NULL), dict(u=NULL), dict(tokens=NULL), dict(shares=NULL), dict(dt=2), dict(rows=0), dict(rows=-1),
+                dict(rows=(1 << 20) + 1), dict(vocab=0), dict(vocab=101), dict(vocab=(1 << 20) + 1, stride=1 << 21),
+                dict(stride=1 << 60), dict(t=nan), dict(p=nan), dict(m=nan)):
+        assert draw(lib, **bad) == INVALID, bad
+    for bad in (dict(x=MIS2, dt=0), dict(x=ctypes.c_void_p(0x1000001)), dict(u=MIS2), dict(t_of=MIS2), dict(k_of=MIS2),
+                dict(p_of=MIS2), dict(m_of=MIS2), dict(tokens=MIS2), dict(shares=MIS2)):
+        assert draw(lib, **bad) == MISALIGNED, bad
+    n = ctypes.c_int64(-1)
+    assert lib.mxq_sample_workspace(3, 100, ctypes.byref(n)) == 0 and n.value >= 0
+    assert lib.mxq_sample_workspace(0, 100, ctypes.byref(n)) == INVALID
+    assert lib.mxq_sample_workspace(3, 0, ctypes.byref(n)) == INVALID
+    assert lib.mxq_sample_workspace(3, 100, None) == INVALID
+    if torch.cuda.device_count() == 0:
+        assert draw(lib) == NOT_SUPPORTED
+        assert draw(lib, x=MIS2, dt=1, t_of=A, t=nan) == NOT_SUPPORTED
+
+
+def test_binding_sample():
+    x, u = torch.zeros(3, 50), torch.zeros(3)
+    for args, kw in (((x[0], u), {}), ((x.t(), u), {}), ((x, u[:2]), {}), ((x, u), dict(temperature=torch.ones(2))),
+                     ((x, u), dict(top_k=torch.ones(3, 1, dtype=torch.int32))), ((x, u), dict(tokens=torch.zeros(2, dtype=torch.int32))),
+                     ((x, u), {})):  # the last: host tensors
+        with pytest.raises(ValueError):
+            mxq.sample(*args, **kw)
+    for args, kw in (((x.half(), u), {}), ((x.double(), u), {}), ((x, u.double()), {}), ((x, u), dict(top_k=torch.ones(3))),
+                     ((x, u), dict(top_p=torch.ones(3, dtype=torch.float64))), ((x, u), dict(tokens=torch.zeros(3))),
+                     ((x, u), dict(shares=torch.zeros(3, dtype=torch.bfloat16))), (([1.0], u), {})):
+        with pytest.raises(TypeError):
+            mxq.sample(*args, **kw)

@@ -459,3 +459,167 @@ def test_tree_mask_of_parents():
     assert np.array_equal(dm.bits_of(host(chain)), np.tril(np.ones((1, 70, 70), dtype=bool)))
     bits = dm.bits_of(host(m))
     tree_case(3, [20, 0], 4, 1, 2, 64, 16, "mxfp8", bits=bits)
+
+
+# ------------------------------------------------------------------ the draw of a token
+
+def logits_like(rng, rows, vocab, sure=None):
+    """A wide body and a few likely tokens; rows from sure of one to broad."""
+    x = rng.standard_normal((rows, vocab)) * 2.5
+    for r in range(rows):
+        at = rng.integers(0, vocab, size=min(40, vocab))
+        x[r, at] += (14 * rng.random() if sure is None else sure) * rng.random(len(at))
+    return x
+
+
+def draw_case(x, dtype, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, pad=0, shift=0, what="", **kw):
+    """One call, every row checked; settings are numbers or lists of one a row."""
+    rows, vocab = x.shape
+    wide = np.full((rows, vocab + pad), 1e4)  # what lies between the rows is larger than anything in them
+    wide[:, shift:shift + vocab] = x
+    stored_bits, x64 = stored(wide, dtype)
+    x64 = x64[:, shift:shift + vocab]
+    u = np.asarray(u, dtype=np.float32)
+
+    def arg(v, dt):
+        return dev(np.asarray(v, dtype=dt)) if isinstance(v, (list, np.ndarray)) else v
+
+    tokens, shares = mxq.sample(dev(stored_bits)[:, shift:shift + vocab], dev(u), temperature=arg(temperature, np.float32),
+                                top_k=arg(top_k, np.int32), top_p=arg(top_p, np.float32), min_p=arg(min_p, np.float32), **kw)
+    assert tokens.dtype == torch.int32 and shares.dtype == torch.float32
+    tokens, shares = host(tokens), host(shares)
+
+    def one(v, r):
+        return v[r] if isinstance(v, (list, np.ndarray)) else v
+
+    for r in range(rows):
+        dm.draw_check(x64[r], u[r], one(temperature, r), one(top_k, r), one(top_p, r), one(min_p, r), int(tokens[r]),
+                      float(shares[r]), f"{what} row {r}")
+    return tokens, shares
+
+
+SETTINGS = [dict(), dict(temperature=0.0), dict(temperature=0.3), dict(temperature=2.5), dict(top_k=1), dict(top_k=5),
+            dict(top_k=50), dict(top_p=0.9), dict(top_p=0.5, temperature=0.7), dict(min_p=0.05),
+            dict(top_k=20, top_p=0.8), dict(top_k=40, top_p=0.95, min_p=0.02, temperature=1.3)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [1, 2, 3, 7, 8, 9, 63, 64, 65, 511, 512, 513, 1000, 4097, 8191, 16385])
+def test_sample_sizes_and_settings(vocab, dtype):
+    rng = np.random.default_rng(vocab)
+    for i, s in enumerate(SETTINGS):
+        x = logits_like(rng, 4, vocab)
+        draw_case(x, dtype, rng.random(4), pad=i, shift=i // 2, what=str(s), **s)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(1, 131072, "bf16"), (2, 50001, "f32"), (3, 200003, "bf16"), (1, 1 << 20, "f32"),
+                                              (300, 2000, "f32"), (1100, 600, "bf16"), (70, 32768, "bf16")])
+def test_sample_large(rows, vocab, dtype):
+    rng = np.random.default_rng(rows)
+    x = logits_like(rng, rows, vocab)
+    picks = [SETTINGS[int(i)] for i in rng.integers(0, len(SETTINGS), size=rows)]
+    mixed = {n: [s.get(n, d) for s in picks] for n, d in (("temperature", 1.0), ("top_k", 0), ("top_p", 1.0), ("min_p", 0.0))}
+    draw_case(x, dtype, rng.random(rows), **mixed)
+    for s in SETTINGS[3::4]:
+        draw_case(x[:20], dtype, rng.random(min(rows, 20)), **s)
+
+
+@pytest.mark.parametrize("sure", [0.0, 6.0, 30.0])
+@pytest.mark.parametrize("s", [dict(), dict(top_p=0.95), dict(top_p=0.999, temperature=1.5), dict(top_k=3000),
+                               dict(top_k=30000, top_p=0.9), dict(top_k=70000), dict(min_p=1e-4), dict(min_p=0.3)])
+def test_sample_broad_and_sure_rows(s, sure):
+    """Cuts that leave one token, some, and tens of thousands."""
+    rng = np.random.default_rng(3)
+    draw_case(logits_like(rng, 6, 100000, sure), "f32", rng.random(6), **s)
+    draw_case(logits_like(rng, 6, 100000, sure), "bf16", rng.random(6), **s)
+
+
+@pytest.mark.parametrize("vocab", [1, 10, 1000, 70000])
+def test_sample_equal_logits(vocab):
+    """Equal logits: order is by index, sums are exact, and so is every threshold.
+    With n kept, u draws token floor(u n)."""
+    for value in (0.0, -3.5, 7.0):
+        x = torch.full((8, vocab), value, device="cuda")
+        x[1::2] = x[1::2] * 1.0 if value else -0.0  # (zeros of either sign are equal)
+        u = torch.tensor([0.0, 0.25, 0.5, 0.75, 0.999, 2.0 ** -24, 1 - 2.0 ** -24, 0.5], device="cuda")
+        for s, n in ((dict(), vocab), (dict(top_k=3), min(3, vocab)), (dict(top_p=0.5), max(1, -(-vocab // 2))),
+                     (dict(top_p=0.25, top_k=8), 2 if vocab >= 8 else max(1, -(-vocab // 4))), (dict(min_p=1.0), vocab),
+                     (dict(top_k=vocab - 1), max(1, vocab - 1)), (dict(temperature=0.0), 1)):
+            t, p = mxq.sample(x.to(torch.bfloat16), u, **s)
+            want = (u.double() * n).floor().clamp(max=n - 1).int()
+            assert torch.equal(t, want), (value, s, t, want)
+            assert torch.equal(p, torch.full_like(p, 1.0) / n)
+
+
+def test_sample_ties_at_the_cut():
+    """Several equal logits at the last place that top-k or top-p leaves: the first by index stay."""
+    x = np.full((64, 300), -4.0)
+    x[:, [250, 30, 31, 200, 100]] = 2.0
+    x[:, 150] = 3.0
+    u = (np.arange(64) + 0.5) / 64
+    for dtype in ("bf16", "f32"):
+        t, _ = draw_case(x, dtype, u, top_k=3)
+        assert set(t.tolist()) == {150, 30, 31}
+        w = np.exp(-1.0)
+        t, _ = draw_case(x, dtype, u, top_p=float((1 + 2.5 * w) / (1 + 5 * w + 294 * np.exp(-7.0))))
+        assert set(t.tolist()) == {150, 30, 31, 100}
+
+
+def test_sample_every_u_of_a_small_row():
+    """Shares add up: each token's number of draws over even u is its share of them."""
+    x = np.array([[0.0, -np.inf, 1.0, 0.5, -2.0, 1.0, -np.inf]])
+    n = 4096
+    t, p = draw_case(np.repeat(x, n, axis=0), "f32", (np.arange(n) + 0.5) / n)
+    w = np.exp(x[0])
+    assert np.abs(np.bincount(t, minlength=7) - n * w / w.sum()).max() <= 1
+
+
+def test_sample_u_at_and_past_its_ends():
+    x = np.array([[1.0, 2.0, -np.inf, 0.0, 2.0, -50.0, -np.inf]] * 6)
+    u = [0.0, 1 - 2.0 ** -24, 1.0, 1.5, -0.5, np.nan]
+    for s, first, last in ((dict(), 0, 4), (dict(top_k=2), 1, 4), (dict(top_p=0.3), 1, 1)):
+        t, _ = mxq.sample(dev(x.astype(np.float32)), dev(np.array(u, dtype=np.float32)), **s)
+        t = t.tolist()
+        # (token 5's weight, e^-52, counts as 0)
+        assert t[0] == t[4] == t[5] == first and t[1] == t[2] == t[3] == last
+
+
+def test_sample_rows_without_a_distribution():
+    x = np.random.default_rng(0).standard_normal((8, 1000))
+    x[1, 700] = np.nan
+    x[2, 0] = np.inf
+    x[3] = -np.inf
+    x[4, :999] = -np.inf  # one token left
+    x[5, ::2] = -np.inf
+    bad = np.float32(x)
+    bad.view(np.uint32)[6, 3] = 0xFFC00001  # a NaN of the other sign
+    for s in (dict(), dict(temperature=0.0), dict(top_k=5), dict(top_p=0.9), dict(min_p=0.1)):
+        t, p = draw_case(bad.astype(np.float64), "f32", np.full(8, 0.4), **s)
+        assert t[4] == 999 and p[4] == 1 and (t[[1, 2, 3, 6]] == -1).all() and t[5] % 2 == 1
+        draw_case(bad.astype(np.float64), "bf16", np.full(8, 0.4), **s)
+
+
+@pytest.mark.parametrize("temperature", [1e-45, 1e-30, 1e-6, 1e6, 1e30, float("inf")])
+def test_sample_extreme_temperatures(temperature):
+    rng = np.random.default_rng(7)
+    x = rng.standard_normal((5, 5000)) * 3
+    x[1, 4], x[2, 9] = -np.inf, 300.0
+    for s in (dict(), dict(top_k=7), dict(top_p=0.6), dict(min_p=0.5)):
+        draw_case(x, "f32", rng.random(5), temperature=temperature, **s)
+    big = x * 1e37  # differences that pass fp32's range
+    draw_case(big, "f32", rng.random(5), temperature=1e37, top_p=0.9)
+
+
+def test_sample_outputs_and_repeat():
+    """Caller's outputs and workspace, and the same bits again."""
+    rng = np.random.default_rng(8)
+    x, u = dev(logits_like(rng, 40, 30000).astype(np.float32)), dev(rng.random(40).astype(np.float32))
+    for s in SETTINGS:
+        t, p = mxq.sample(x, u, **s)
+        tokens, shares = torch.full_like(t, -9), torch.full_like(p, -9)
+        ws = torch.full((1 << 24,), 0xA5, dtype=torch.uint8, device="cuda")
+        got = mxq.sample(x, u, tokens=tokens, shares=shares, workspace=ws, **s)
+        assert got[0] is tokens and got[1] is shares and torch.equal(t, tokens) and torch.equal(p, shares)
+        for r in (0, 17):  # a row alone, split otherwise
+            t1, p1 = mxq.sample(x[r:r + 1], u[r:r + 1], **s)
+            assert torch.equal(t1, t[r:r + 1]) and torch.equal(p1, p[r:r + 1])
