@@ -10,20 +10,26 @@
 // below 2^-44 of the largest count as 0 (all of them in a row of 2^20 are below
 // 2^-24 of it).  Order is that of the logits' bits as whole numbers.
 //
-// Rows of up to 8192 logits take one block (k_sample_row), which cuts the order
-// eight bits of the logits at a time.  Longer rows are split, 8192 logits a
-// block, in three launches:
-//   k_sample_scan: a block's largest; and, by the row's settings, the index of
-//     the largest (greedy), the weights' sums of its segments of 512 (nothing
-//     cut off), or a histogram of numbers and weights over 1024 bins of 1/32 of
-//     the exponent (top-k, top-p), all relative to the block's own largest;
+// A row's settings decide what is done.  Greedy: the index of the largest.
+// Nothing cut off: the weights' sums of segments of 512 tokens, then the segment
+// and the token that u falls into.  Top-k and top-p: a histogram over 1024 bins of
+// 1/32 of the exponent names the bins that a cut lies in (a margin covers its
+// rounded weights); their tokens are listed (2048 at most) and ranked, each
+// against all others, with exact sums.  A cut in a bin with more tokens than
+// that (equal logits, mostly) is found eight bits of the logits at a time, in
+// passes over the row (whole_row).
+//
+// Rows of up to about 8192 logits take one block (k_sample_row).  Longer ones are
+// split, 8192 logits a block, in four launches:
+//   k_sample_scan: the sums or the histogram of a block, relative to its largest;
 //   k_sample_plan: a row's blocks joined: rows without a cut are finished here,
 //     for others the bins that a cut can lie in;
 //   k_sample_cut: a second pass that sums, by segment, what is certainly kept, and
-//     lists the tokens of those bins (all down to the cut, if they are at most
-//     2048); the row's last block cuts the list and draws.
-// A row whose cut lies in a bin with more than 2048 tokens (equal logits, mostly)
-// is left to one block of k_sample_cut, which does what k_sample_row does.
+//     lists the tokens of those bins (all down to the cut, if they fit);
+//   k_sample_draw: a row's list cut, and its token drawn.
+// (Joined by a ticket in k_sample_cut, whose last block of a row went on with it,
+// three launches were slower: each block's release to the other chiplets cost
+// more than a launch, 97 rows of 50001 103 us for 20 + 15.)
 // What a row gives depends on that row alone, not on the others of the call.
 #include <float.h>
 
@@ -47,6 +53,11 @@ constexpr int kMostBlocks = (kMostSegments + kBlockSegments - 1) / kBlockSegment
 constexpr int kBins = 1024;     // the last one: weights below e^-31.9, which count as 0
 constexpr float kBinsPer = 32;  // of the exponent
 constexpr int kList = 2048;
+constexpr int kRank = kThreads;  // tokens that are ranked, one a thread
+// A histogram's entry: the number of tokens, and their weights in units of 2^-36
+// (cut off, so up to 2^20 of them are less than 2^-16 of the largest below).
+constexpr int kPackBits = 50, kPackShift = 7;
+constexpr double kMargin = 0x1p-15;
 
 // One row, as groups of 8 elements on 32 (bf16: 16) byte boundaries, the first
 // `lead` elements of which lie before the row.
@@ -132,28 +143,32 @@ struct Settings {
   __device__ bool binned() const { return !greedy && (cut_k || cut_p); }
 };
 
-// Weights relative to `top`, in fp64: exp(z) = 2^n times the Taylor polynomial of
-// 2^y, |y| <= 1/2 (it ends below 2^-51).
+// Weights relative to `top`, in fp64: 2^z = 2^n times the Taylor polynomial of 2^y,
+// |y| <= 1/2 (it ends below 2^-51).  Its coefficients, (ln 2)^k / k!, are kept in
+// scalar registers: the compiler, which sees constants, would move each into a
+// vector register for each of the products (12 of about 26 instructions more).
 struct Weights {
   double top, per;  // log2 e / temperature
-  __device__ Weights(float t, float temperature) : top((double)t), per(0x1.71547652b82fep+0 / (double)temperature) {}
+  double c[12];
+  __device__ Weights(float t, float temperature)
+      : top((double)t),
+        per(0x1.71547652b82fep+0 / (double)temperature),
+        c{0x1.62e42fefa39efp-1,  0x1.ebfbdff82c58fp-3,  0x1.c6b08d704a0c0p-5,  0x1.3b2ab6fba4e77p-7,
+          0x1.5d87fe78a6731p-10, 0x1.430912f86c787p-13, 0x1.ffcbfc588b0c7p-17, 0x1.62c0223a5c824p-20,
+          0x1.b5253d395e7c4p-24, 0x1.e4cf5158b8ecap-28, 0x1.e8cac7351bb25p-32, 0x1.c3bd650fc2986p-36} {
+#pragma unroll
+    for (int i = 0; i < 12; i++) asm("" : "+s"(c[i]));
+  }
   __device__ double of(float x) const {
     const double z = fmax(((double)x - top) * per, -90.0);  // (also what is not a number: -inf * 0)
-    const double n = __builtin_rint(z), y = z - n;
-    double p = 0x1.c3bd650fc2986p-36;  // (ln 2)^12 / 12!, and so on
-    p = __builtin_fma(p, y, 0x1.e8cac7351bb25p-32);
-    p = __builtin_fma(p, y, 0x1.e4cf5158b8ecap-28);
-    p = __builtin_fma(p, y, 0x1.b5253d395e7c4p-24);
-    p = __builtin_fma(p, y, 0x1.62c0223a5c824p-20);
-    p = __builtin_fma(p, y, 0x1.ffcbfc588b0c7p-17);
-    p = __builtin_fma(p, y, 0x1.430912f86c787p-13);
-    p = __builtin_fma(p, y, 0x1.5d87fe78a6731p-10);
-    p = __builtin_fma(p, y, 0x1.3b2ab6fba4e77p-7);
-    p = __builtin_fma(p, y, 0x1.c6b08d704a0c0p-5);
-    p = __builtin_fma(p, y, 0x1.ebfbdff82c58fp-3);
-    p = __builtin_fma(p, y, 0x1.62e42fefa39efp-1);
+    const double t = z + 0x1.8p52, y = z - (t - 0x1.8p52);  // n, the nearest whole number, in the low bits of t
+    double p = c[11];
+#pragma unroll
+    for (int i = 10; i >= 0; i--) p = __builtin_fma(p, y, c[i]);
     p = __builtin_fma(p, y, 1.0);
-    return __builtin_ldexp(p, (int)n);
+    u32x2 w = __builtin_bit_cast(u32x2, p);
+    w.y += __builtin_bit_cast(u32x2, t).x << 20;  // times 2^n
+    return __builtin_bit_cast(double, w);
   }
   // w in units of 2^-43 (the last bit of numbers in [512, 1024)).
   static __device__ u64 units(double w) { return (u64)__double_as_longlong(w + 512.0) - 0x4080000000000000ull; }
@@ -455,102 +470,371 @@ __device__ void whole_row(const SampleArgs& a, int64_t r, const Row<kBf16>& row,
     draw<kBf16>(a, r, row, mass, kept, [](int) { return 1.0; }, [&](int) { return wt; });
 }
 
-// What the kernels of long rows hand on, a row each.
-struct Plan {
-  int mode;  // kDone, kListed, kAlone
-  unsigned top;
-  int lo, hi, bin_k;           // listed: bins lo to hi, and bin_k where top-k cuts (else -1)
-  unsigned above_k, ticket;    // tokens above bin_k
-  unsigned listed;
-  double mass_above_k, total;  // in units of the row's largest
+// One block's part of a row: the groups of its segments, one a lane and turn.
+template <bool kBf16>
+struct Part {
+  float x[kTurns][kEach];
+  int first;  // segment of turn 0 (a turn's are kWaves further on)
+  __device__ Part(const Row<kBf16>& row, unsigned block)
+      : first((int)block * kBlockSegments + (int)(threadIdx.x >> 6)) {
+    const int groups = row.groups();
+#pragma unroll
+    for (int t = 0; t < kTurns; t++) {
+#pragma unroll
+      for (int j = 0; j < kEach; j++) x[t][j] = -INFINITY;
+      if (group(t) < groups) row.load(group(t), x[t]);
+    }
+  }
+  __device__ int segment(int t) const { return first + t * kWaves; }
+  __device__ int group(int t) const { return segment(t) * 64 + (int)(threadIdx.x & 63); }
+  // Key of the largest, over the block.
+  __device__ unsigned top(unsigned* lds) const {
+    float v = x[0][0];  // (a NaN stays)
+#pragma unroll
+    for (int t = 0; t < kTurns; t++)
+#pragma unroll
+      for (int j = 0; j < kEach; j++) v = __builtin_elementwise_maximum(v, x[t][j]);
+    return max_block(top_key(v), lds);
+  }
+  // Index of the first that has the key `top`, as its complement (0: none).
+  __device__ unsigned first_top(const Row<kBf16>& row, unsigned top, unsigned* lds) const {
+    unsigned best = 0;
+#pragma unroll
+    for (int t = 0; t < kTurns; t++)
+#pragma unroll
+      for (int j = 0; j < kEach; j++)
+        if (key_of(x[t][j]) == top) best = max(best, ~(unsigned)row.index_of(group(t), j));
+    return max_block(best, lds);
+  }
 };
-enum { kDone, kListed, kAlone };
 
-struct SampleParams {
-  SampleArgs a;
-  int64_t row0;           // first row of this launch
-  unsigned blocks;        // of a row
-  Plan* plan;             // [rows]
-  unsigned *tops, *where;  // [rows][blocks]: the largest's key, and (greedy) its index
-  u64* mass;              // [rows][blocks * kBlockSegments]
-  u64* bin_mass;          // [rows][blocks][kBins]
-  unsigned* bin_count;
-  u32x2* list;            // [rows][kList]: key, index
+__device__ __forceinline__ u64 packed(u64 units) { return (1ull << kPackBits) + (units >> kPackShift); }
+
+// Where a row's cuts lie: top-k in bin_k (-1: it does not cut), top-p in one of
+// the bins p_lo to p_hi; the tokens above these, and down to the last of them.
+struct Cuts {
+  int bin_k, p_lo, p_hi;
+  unsigned above_k, above_p, through_p, through;
 };
+struct FindLds {
+  double sums[kBins];  // of a bin and those above it
+  unsigned counts[kBins];
+  double wave_mass[kBins / 64];
+  unsigned wave_count[kBins / 64];
+  int found[3];
+};
+// The first bin of which `here` holds, into *found (it holds of all after it).
+template <int kPer>
+__device__ __forceinline__ void first_bin(const bool (&here)[kPer], int bin0, int* found) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < kPer; i++) any |= here[i];
+  const u64 who = __builtin_amdgcn_ballot_w64(any);
+  if (!who || (int)(threadIdx.x & 63) != __builtin_ctzll(who)) return;
+  int at = 0;
+#pragma unroll
+  for (int i = kPer - 1; i >= 0; i--) at = here[i] ? i : at;
+  atomicMin(found, bin0 + at);
+}
+// m, n: weights (as rounded in a histogram) and numbers of this thread's bins.
+template <int kPer>
+__device__ Cuts find_cuts(double (&m)[kPer], unsigned (&n)[kPer], const Settings& set, double total, FindLds& sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bin0 = (int)threadIdx.x * kPer;
+#pragma unroll
+  for (int i = 1; i < kPer; i++) m[i] += m[i - 1], n[i] += n[i - 1];
+  double mm = m[kPer - 1];
+  unsigned nn = n[kPer - 1];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double om = __shfl_up(mm, d, 64);
+    const unsigned on = __shfl_up(nn, d, 64);
+    if (lane >= d) mm += om, nn += on;
+  }
+  if (lane == 63) sh.wave_mass[wave] = mm, sh.wave_count[wave] = nn;
+  if (threadIdx.x < 3) sh.found[threadIdx.x] = kBins;
+  __syncthreads();
+  mm -= m[kPer - 1], nn -= n[kPer - 1];
+  for (int w = 0; w < wave; w++) mm += sh.wave_mass[w], nn += sh.wave_count[w];
+  bool here[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; i++) {
+    sh.sums[bin0 + i] = m[i] += mm;
+    sh.counts[bin0 + i] = n[i] += nn;
+    // (a cut below the bins, where weights count as 0, is none)
+    here[i] = set.cut_k && bin0 + i < kBins - 1 && (int64_t)n[i] >= set.k;
+  }
+  first_bin(here, bin0, &sh.found[0]);
+  __syncthreads();
+  Cuts c = {-1, 0, -1, 0, 0, 0, 0};
+  if (set.cut_k && sh.found[0] < kBins) c.bin_k = sh.found[0];
+  if (c.bin_k > 0) c.above_k = sh.counts[c.bin_k - 1];
+  if (c.bin_k >= 0) c.through = sh.counts[c.bin_k];
+  if (set.cut_p) {
+    const double least = c.bin_k < 0 ? total : c.bin_k > 0 ? sh.sums[c.bin_k - 1] : 0;
+    const double most = c.bin_k < 0 ? total : sh.sums[c.bin_k] * (1 + kMargin);
+#pragma unroll
+    for (int i = 0; i < kPer; i++) here[i] = n[i] > 0 && m[i] >= (double)set.top_p * least * (1 - kMargin);
+    first_bin(here, bin0, &sh.found[1]);
+#pragma unroll
+    for (int i = 0; i < kPer; i++) here[i] = n[i] > 0 && m[i] >= (double)set.top_p * most * (1 + kMargin);
+    first_bin(here, bin0, &sh.found[2]);
+    __syncthreads();
+    c.p_hi = min(sh.found[2], c.bin_k < 0 ? kBins - 2 : c.bin_k);
+    c.p_lo = min(sh.found[1], c.p_hi);
+    if (c.p_lo > 0) c.above_p = sh.counts[c.p_lo - 1];
+    c.through_p = sh.counts[c.p_hi];
+    c.through = max(c.through, c.through_p);
+  }
+  return c;
+}
+
+// Listed tokens in LDS, those of bins `lo` to `hi`.
+struct ListLds {
+  u32x2 at[kList];  // key, index
+  u64 units[kList];
+};
+struct List {
+  const ListLds& list;
+  int n, lo, hi;
+  Bins bins;
+  float grid_top;
+  // g(place, key, index)
+  template <class G>
+  __device__ void each_place(G g) const {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const u32x2 e = list.at[i];
+      const int b = bins.of(of_key(e.x), grid_top);
+      if (b >= lo && b <= hi) g(i, e.x, (int)e.y);
+    }
+  }
+  template <class F>
+  __device__ void each(F f) const {
+    each_place([&](int, unsigned key, int index) { f(key, index); });
+  }
+  __device__ u64 mass(u64* lds) const {
+    u64 m = 0;
+    each_place([&](int i, unsigned, int) { m += list.units[i]; });
+    return sum_block(m, lds);
+  }
+};
+
+// Tokens to rank: order (key, then the complement of the index) and units.
+struct RankLds {
+  u64 order[kRank], units[kRank];
+  u64 order_at, mass_at, order_low, mass_low;
+  unsigned n, hit;
+};
+// The source's tokens into LDS; their number (above kRank: not all of them).
+__device__ int gather(const List& src, RankLds& sh) {
+  if (threadIdx.x == 0) sh.n = 0, sh.hit = 0;
+  __syncthreads();
+  src.each_place([&](int i, unsigned key, int index) {
+    const unsigned at = atomicAdd(&sh.n, 1u);
+    if (at >= kRank) return;
+    sh.order[at] = ((u64)key << 32) | ~(unsigned)index;
+    sh.units[at] = src.list.units[i];
+  });
+  __syncthreads();
+  return (int)sh.n;
+}
+// The last token, in order, that is taken: the one at which a count is complete,
+// or the first at which the mass is.  `count` and `mass` lie above the tokens.
+struct Last {
+  u64 order, mass;  // mass: of it and all above it
+};
+template <bool kCount>
+__device__ Last rank(int n, unsigned count, u64 mass, unsigned k, double reach, RankLds& sh) {
+  if ((int)threadIdx.x < n) {
+    const u64 order = sh.order[threadIdx.x];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j++) {
+      const bool over = sh.order[j] > order;
+      before += over;
+      mass += over ? sh.units[j] : 0;
+    }
+    const u64 with = mass + sh.units[threadIdx.x];
+    const bool hit = kCount ? count + before + 1 == k : (double)with >= reach && !((double)mass >= reach);
+    if (hit) sh.order_at = order, sh.mass_at = with, sh.hit = 1;
+    if (before == n - 1) sh.order_low = order, sh.mass_low = with;
+  }
+  __syncthreads();
+  const Last l = sh.hit ? Last{sh.order_at, sh.mass_at} : Last{sh.order_low, sh.mass_low};
+  __syncthreads();
+  return l;
+}
+
+// The cut of a row whose candidates are listed.  mass_k and mass_p lie above
+// bin_k and p_lo; `total` is the row's.
+template <bool kBf16>
+__device__ Kept cut_list(const ListLds& list, int n, const Cuts& cuts, u64 mass_k, u64 mass_p, double total,
+                         const Settings& set, const Weights& wt, const Bins& bins, float grid_top, RankLds& rk, CutLds& sh) {
+  const List in_k = {list, n, cuts.bin_k, cuts.bin_k, bins, grid_top}, in_p = {list, n, cuts.p_lo, cuts.p_hi, bins, grid_top};
+  const bool cut_k = cuts.bin_k >= 0;
+  Kept kept = {0, 0x7FFFFFFF, set.min_w};
+  u64 order = 0;
+  bool few = true;
+  if (cut_k) {
+    const int c = gather(in_k, rk);
+    few = c <= kRank;
+    if (few) {
+      const Last l = rank<true>(c, cuts.above_k, mass_k, (unsigned)set.k, 0, rk);
+      order = l.order, total = (double)l.mass;
+    }
+  }
+  if (set.cut_p && few) {
+    const int c = gather(in_p, rk);
+    few = c <= kRank;
+    // (at least one token)
+    if (few) order = max(order, rank<false>(c, 0, mass_p, 0, fmax((double)set.top_p * total, 0.5), rk).order);
+  }
+  if (!few)
+    return cut_both<kBf16>(in_k, {0, cuts.above_k, mass_k}, cut_k, (unsigned)set.k, in_p, {0, 0, mass_p}, set.cut_p,
+                           set.top_p, total, wt, set.min_w, sh);
+  kept.key = (unsigned)(order >> 32), kept.last = (int)~(unsigned)order;
+  return kept;
+}
 
 __device__ __forceinline__ void no_token(const SampleArgs& a, int64_t r) {
   a.tokens[r] = -1;
   a.shares[r] = __builtin_nanf("");
 }
 
+// Rows that one block holds.
 template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void k_sample_row(SampleArgs a) {
   __shared__ CutLds sh;
-  __shared__ u64 mass[kBlockSegments + 1];
+  __shared__ FindLds find;
+  __shared__ ListLds list;
+  __shared__ RankLds rk;
+  __shared__ u64 bin[kBins];
+  __shared__ u64 mass[kBlockSegments];
+  __shared__ unsigned lds_n;
   const int64_t r = blockIdx.x;
   const Row<kBf16> row(a, r);
-  Settings set(a, r);
-  unsigned top = 0;
-  for (int i = threadIdx.x; i < row.groups(); i += kThreads) {
-    float x[kEach];
-    row.load(i, x);
-#pragma unroll
-    for (int j = 0; j < kEach; j++) top = max(top, top_key(x[j]));
-  }
-  top = max_block(top, sh.wave_max);
+  const Settings set(a, r);
+  const Part<kBf16> part(row, 0);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const unsigned top = part.top(sh.wave_max);
   if (no_weights(top)) {
     if (threadIdx.x == 0) no_token(a, r);
     return;
   }
   if (set.greedy) {
-    unsigned at = 0;  // the largest of ~index
-    row.each([&](unsigned key, int index) {
-      if (key == top) at = max(at, ~(unsigned)index);
-    });
-    at = max_block(at, sh.wave_max);
+    const unsigned at = part.first_top(row, top, sh.wave_max);
     if (threadIdx.x == 0) a.tokens[r] = (int)~at, a.shares[r] = 1;
     return;
   }
-  whole_row<kBf16>(a, r, row, set, of_key(top), mass, sh);
+  const Weights wt(of_key(top), set.temperature);
+  Kept kept = {0, 0x7FFFFFFF, set.min_w};
+  if (set.binned()) {
+    const Bins bins(set.temperature);
+    const float grid_top = bins.grid(of_key(top));
+    for (int i = threadIdx.x; i < kBins; i += kThreads) bin[i] = 0;
+    if (threadIdx.x == 0) lds_n = 0;
+    __syncthreads();
+    u64 units[kTurns][kEach], sum = 0;
+#pragma unroll
+    for (int t = 0; t < kTurns; t++)
+#pragma unroll
+      for (int j = 0; j < kEach; j++) {
+        const int b = bins.of(part.x[t][j], grid_top);
+        units[t][j] = Weights::units(wt.of(part.x[t][j]));
+        sum += units[t][j];
+        if (b < kBins - 1 && part.x[t][j] > -INFINITY) atomicAdd(&bin[b], packed(units[t][j]));
+      }
+    sum = sum_block(sum, sh.wave_sum);
+    double m[kBins / kThreads];
+    unsigned n[kBins / kThreads];
+#pragma unroll
+    for (int i = 0; i < kBins / kThreads; i++) {
+      const u64 v = bin[threadIdx.x * (kBins / kThreads) + i];
+      n[i] = (unsigned)(v >> kPackBits), m[i] = (double)((v & ((1ull << kPackBits) - 1)) << kPackShift);
+    }
+    const Cuts cuts = find_cuts(m, n, set, (double)sum, find);
+    if (cuts.bin_k >= 0 || set.cut_p) {
+      // the candidates, and what lies above them
+      u64 above_k = 0, above_p = 0;
+#pragma unroll
+      for (int t = 0; t < kTurns; t++)
+#pragma unroll
+        for (int j = 0; j < kEach; j++) {
+          const int b = bins.of(part.x[t][j], grid_top);
+          if (b < cuts.bin_k) above_k += units[t][j];
+          if (b < cuts.p_lo) above_p += units[t][j];
+          if (!(b == cuts.bin_k || (b >= cuts.p_lo && b <= cuts.p_hi)) || !(part.x[t][j] > -INFINITY)) continue;
+          const unsigned at = atomicAdd(&lds_n, 1u);
+          if (at >= kList) continue;
+          list.at[at] = (u32x2){key_of(part.x[t][j]), (unsigned)row.index_of(part.group(t), j)};
+          list.units[at] = units[t][j];
+        }
+      above_k = sum_block(above_k, sh.wave_sum);
+      above_p = sum_block(above_p, sh.wave_sum);  // (and barriers)
+      if (lds_n > kList || !(fabsf(grid_top) < kGridMost)) {
+        whole_row<kBf16>(a, r, row, set, of_key(top), mass, sh);
+        return;
+      }
+      kept = cut_list<kBf16>(list, (int)lds_n, cuts, above_k, above_p, (double)sum, set, wt, bins, grid_top, rk, sh);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kTurns; t++) {
+    u64 m = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; j++) {
+      const double w = wt.of(part.x[t][j]);
+      if (kept.has(key_of(part.x[t][j]), row.index_of(part.group(t), j), w)) m += Weights::units(w);
+    }
+    m = sum_wave64(m);
+    if (lane == 0) mass[part.segment(t)] = m;
+  }
+  __syncthreads();
+  if (wave == 0) draw<kBf16>(a, r, row, mass, kept, [](int) { return 1.0; }, [&](int) { return wt; });
 }
+
+// What the kernels of long rows hand on, a row each.
+struct Plan {
+  int mode;
+  unsigned top;
+  int lo;              // bins above it are kept but for min-p; those from it on are listed
+  int all;             // all bins down to the cuts are listed
+  int need_k;          // bins above bin_k are neither sure nor listed
+  unsigned listed;
+  Cuts cuts;
+  double total;        // the row's weights, in units of its largest
+  u64 mass_k;          // (need_k) of the bins above bin_k
+};
+enum { kDone, kListed, kAlone };
+
+struct SampleParams {
+  SampleArgs a;
+  int64_t row0;            // first row of this launch
+  unsigned blocks;         // of a row
+  Plan* plan;              // [rows]
+  unsigned *tops, *where;  // [rows][blocks]: the largest's key, and (greedy) its index
+  u64* mass;               // [rows][blocks][kBlockSegments]; with a histogram, [0] is the block's sum
+  u64* bins;               // [rows][blocks][kBins]
+  u32x2* list;             // [rows][kList]: key, index
+};
 
 template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams p) {
   __shared__ unsigned lds_max[kWaves];
-  __shared__ u64 bin_mass[kBins];
-  __shared__ unsigned bin_count[kBins];
+  __shared__ u64 lds_sum[kWaves];
+  __shared__ u64 bin[kBins];
   const unsigned rr = blockIdx.x / p.blocks, b = blockIdx.x % p.blocks;
   const int64_t r = p.row0 + rr;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const Row<kBf16> row(p.a, r);
   const Settings set(p.a, r);
-  const int s0 = (int)b * kBlockSegments + wave, groups = row.groups();
-  float x[kTurns][kEach];
-#pragma unroll
-  for (int t = 0; t < kTurns; t++) {
-    const int g = (s0 + t * kWaves) * 64 + lane;
-#pragma unroll
-    for (int j = 0; j < kEach; j++) x[t][j] = -INFINITY;
-    if (g < groups) row.load(g, x[t]);
-  }
-  unsigned top = 0;
-#pragma unroll
-  for (int t = 0; t < kTurns; t++)
-#pragma unroll
-    for (int j = 0; j < kEach; j++) top = max(top, top_key(x[t][j]));
+  const Part<kBf16> part(row, b);
   if (set.binned())
-    for (int i = threadIdx.x; i < kBins; i += kThreads) bin_mass[i] = 0, bin_count[i] = 0;
-  top = max_block(top, lds_max);
+    for (int i = threadIdx.x; i < kBins; i += kThreads) bin[i] = 0;
+  const unsigned top = part.top(lds_max);
   const int64_t at = (int64_t)rr * p.blocks + b;
   if (threadIdx.x == 0) p.tops[at] = top;
   if (set.greedy) {
-    unsigned best = 0;  // the largest of ~index
-#pragma unroll
-    for (int t = 0; t < kTurns; t++)
-#pragma unroll
-      for (int j = 0; j < kEach; j++)
-        if (top_key(x[t][j]) == top) best = max(best, ~(unsigned)row.index_of((s0 + t * kWaves) * 64 + lane, j));
-    best = max_block(best, lds_max);
+    const unsigned best = part.first_top(row, top, lds_max);
     if (threadIdx.x == 0) p.where[at] = ~best;
     return;
   }
@@ -561,28 +845,27 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams p) {
     for (int t = 0; t < kTurns; t++) {
       u64 m = 0;
 #pragma unroll
-      for (int j = 0; j < kEach; j++) m += Weights::units(wt.of(x[t][j]));
+      for (int j = 0; j < kEach; j++) m += Weights::units(wt.of(part.x[t][j]));
       m = sum_wave64(m);
       if (lane == 0) p.mass[at * kBlockSegments + t * kWaves + wave] = m;
     }
   } else if (set.binned()) {
     const Bins bins(set.temperature);
     const float grid_top = bins.grid(of_key(top));
+    u64 sum = 0;
 #pragma unroll
     for (int t = 0; t < kTurns; t++)
 #pragma unroll
       for (int j = 0; j < kEach; j++) {
-        const int bin = bins.of(x[t][j], grid_top);
-        if (bin >= kBins - 1 || !(x[t][j] > -INFINITY)) continue;
-        atomicAdd(&bin_count[bin], 1u);
-        const u64 w = Weights::units(wt.of(x[t][j]));
-        if (w) atomicAdd(&bin_mass[bin], w);
+        const int i = bins.of(part.x[t][j], grid_top);
+        if (i >= kBins - 1 || !(part.x[t][j] > -INFINITY)) continue;
+        const u64 units = Weights::units(wt.of(part.x[t][j]));
+        sum += units;
+        atomicAdd(&bin[i], packed(units));
       }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      p.bin_mass[at * kBins + i] = bin_mass[i];
-      p.bin_count[at * kBins + i] = bin_count[i];
-    }
+    sum = sum_block(sum, lds_sum);
+    if (threadIdx.x == 0) p.mass[at * kBlockSegments] = sum;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) p.bins[at * kBins + i] = bin[i];
   }
 }
 
@@ -590,23 +873,20 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams p) {
 template <bool kBf16>
 __global__ __launch_bounds__(kBins) void k_sample_plan(SampleParams p) {
   __shared__ unsigned lds_max[kBins / 64];
-  __shared__ double scale[kMostBlocks];
+  __shared__ unsigned tops[kMostBlocks];
+  __shared__ double scale[kMostBlocks];  // of a block's units
+  __shared__ int shift[kMostBlocks];     // of its bins
   __shared__ u64 mass[kMostBlocks * kBlockSegments];
-  __shared__ double sums[kBins];     // of a bin and those above it
-  __shared__ unsigned counts[kBins];
-  __shared__ double wave_mass[kBins / 64];
-  __shared__ unsigned wave_count[kBins / 64];
-  __shared__ int found[3];
+  __shared__ FindLds find;
   const unsigned rr = blockIdx.x;
   const int64_t r = p.row0 + rr, first = (int64_t)rr * p.blocks;
   const SampleArgs& a = p.a;
   const Row<kBf16> row(a, r);
   const Settings set(a, r);
-  const int bin = threadIdx.x, lane = bin & 63, wave = bin >> 6;
   unsigned top = 0;
-  for (unsigned b = threadIdx.x; b < p.blocks; b += kBins) top = max(top, p.tops[first + b]);
+  for (unsigned b = threadIdx.x; b < p.blocks; b += kBins) top = max(top, tops[b] = p.tops[first + b]);
   top = max_block(top, lds_max);
-  Plan plan = {kDone, top, 0, -1, -1, 0, 0, 0, 0, 0};
+  Plan plan = {kDone, top, kBins, 0, 0, 0, {-1, 0, -1, 0, 0, 0, 0}, 0, 0};
   if (no_weights(top)) {
     if (threadIdx.x == 0) no_token(a, r), p.plan[rr] = plan;
     return;
@@ -614,117 +894,131 @@ __global__ __launch_bounds__(kBins) void k_sample_plan(SampleParams p) {
   if (set.greedy) {
     unsigned at = 0;
     for (unsigned b = threadIdx.x; b < p.blocks; b += kBins)
-      if (p.tops[first + b] == top) at = max(at, ~p.where[first + b]);
+      if (tops[b] == top) at = max(at, ~p.where[first + b]);
     at = max_block(at, lds_max);
     if (threadIdx.x == 0) a.tokens[r] = (int)~at, a.shares[r] = 1, p.plan[rr] = plan;
     return;
   }
   const Weights wt(of_key(top), set.temperature);
+  const Bins bins(set.temperature);
+  const float grid_top = bins.grid(of_key(top));
+  for (unsigned b = threadIdx.x; b < p.blocks; b += kBins) {
+    const float t = of_key(tops[b]);
+    scale[b] = wt.of(t);
+    shift[b] = (int)fminf(grid_top - bins.grid(t), (float)kBins);
+  }
   if (set.plain()) {
-    for (unsigned b = threadIdx.x; b < p.blocks; b += kBins) scale[b] = wt.of(of_key(p.tops[first + b]));
     for (int s = threadIdx.x; s < row.segments(); s += kBins) mass[s] = p.mass[first * kBlockSegments + s];
     if (threadIdx.x == 0) p.plan[rr] = plan;
     __syncthreads();
-    if (wave == 0)
+    if (threadIdx.x < 64)
       draw<kBf16>(a, r, row, mass, {0, 0x7FFFFFFF, 0}, [&](int s) { return scale[s / kBlockSegments]; },
-                  [&](int s) { return Weights(of_key(p.tops[first + s / kBlockSegments]), set.temperature); });
+                  [&](int s) { return Weights(of_key(tops[s / kBlockSegments]), set.temperature); });
     return;
   }
   plan.mode = kListed;
-  if (!set.binned()) {  // min-p alone: every token by its own weight
-    plan.lo = kBins;
-    if (threadIdx.x == 0) p.plan[rr] = plan;
-    return;
-  }
-
-  // the blocks' bins, as bins of the row
-  const Bins bins(set.temperature);
-  const float grid_top = bins.grid(of_key(top));
-  double m = 0;
-  unsigned n = 0;
-  for (unsigned b = 0; b < p.blocks; b++) {
-    const unsigned t = p.tops[first + b];
-    const int from = bin - (int)fminf(grid_top - bins.grid(of_key(t)), (float)kBins);
-    if (from < 0 || bin == kBins - 1) continue;
-    n += p.bin_count[(first + b) * kBins + from];
-    m += (double)p.bin_mass[(first + b) * kBins + from] * wt.of(of_key(t));
-  }
-  const unsigned mine = n;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double om = __shfl_up(m, d, 64);
-    const unsigned on = __shfl_up(n, d, 64);
-    if (lane >= d) m += om, n += on;
-  }
-  if (lane == 63) wave_mass[wave] = m, wave_count[wave] = n;
-  if (threadIdx.x < 3) found[threadIdx.x] = kBins;
-  __syncthreads();
-  for (int w = 0; w < wave; w++) m += wave_mass[w], n += wave_count[w];
-  sums[bin] = m, counts[bin] = n;
-  // (a cut below the bins, where weights count as 0, is none)
-  if (set.cut_k && bin < kBins - 1 && (int64_t)n >= set.k) atomicMin(&found[0], bin);
-  __syncthreads();
-  const bool cut_k = set.cut_k && found[0] < kBins;
-  const int bin_k = cut_k ? found[0] : -1;
-  const double total = sums[kBins - 1];
-  if (set.cut_p) {
-    // the sums here are rounded: the bins that the cut can lie in, with a margin
-    const double least = cut_k ? (bin_k > 0 ? sums[bin_k - 1] : 0) : total, most = cut_k ? sums[bin_k] : total;
-    if (mine > 0 && m >= (double)set.top_p * least * (1 - 1e-9)) atomicMin(&found[1], bin);
-    if (mine > 0 && m >= (double)set.top_p * most * (1 + 1e-9)) atomicMin(&found[2], bin);
+  if (set.binned()) {
     __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    int lo = bin_k, hi = bin_k;
-    if (set.cut_p) {
-      hi = min(found[2], cut_k ? bin_k : kBins - 2);
-      lo = min(found[1], hi);
+    // the blocks' bins, as bins of the row
+    const int mine = threadIdx.x;
+    double m[1] = {0}, total = 0;
+    unsigned n[1] = {0};
+#pragma unroll 8
+    for (unsigned b = 0; b < p.blocks; b++) {
+      const int from = mine - shift[b];
+      const bool any = from >= 0 && mine < kBins - 1;
+      const u64 v = p.bins[(first + b) * kBins + (any ? from : 0)];
+      n[0] += any ? (unsigned)(v >> kPackBits) : 0;
+      m[0] += any ? (double)((v & ((1ull << kPackBits) - 1)) << kPackShift) * scale[b] : 0;
+      total += (double)p.mass[(first + b) * kBlockSegments] * scale[b];
     }
-    plan.bin_k = bin_k;
+    const Cuts cuts = find_cuts(m, n, set, total, find);
+    plan.cuts = cuts;
     plan.total = total;
-    if (cut_k && bin_k > 0) plan.above_k = counts[bin_k - 1], plan.mass_above_k = sums[bin_k - 1];
-    if (!cut_k && !set.cut_p) {  // top-k below the bins: all that counts
-      plan.lo = kBins;
-    } else if (counts[max(hi, bin_k)] <= kList) {
-      plan.lo = 0, plan.hi = max(hi, bin_k);
+    if (cuts.bin_k < 0 && !set.cut_p) {
+      // top-k below the bins: all that counts is kept
+    } else if (cuts.through <= kList) {
+      plan.lo = 0, plan.all = 1;
     } else {
-      plan.lo = lo, plan.hi = hi;
-      const unsigned listed = counts[hi] - (lo > 0 ? counts[lo - 1] : 0) + (bin_k > hi ? counts[bin_k] - counts[bin_k - 1] : 0);
+      plan.lo = set.cut_p ? cuts.p_lo : cuts.bin_k;
+      unsigned listed = set.cut_p ? cuts.through_p - cuts.above_p : 0;
+      if (cuts.bin_k > cuts.p_hi) listed += cuts.through - cuts.above_k;
+      plan.need_k = set.cut_p && cuts.bin_k > cuts.p_hi;
       if (listed > kList) plan.mode = kAlone;
     }
     if (!(fabsf(grid_top) < kGridMost)) plan.mode = kAlone;
-    p.plan[rr] = plan;
-  }
+  }  // else min-p alone: every token by its own weight
+  if (threadIdx.x == 0) p.plan[rr] = plan;
 }
-
-// A list in LDS, the elements of bins `lo` to `hi`.
-struct List {
-  const u32x2* at;
-  int n, lo, hi;
-  Bins bins;
-  float grid_top;
-  template <class F>
-  __device__ void each(F f) const {
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const u32x2 e = at[i];
-      const int b = bins.of(of_key(e.x), grid_top);
-      if (b >= lo && b <= hi) f(e.x, (int)e.y);
-    }
-  }
-};
 
 template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void k_sample_cut(SampleParams p) {
-  __shared__ CutLds sh;
-  __shared__ u64 mass[kMostSegments];
+  __shared__ u64 lds_sum[kWaves];
   __shared__ u32x2 list[kList];
   __shared__ unsigned lds_n, lds_from;
-  __shared__ bool lds_last;
   const unsigned rr = blockIdx.x / p.blocks, b = blockIdx.x % p.blocks;
   const Plan plan = p.plan[rr];
-  if (plan.mode == kDone || (plan.mode == kAlone && b != 0)) return;
+  if (plan.mode != kListed) return;
   const int64_t r = p.row0 + rr;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const Row<kBf16> row(p.a, r);
+  const Settings set(p.a, r);
+  const Part<kBf16> part(row, b);
+  const Weights wt(of_key(plan.top), set.temperature);
+  const Bins bins(set.temperature);
+  const float grid_top = bins.grid(of_key(plan.top));
+  const Cuts& cuts = plan.cuts;
+  const int list_hi = plan.all ? max(cuts.p_hi, cuts.bin_k) : cuts.p_hi;
+  if (threadIdx.x == 0) lds_n = 0;
+  __syncthreads();
+  u64* row_mass = p.mass + (int64_t)rr * p.blocks * kBlockSegments;
+  u64 above_k = 0;
+#pragma unroll
+  for (int t = 0; t < kTurns; t++) {
+    u64 m = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; j++) {
+      const float x = part.x[t][j];
+      const int i = bins.of(x, grid_top);
+      if (i < plan.lo || (plan.need_k && i < cuts.bin_k)) {
+        const double w = wt.of(x);
+        if (i < plan.lo && !(w < set.min_w)) m += Weights::units(w);
+        above_k += Weights::units(w);
+      }
+      if (i >= plan.lo && (i <= list_hi || i == cuts.bin_k) && x > -INFINITY) {
+        const unsigned at = atomicAdd(&lds_n, 1u);
+        if (at < kList) list[at] = (u32x2){key_of(x), (unsigned)row.index_of(part.group(t), j)};
+      }
+    }
+    if (plan.lo > 0) {
+      m = sum_wave64(m);
+      if (lane == 0) row_mass[part.segment(t)] = m;
+    }
+  }
+  if (plan.need_k) {
+    above_k = sum_block(above_k, lds_sum);
+    if (threadIdx.x == 0) atomicAdd(&p.plan[rr].mass_k, above_k);
+  }
+  __syncthreads();
+  const unsigned n = min(lds_n, (unsigned)kList);
+  if (threadIdx.x == 0) lds_from = n ? atomicAdd(&p.plan[rr].listed, n) : 0;
+  __syncthreads();
+  u32x2* row_list = p.list + (int64_t)rr * kList;
+  for (unsigned i = threadIdx.x; i < n; i += kThreads)
+    if (lds_from + i < kList) row_list[lds_from + i] = list[i];
+}
+
+// The lists are cut, and the tokens drawn: one row a block.
+template <bool kBf16>
+__global__ __launch_bounds__(kThreads) void k_sample_draw(SampleParams p) {
+  __shared__ CutLds sh;
+  __shared__ u64 mass[kMostSegments];
+  __shared__ ListLds list;
+  __shared__ RankLds rk;
+  const unsigned rr = blockIdx.x;
+  const Plan plan = p.plan[rr];
+  if (plan.mode == kDone) return;
+  const int64_t r = p.row0 + rr;
   const SampleArgs& a = p.a;
   const Row<kBf16> row(a, r);
   const Settings set(a, r);
@@ -735,85 +1029,42 @@ __global__ __launch_bounds__(kThreads) void k_sample_cut(SampleParams p) {
   const Weights wt(of_key(plan.top), set.temperature);
   const Bins bins(set.temperature);
   const float grid_top = bins.grid(of_key(plan.top));
-  if (threadIdx.x == 0) lds_n = 0;
-  __syncthreads();
-  u64* row_mass = p.mass + (int64_t)rr * p.blocks * kBlockSegments;
-#pragma unroll
-  for (int t = 0; t < kTurns; t++) {
-    const int s = (int)b * kBlockSegments + t * kWaves + wave, g = s * 64 + lane;
-    float x[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; j++) x[j] = -INFINITY;
-    if (g < row.groups()) row.load(g, x);
-    u64 m = 0;
-#pragma unroll
-    for (int j = 0; j < kEach; j++) {
-      const int bin = bins.of(x[j], grid_top);
-      if (bin < plan.lo) {
-        const double w = wt.of(x[j]);
-        if (!(w < set.min_w)) m += Weights::units(w);
-      } else if ((bin <= plan.hi || bin == plan.bin_k) && x[j] > -INFINITY) {
-        const unsigned at = atomicAdd(&lds_n, 1u);
-        if (at < kList) list[at] = (u32x2){key_of(x[j]), (unsigned)row.index_of(g, j)};
-      }
-    }
-    if (plan.lo > 0) {
-      m = sum_wave64(m);
-      if (lane == 0) row_mass[s] = m;
-    }
+  const Cuts& cuts = plan.cuts;
+  const u64* row_mass = p.mass + (int64_t)rr * p.blocks * kBlockSegments;
+  const u32x2* row_list = p.list + (int64_t)rr * kList;
+  const int all = (int)min(plan.listed, (unsigned)kList);
+  for (int i = threadIdx.x; i < all; i += kThreads) {
+    list.at[i] = row_list[i];
+    list.units[i] = Weights::units(wt.of(of_key(list.at[i].x)));
   }
-  __syncthreads();
-  const unsigned n = min(lds_n, (unsigned)kList);
-  if (threadIdx.x == 0) lds_from = n ? atomicAdd(&p.plan[rr].listed, n) : 0;
-  __syncthreads();
-  u32x2* row_list = p.list + (int64_t)rr * kList;
-  for (unsigned i = threadIdx.x; i < n; i += kThreads)
-    if (lds_from + i < kList) row_list[lds_from + i] = list[i];
-  // the row's last block goes on
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) lds_last = atomicAdd(&p.plan[rr].ticket, 1u) == p.blocks - 1;
-  __syncthreads();
-  if (!lds_last) return;
-  __threadfence();
-
-  if (threadIdx.x == 0) lds_n = min(atomicAdd(&p.plan[rr].listed, 0u), (unsigned)kList);
-  __syncthreads();
-  const int all = (int)lds_n, segments = row.segments();
-  for (int i = threadIdx.x; i < all; i += kThreads) list[i] = row_list[i];
   u64 sure = 0;
-  for (int s = threadIdx.x; s < segments; s += kThreads) {
+  for (int s = threadIdx.x; s < row.segments(); s += kThreads) {
     mass[s] = plan.lo > 0 ? row_mass[s] : 0;
     sure += mass[s];
   }
-  sure = sum_block(sure, sh.wave_sum);  // (and a barrier)
+  sure = sum_block(sure, sh.wave_sum);  // (and barriers)
   Kept kept = {0, 0x7FFFFFFF, set.min_w};
-  const bool cut_k = plan.bin_k >= 0;
   if (plan.lo < kBins) {
-    // top-k cuts bin_k; top-p the listed bins, above which lies what is sure (that
-    // min-p has left; where it has taken some, it takes all of the list as well)
-    const List in_k = {list, all, plan.bin_k, plan.bin_k, bins, grid_top};
-    const List in_p = {list, all, plan.lo, plan.hi, bins, grid_top};
-    u64 above = 0;
-    if (cut_k) {
-      if (plan.lo == 0) {
-        const List over = {list, all, 0, plan.bin_k - 1, bins, grid_top};
-        over.each([&](unsigned key, int) { above += Weights::units(wt.of(of_key(key))); });
-        above = sum_block(above, sh.wave_sum);
-      } else {
-        above = (u64)plan.mass_above_k;
-      }
+    // What lies above the cuts.  (Where min-p has taken some of the sure tokens, it
+    // takes all that are listed too, and where top-p cuts them says nothing.)
+    u64 mass_k = sure, mass_p = sure;
+    if (plan.all) {
+      mass_k = List{list, all, 0, cuts.bin_k - 1, bins, grid_top}.mass(sh.wave_sum);
+      mass_p = List{list, all, 0, cuts.p_lo - 1, bins, grid_top}.mass(sh.wave_sum);
+    } else if (plan.need_k) {
+      mass_k = plan.mass_k;
+    } else if (set.cut_p && cuts.bin_k >= 0) {  // bin_k is one of top-p's bins
+      mass_k = sure + List{list, all, plan.lo, cuts.bin_k - 1, bins, grid_top}.mass(sh.wave_sum);
     }
-    kept = cut_both<kBf16>(in_k, {0, plan.above_k, above}, cut_k, (unsigned)set.k, in_p, {0, 0, sure}, set.cut_p, set.top_p,
-                           plan.total, wt, set.min_w, sh);
+    kept = cut_list<kBf16>(list, all, cuts, mass_k, mass_p, plan.total, set, wt, bins, grid_top, rk, sh);
     __syncthreads();
     for (int i = threadIdx.x; i < all; i += kThreads) {
-      const double w = wt.of(of_key(list[i].x));
-      if (kept.has(list[i].x, (int)list[i].y, w)) atomicAdd(&mass[row.segment_of((int)list[i].y)], Weights::units(w));
+      const u32x2 e = list.at[i];
+      if (kept.has(e.x, (int)e.y, wt.of(of_key(e.x)))) atomicAdd(&mass[row.segment_of((int)e.y)], list.units[i]);
     }
   }
   __syncthreads();
-  if (wave == 0) draw<kBf16>(a, r, row, mass, kept, [](int) { return 1.0; }, [&](int) { return wt; });
+  if (threadIdx.x < 64) draw<kBf16>(a, r, row, mass, kept, [](int) { return 1.0; }, [&](int) { return wt; });
 }
 
 // Blocks of a row whose groups begin up to `lead` elements before it.
@@ -821,12 +1072,12 @@ unsigned row_blocks(int64_t vocab, int lead = kEach - 1) {
   constexpr int64_t kBlock = (int64_t)kBlockSegments * kSegment;
   return (unsigned)((vocab + lead + kBlock - 1) / kBlock);
 }
-bool one_block(int64_t vocab) { return vocab <= 8192; }
+bool one_block(int64_t vocab) { return row_blocks(vocab) == 1; }
 
 // Workspace of a long row, and the rows of a launch: 64 MiB of it, a row at least.
 int64_t row_bytes(int64_t vocab) {
   const int64_t b = row_blocks(vocab);
-  return (b * (8 + kBlockSegments * 8 + kBins * 12) + (int64_t)sizeof(Plan) + kList * 8 + 15) / 16 * 16;
+  return (b * (8 + kBlockSegments * 8 + kBins * 8) + (int64_t)sizeof(Plan) + kList * 8 + 15) / 16 * 16;
 }
 int64_t rows_at_once(int64_t rows, int64_t vocab) {
   return std::min(rows, std::max<int64_t>(1, ((int64_t)64 << 20) / row_bytes(vocab)));
@@ -850,11 +1101,10 @@ hipError_t launch_sample(const SampleArgs& a, bool bf16, void* workspace, hipStr
   const bool same = a.rows == 1 || a.stride % kEach == 0;  // all rows begin alike
   p.blocks = row_blocks(a.vocab, same ? (int)((uintptr_t)a.logits / (bf16 ? 2 : 4) % kEach) : kEach - 1);
   p.mass = (u64*)workspace;
-  p.bin_mass = p.mass + most * p.blocks * kBlockSegments;
-  p.list = (u32x2*)(p.bin_mass + most * p.blocks * kBins);
+  p.bins = p.mass + most * p.blocks * kBlockSegments;
+  p.list = (u32x2*)(p.bins + most * p.blocks * kBins);
   p.plan = (Plan*)(p.list + most * kList);
-  p.bin_count = (unsigned*)(p.plan + most);
-  p.tops = p.bin_count + most * p.blocks * kBins;
+  p.tops = (unsigned*)(p.plan + most);
   p.where = p.tops + most * p.blocks;
   // (a row without a cut is finished by the second launch)
   const bool plain = !a.temperature_of && a.temperature > 0 && !a.top_k_of && (a.top_k <= 0 || a.top_k >= a.vocab) &&
@@ -865,11 +1115,15 @@ hipError_t launch_sample(const SampleArgs& a, bool bf16, void* workspace, hipStr
     if (bf16) {
       k_sample_scan<true><<<all, dim3(kThreads), 0, st>>>(p);
       k_sample_plan<true><<<each, dim3(kBins), 0, st>>>(p);
-      if (!plain) k_sample_cut<true><<<all, dim3(kThreads), 0, st>>>(p);
+      if (plain) continue;
+      k_sample_cut<true><<<all, dim3(kThreads), 0, st>>>(p);
+      k_sample_draw<true><<<each, dim3(kThreads), 0, st>>>(p);
     } else {
       k_sample_scan<false><<<all, dim3(kThreads), 0, st>>>(p);
       k_sample_plan<false><<<each, dim3(kBins), 0, st>>>(p);
-      if (!plain) k_sample_cut<false><<<all, dim3(kThreads), 0, st>>>(p);
+      if (plain) continue;
+      k_sample_cut<false><<<all, dim3(kThreads), 0, st>>>(p);
+      k_sample_draw<false><<<each, dim3(kThreads), 0, st>>>(p);
     }
   }
   return hipGetLastError();
