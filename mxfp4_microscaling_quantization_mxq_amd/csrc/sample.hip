@@ -12,10 +12,11 @@
 //
 // A row's settings decide what is done.  Greedy: the index of the largest.
 // Nothing cut off: the weights' sums of segments of 512 tokens, then the segment
-// and the token that u falls into.  Top-k and top-p: a histogram over 1024 bins of
-// 1/32 of the exponent names the bins that a cut lies in (a margin covers its
-// rounded weights); their tokens are listed (2048 at most) and ranked, each
-// against all others, with exact sums.  A cut in a bin with more tokens than
+// and the token that u falls into.  Top-k and top-p: a histogram over 512 bins of
+// 1/16 of the exponent names the bins that a cut lies in (a margin covers its
+// rounded weights); their tokens are listed (4096 at most) and the cut is
+// found in 64 finer bins of these, whose tokens are ranked, each against all others,
+// with exact sums.  A cut in a bin with more tokens than
 // that (equal logits, mostly) is found eight bits of the logits at a time, in
 // passes over the row (whole_row).
 //
@@ -50,10 +51,14 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kTurns = 2;                          // segments of a wave of k_sample_scan
 constexpr int kBlockSegments = kWaves * kTurns;    // 8192 logits a block
 constexpr int kMostBlocks = (kMostSegments + kBlockSegments - 1) / kBlockSegments;
-constexpr int kBins = 1024;     // the last one: weights below e^-31.9, which count as 0
-constexpr float kBinsPer = 32;  // of the exponent
-constexpr int kList = 2048;
+constexpr int kBins = kThreads;  // the last one: weights below e^-31.8, which count as 0
+constexpr float kBinsPer = 16;   // of the exponent
+constexpr int kList = 4096;
 constexpr int kRank = kThreads;  // tokens that are ranked, one a thread
+constexpr int kFew = 96;         // up to which they are ranked at once
+// Up to which a row's whole list is ranked by order and by index: 128 tokens take
+// 6 us, 192 about 13, 440 60, the other way through segments 15 for any number.
+constexpr int kFewListed = 192;
 // A histogram's entry: the number of tokens, and their weights in units of 2^-36
 // (cut off, so up to 2^20 of them are less than 2^-16 of the largest below).
 constexpr int kPackBits = 50, kPackShift = 7;
@@ -367,37 +372,39 @@ template <bool kBf16, class Scale, class Wts>
 __device__ void draw(const SampleArgs& a, int64_t r, const Row<kBf16>& row, const u64* mass, const Kept& kept,
                      Scale scale_of, Wts weights_of) {
   const int lane = threadIdx.x & 63, groups = row.groups(), segments = row.segments();
-  // sums of runs of 64 segments a step, in order
-  double sum = 0;
-  for (int s0 = 0; s0 < segments; s0 += 64) {
-    double v = s0 + lane < segments ? (double)mass[s0 + lane] * scale_of(s0 + lane) : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_up(v, d, 64);
-      if (lane >= d) v += o;
-    }
-    sum += __shfl(v, 63, 64);
+  // a lane takes a run of segments: their sum, and (last) the last one with any mass
+  const int each = (segments + 63) / 64, s0 = lane * each, s1 = min(s0 + each, segments);
+  double own = 0;
+  int last = -1;
+  for (int s = s0; s < s1; s++) {
+    own += (double)mass[s] * scale_of(s);
+    if (mass[s]) last = s;
   }
-  const double goal = fmin(fmax((double)a.u[r], 0.0), 1.0) * sum;
-  double run = 0, run_at = 0, run_last = 0;
-  int at = -1, last = 0;  // the segment, and the last one with any mass
-  for (int s0 = 0; s0 < segments && at < 0; s0 += 64) {
-    const u64 m = s0 + lane < segments ? mass[s0 + lane] : 0;
-    double v = m ? (double)m * scale_of(s0 + lane) : 0;
+  double incl = own;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_up(v, d, 64);
-      if (lane >= d) v += o;
-    }
-    double before = __shfl_up(v, 1, 64);
-    before = run + (lane ? before : 0);
-    const u64 some = __builtin_amdgcn_ballot_w64(m > 0);
-    const u64 past = __builtin_amdgcn_ballot_w64(m > 0 && run + v > goal);
-    if (some) last = s0 + 63 - __builtin_clzll(some), run_last = __shfl(before, 63 - __builtin_clzll(some), 64);
-    if (past) at = s0 + __builtin_ctzll(past), run_at = __shfl(before, __builtin_ctzll(past), 64);
-    run += __shfl(v, 63, 64);
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
   }
-  if (at < 0) at = last, run_at = run_last;  // u = 1: the last that may be drawn
+  const double sum = __shfl(incl, 63, 64), goal = fmin(fmax((double)a.u[r], 0.0), 1.0) * sum;
+  double run_at = __shfl_up(incl, 1, 64);  // before the run, then before the segment
+  if (lane == 0) run_at = 0;
+  const u64 past = __builtin_amdgcn_ballot_w64(last >= 0 && incl > goal), some = __builtin_amdgcn_ballot_w64(last >= 0);
+  const int runner = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : 0;  // (u = 1: the last)
+  int at = last;
+  if (lane == runner) {
+    double run = run_at;
+    for (int s = s0; s < s1; s++) {
+      const double v = (double)mass[s] * scale_of(s);
+      if (mass[s]) run_at = run;
+      if (mass[s] && run + v > goal) {
+        at = s;
+        break;
+      }
+      run += v;
+    }
+  }
+  at = max(0, __shfl(at, runner, 64)), run_at = __shfl(run_at, runner, 64);
   const double left = (goal - run_at) / scale_of(at);
   const Weights wt = weights_of(at);
   const int group = at * 64 + lane;
@@ -412,13 +419,13 @@ __device__ void draw(const SampleArgs& a, int64_t r, const Row<kBf16>& row, cons
     m[j] = kept.has(key_of(x[j]), row.index_of(group, j), w) ? Weights::units(w) : 0;
     mine += m[j];
   }
-  u64 incl = mine;
+  u64 through = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const u64 o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
+    const u64 o = __shfl_up(through, d, 64);
+    if (lane >= d) through += o;
   }
-  u64 before = incl - mine;
+  u64 before = through - mine;
   int pick = -1, end = -1;
 #pragma unroll
   for (int j = 0; j < kEach; j++) {
@@ -509,6 +516,8 @@ struct Part {
 };
 
 __device__ __forceinline__ u64 packed(u64 units) { return (1ull << kPackBits) + (units >> kPackShift); }
+__device__ __forceinline__ unsigned packed_count(u64 v) { return (unsigned)(v >> kPackBits); }
+__device__ __forceinline__ double packed_mass(u64 v) { return (double)((v & ((1ull << kPackBits) - 1)) << kPackShift); }
 
 // Where a row's cuts lie: top-k in bin_k (-1: it does not cut), top-p in one of
 // the bins p_lo to p_hi; the tokens above these, and down to the last of them.
@@ -524,46 +533,28 @@ struct FindLds {
   int found[3];
 };
 // The first bin of which `here` holds, into *found (it holds of all after it).
-template <int kPer>
-__device__ __forceinline__ void first_bin(const bool (&here)[kPer], int bin0, int* found) {
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < kPer; i++) any |= here[i];
-  const u64 who = __builtin_amdgcn_ballot_w64(any);
-  if (!who || (int)(threadIdx.x & 63) != __builtin_ctzll(who)) return;
-  int at = 0;
-#pragma unroll
-  for (int i = kPer - 1; i >= 0; i--) at = here[i] ? i : at;
-  atomicMin(found, bin0 + at);
+__device__ __forceinline__ void first_bin(bool here, int* found) {
+  const u64 who = __builtin_amdgcn_ballot_w64(here);
+  if (who && (int)(threadIdx.x & 63) == __builtin_ctzll(who)) atomicMin(found, (int)threadIdx.x);
 }
-// m, n: weights (as rounded in a histogram) and numbers of this thread's bins.
-template <int kPer>
-__device__ Cuts find_cuts(double (&m)[kPer], unsigned (&n)[kPer], const Settings& set, double total, FindLds& sh) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bin0 = (int)threadIdx.x * kPer;
-#pragma unroll
-  for (int i = 1; i < kPer; i++) m[i] += m[i - 1], n[i] += n[i - 1];
-  double mm = m[kPer - 1];
-  unsigned nn = n[kPer - 1];
+// m, n: weights (as rounded in a histogram) and number of this thread's bin.
+__device__ Cuts find_cuts(double m, unsigned n, const Settings& set, double total, FindLds& sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bin = (int)threadIdx.x;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const double om = __shfl_up(mm, d, 64);
-    const unsigned on = __shfl_up(nn, d, 64);
-    if (lane >= d) mm += om, nn += on;
+    const double om = __shfl_up(m, d, 64);
+    const unsigned on = __shfl_up(n, d, 64);
+    if (lane >= d) m += om, n += on;
   }
-  if (lane == 63) sh.wave_mass[wave] = mm, sh.wave_count[wave] = nn;
+  if (lane == 63) sh.wave_mass[wave] = m, sh.wave_count[wave] = n;
   if (threadIdx.x < 3) sh.found[threadIdx.x] = kBins;
   __syncthreads();
-  mm -= m[kPer - 1], nn -= n[kPer - 1];
-  for (int w = 0; w < wave; w++) mm += sh.wave_mass[w], nn += sh.wave_count[w];
-  bool here[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    sh.sums[bin0 + i] = m[i] += mm;
-    sh.counts[bin0 + i] = n[i] += nn;
-    // (a cut below the bins, where weights count as 0, is none)
-    here[i] = set.cut_k && bin0 + i < kBins - 1 && (int64_t)n[i] >= set.k;
-  }
-  first_bin(here, bin0, &sh.found[0]);
+  for (int w = 0; w < kBins / 64; w++)
+    if (w < wave) m += sh.wave_mass[w], n += sh.wave_count[w];
+  sh.sums[bin] = m, sh.counts[bin] = n;
+  // (a cut below the bins, where weights count as 0, is none)
+  first_bin(set.cut_k && bin < kBins - 1 && (int64_t)n >= set.k, &sh.found[0]);
   __syncthreads();
   Cuts c = {-1, 0, -1, 0, 0, 0, 0};
   if (set.cut_k && sh.found[0] < kBins) c.bin_k = sh.found[0];
@@ -572,12 +563,8 @@ __device__ Cuts find_cuts(double (&m)[kPer], unsigned (&n)[kPer], const Settings
   if (set.cut_p) {
     const double least = c.bin_k < 0 ? total : c.bin_k > 0 ? sh.sums[c.bin_k - 1] : 0;
     const double most = c.bin_k < 0 ? total : sh.sums[c.bin_k] * (1 + kMargin);
-#pragma unroll
-    for (int i = 0; i < kPer; i++) here[i] = n[i] > 0 && m[i] >= (double)set.top_p * least * (1 - kMargin);
-    first_bin(here, bin0, &sh.found[1]);
-#pragma unroll
-    for (int i = 0; i < kPer; i++) here[i] = n[i] > 0 && m[i] >= (double)set.top_p * most * (1 + kMargin);
-    first_bin(here, bin0, &sh.found[2]);
+    first_bin(n > 0 && m >= (double)set.top_p * least * (1 - kMargin), &sh.found[1]);
+    first_bin(n > 0 && m >= (double)set.top_p * most * (1 + kMargin), &sh.found[2]);
     __syncthreads();
     c.p_hi = min(sh.found[2], c.bin_k < 0 ? kBins - 2 : c.bin_k);
     c.p_lo = min(sh.found[1], c.p_hi);
@@ -618,17 +605,25 @@ struct List {
   }
 };
 
+struct Range {
+  unsigned lo, hi;  // of keys
+};
 // Tokens to rank: order (key, then the complement of the index) and units.
 struct RankLds {
   u64 order[kRank], units[kRank];
   u64 order_at, mass_at, order_low, mass_low;
   unsigned n, hit;
+  u64 bin_mass[64], above_mass;  // narrowing
+  unsigned bin_count[64], above_count;
+  Range wave_range[kWaves];
 };
-// The source's tokens into LDS; their number (above kRank: not all of them).
-__device__ int gather(const List& src, RankLds& sh) {
+// The source's tokens with keys in a range into LDS; their number (above kRank:
+// not all of them are there).
+__device__ int gather(const List& src, Range in, RankLds& sh) {
   if (threadIdx.x == 0) sh.n = 0, sh.hit = 0;
   __syncthreads();
   src.each_place([&](int i, unsigned key, int index) {
+    if (key < in.lo || key > in.hi) return;
     const unsigned at = atomicAdd(&sh.n, 1u);
     if (at >= kRank) return;
     sh.order[at] = ((u64)key << 32) | ~(unsigned)index;
@@ -636,6 +631,58 @@ __device__ int gather(const List& src, RankLds& sh) {
   });
   __syncthreads();
   return (int)sh.n;
+}
+// The range of the source's keys.
+__device__ Range range_of(const List& src, RankLds& sh) {
+  Range r = {~0u, 0};
+  src.each([&](unsigned key, int) { r.lo = min(r.lo, key), r.hi = max(r.hi, key); });
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    r.lo = min(r.lo, (unsigned)__shfl_xor((int)r.lo, m, 64));
+    r.hi = max(r.hi, (unsigned)__shfl_xor((int)r.hi, m, 64));
+  }
+  if ((threadIdx.x & 63) == 0) sh.wave_range[threadIdx.x >> 6] = r;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; w++) r.lo = min(r.lo, sh.wave_range[w].lo), r.hi = max(r.hi, sh.wave_range[w].hi);
+  return r;
+}
+// 64 bins of a range of keys: the one in which a count or a mass is reached, as
+// the range of its keys; count and mass, of what lies above, are moved to it.
+template <bool kCount>
+__device__ Range narrow(const List& src, Range in, unsigned& count, u64& mass, unsigned k, double reach, RankLds& sh) {
+  const int shift = max(0, 26 - __builtin_clz((in.hi - in.lo) | 1));
+  if (threadIdx.x < 64) sh.bin_mass[threadIdx.x] = 0, sh.bin_count[threadIdx.x] = 0;
+  __syncthreads();
+  src.each_place([&](int i, unsigned key, int) {
+    if (key < in.lo || key > in.hi) return;
+    const unsigned b = (in.hi - key) >> shift;
+    atomicAdd(&sh.bin_count[b], 1u);
+    atomicAdd(&sh.bin_mass[b], src.list.units[i]);
+  });
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    const unsigned n = sh.bin_count[lane];
+    unsigned bn = n;
+    u64 m = sh.bin_mass[lane], bm = m;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const unsigned on = __shfl_up(bn, s, 64);
+      const u64 om = __shfl_up(bm, s, 64);
+      if (lane >= s) bn += on, bm += om;
+    }
+    u64 who = __builtin_amdgcn_ballot_w64(n > 0 && (kCount ? count + bn >= k : (double)(mass + bm) >= reach));
+    const u64 some = __builtin_amdgcn_ballot_w64(n > 0);
+    // (where rounding leaves none, the lowest that holds any)
+    const int owner = who ? __builtin_ctzll(who) : some ? 63 - __builtin_clzll(some) : 0;
+    if (lane == owner) sh.hit = lane, sh.above_count = count + (bn - n), sh.above_mass = mass + (bm - m);
+  }
+  __syncthreads();
+  count = sh.above_count, mass = sh.above_mass;
+  const unsigned b = sh.hit, hi = in.hi - (b << shift), step = (1u << shift) - 1;
+  __syncthreads();
+  return {hi - in.lo < step ? in.lo : hi - step, hi};
 }
 // The last token, in order, that is taken: the one at which a count is complete,
 // or the first at which the mass is.  `count` and `mass` lie above the tokens.
@@ -674,19 +721,26 @@ __device__ Kept cut_list(const ListLds& list, int n, const Cuts& cuts, u64 mass_
   Kept kept = {0, 0x7FFFFFFF, set.min_w};
   u64 order = 0;
   bool few = true;
+  const Range whole = {0, ~0u};
   if (cut_k) {
-    const int c = gather(in_k, rk);
+    unsigned above = cuts.above_k;
+    u64 mass = mass_k;
+    int c = gather(in_k, whole, rk);
+    if (c > kFew) c = gather(in_k, narrow<true>(in_k, range_of(in_k, rk), above, mass, (unsigned)set.k, 0, rk), rk);
     few = c <= kRank;
     if (few) {
-      const Last l = rank<true>(c, cuts.above_k, mass_k, (unsigned)set.k, 0, rk);
+      const Last l = rank<true>(c, above, mass, (unsigned)set.k, 0, rk);
       order = l.order, total = (double)l.mass;
     }
   }
   if (set.cut_p && few) {
-    const int c = gather(in_p, rk);
+    const double reach = fmax((double)set.top_p * total, 0.5);  // (at least one token)
+    unsigned above = 0;
+    u64 mass = mass_p;
+    int c = gather(in_p, whole, rk);
+    if (c > kFew) c = gather(in_p, narrow<false>(in_p, range_of(in_p, rk), above, mass, 0, reach, rk), rk);
     few = c <= kRank;
-    // (at least one token)
-    if (few) order = max(order, rank<false>(c, 0, mass_p, 0, fmax((double)set.top_p * total, 0.5), rk).order);
+    if (few) order = max(order, rank<false>(c, 0, mass, 0, reach, rk).order);
   }
   if (!few)
     return cut_both<kBf16>(in_k, {0, cuts.above_k, mass_k}, cut_k, (unsigned)set.k, in_p, {0, 0, mass_p}, set.cut_p,
@@ -744,14 +798,7 @@ __global__ __launch_bounds__(kThreads) void k_sample_row(SampleArgs a) {
         if (b < kBins - 1 && part.x[t][j] > -INFINITY) atomicAdd(&bin[b], packed(units[t][j]));
       }
     sum = sum_block(sum, sh.wave_sum);
-    double m[kBins / kThreads];
-    unsigned n[kBins / kThreads];
-#pragma unroll
-    for (int i = 0; i < kBins / kThreads; i++) {
-      const u64 v = bin[threadIdx.x * (kBins / kThreads) + i];
-      n[i] = (unsigned)(v >> kPackBits), m[i] = (double)((v & ((1ull << kPackBits) - 1)) << kPackShift);
-    }
-    const Cuts cuts = find_cuts(m, n, set, (double)sum, find);
+    const Cuts cuts = find_cuts(packed_mass(bin[threadIdx.x]), packed_count(bin[threadIdx.x]), set, (double)sum, find);
     if (cuts.bin_k >= 0 || set.cut_p) {
       // the candidates, and what lies above them
       u64 above_k = 0, above_p = 0;
@@ -921,22 +968,25 @@ __global__ __launch_bounds__(kBins) void k_sample_plan(SampleParams p) {
     __syncthreads();
     // the blocks' bins, as bins of the row
     const int mine = threadIdx.x;
-    double m[1] = {0}, total = 0;
-    unsigned n[1] = {0};
+    double m = 0, total = 0;
+    unsigned n = 0;
 #pragma unroll 8
     for (unsigned b = 0; b < p.blocks; b++) {
       const int from = mine - shift[b];
       const bool any = from >= 0 && mine < kBins - 1;
       const u64 v = p.bins[(first + b) * kBins + (any ? from : 0)];
-      n[0] += any ? (unsigned)(v >> kPackBits) : 0;
-      m[0] += any ? (double)((v & ((1ull << kPackBits) - 1)) << kPackShift) * scale[b] : 0;
+      n += any ? packed_count(v) : 0;
+      m += any ? packed_mass(v) * scale[b] : 0;
       total += (double)p.mass[(first + b) * kBlockSegments] * scale[b];
     }
     const Cuts cuts = find_cuts(m, n, set, total, find);
     plan.cuts = cuts;
     plan.total = total;
-    if (cuts.bin_k < 0 && !set.cut_p) {
-      // top-k below the bins: all that counts is kept
+    // the bin in which weights fall below min-p, or one after it
+    const int bin_m = set.min_w > 0 ? (int)fminf(1 - kBinsPer * logf((float)set.min_w), (float)kBins) + 2 : kBins;
+    if ((cuts.bin_k < 0 || bin_m < cuts.bin_k) && (!set.cut_p || bin_m < cuts.p_lo)) {
+      // no cut but min-p's: every token by its own weight (or top-k's lies below
+      // the bins, and all that counts is kept)
     } else if (cuts.through <= kList) {
       plan.lo = 0, plan.all = 1;
     } else {
@@ -1008,6 +1058,72 @@ __global__ __launch_bounds__(kThreads) void k_sample_cut(SampleParams p) {
     if (lds_from + i < kList) row_list[lds_from + i] = list[i];
 }
 
+// A row whose tokens down to its cuts are all listed, at most kFewListed of them: each
+// is ranked against all others, once by order, for the cuts, and once by index,
+// for the draw.  Several threads share a token's comparisons.
+struct FewLds {
+  u64 order[kThreads], units[kThreads], mass[kThreads];  // mass: of the tokens before it, in order or by index
+  unsigned before[kThreads];
+  u64 order_k, mass_k, order_p, sum;
+};
+__device__ void draw_few(const SampleArgs& a, int64_t r, const u32x2* listed, int n, const Settings& set, const Cuts& cuts,
+                         double total, const Weights& wt, FewLds& sh) {
+  const int t = threadIdx.x;
+  int width = 64;
+  while (width < n) width *= 2;
+  const int c = t & (width - 1), parts = kThreads / width, part = t / width;
+  if (t < n) {
+    const u32x2 e = listed[t];
+    sh.order[t] = ((u64)e.x << 32) | ~e.y;
+    sh.units[t] = Weights::units(wt.of(of_key(e.x)));
+  }
+  sh.mass[t] = 0, sh.before[t] = 0;
+  if (t == 0) sh.order_k = sh.order_p = sh.sum = 0;
+  __syncthreads();
+  const u64 order = c < n ? sh.order[c] : 0, own = c < n ? sh.units[c] : 0;
+  if (c < n) {
+    unsigned before = 0;
+    u64 mass = 0;
+#pragma unroll 4
+    for (int j = part; j < n; j += parts) {
+      const bool over = sh.order[j] > order;
+      before += over;
+      mass += over ? sh.units[j] : 0;
+    }
+    if (before) atomicAdd(&sh.before[c], before), atomicAdd(&sh.mass[c], mass);
+  }
+  __syncthreads();
+  const u64 mass = sh.mass[c];
+  if (t < n && cuts.bin_k >= 0 && (int64_t)sh.before[t] + 1 == set.k) sh.order_k = order, sh.mass_k = mass + own;
+  __syncthreads();
+  sh.mass[t] = 0;
+  if (set.cut_p) {
+    const double reach = fmax((double)set.top_p * (cuts.bin_k >= 0 ? (double)sh.mass_k : total), 0.5);
+    if (t < n && (double)(mass + own) >= reach && !((double)mass >= reach)) sh.order_p = order;
+    __syncthreads();
+  }
+  const bool kept = c < n && order >= max(sh.order_k, sh.order_p) && !(wt.of(of_key((unsigned)(order >> 32))) < set.min_w);
+  __syncthreads();
+  if (t < width) sh.units[t] = kept ? own : 0;
+  if (t < n && kept) atomicAdd(&sh.sum, own);
+  __syncthreads();
+  if (kept) {
+    u64 first = 0;
+#pragma unroll 4
+    for (int j = part; j < n; j += parts) first += (unsigned)sh.order[j] >= (unsigned)order ? sh.units[j] : 0;
+    if (first) atomicAdd(&sh.mass[c], first);
+  }
+  __syncthreads();
+  if (t >= n || !kept || own == 0) return;
+  const u64 run = sh.mass[t], sum = sh.sum;
+  const double goal = fmin(fmax((double)a.u[r], 0.0), 1.0) * (double)sum;
+  // (u = 1: the last)
+  if (((double)run > goal && !((double)(run - own) > goal)) || (run == sum && !((double)sum > goal))) {
+    a.tokens[r] = (int)~(unsigned)order;
+    a.shares[r] = (float)(wt.of(of_key((unsigned)(order >> 32))) * 0x1p43 / (double)sum);
+  }
+}
+
 // The lists are cut, and the tokens drawn: one row a block.
 template <bool kBf16>
 __global__ __launch_bounds__(kThreads) void k_sample_draw(SampleParams p) {
@@ -1015,6 +1131,7 @@ __global__ __launch_bounds__(kThreads) void k_sample_draw(SampleParams p) {
   __shared__ u64 mass[kMostSegments];
   __shared__ ListLds list;
   __shared__ RankLds rk;
+  __shared__ FewLds few;
   const unsigned rr = blockIdx.x;
   const Plan plan = p.plan[rr];
   if (plan.mode == kDone) return;
@@ -1033,6 +1150,10 @@ __global__ __launch_bounds__(kThreads) void k_sample_draw(SampleParams p) {
   const u64* row_mass = p.mass + (int64_t)rr * p.blocks * kBlockSegments;
   const u32x2* row_list = p.list + (int64_t)rr * kList;
   const int all = (int)min(plan.listed, (unsigned)kList);
+  if (plan.all && all <= kFewListed) {
+    draw_few(a, r, row_list, all, set, cuts, plan.total, wt, few);
+    return;
+  }
   for (int i = threadIdx.x; i < all; i += kThreads) {
     list.at[i] = row_list[i];
     list.units[i] = Weights::units(wt.of(of_key(list.at[i].x)));
