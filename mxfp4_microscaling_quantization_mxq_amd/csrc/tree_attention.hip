@@ -20,6 +20,8 @@
 // Split.  As for one token: a unit is one sequence, one cache head and a group
 // of its rows; the tiles of all units in order are cut into equal ranges, one a
 // block, and ranges that end inside a unit leave partial results to be joined.
+#include <type_traits>
+
 #include "mxq_attend.h"
 
 namespace mxq {
@@ -37,28 +39,29 @@ struct TreeParams {
   unsigned group;       // query heads per cache head
   unsigned rows;        // group * drafts
   unsigned row_groups;  // units per sequence and cache head
-  unsigned row_shift;   // 2^row_shift waves of a block take rows of their own, the others tiles
+  unsigned row_shift;   // 2^row_shift waves of a block take rows of their own, the others tiles (k_tree_attend)
   // Workspace, as for one token: records {parts, the block that opened the
   // unit, the unit} by opening block (by_block) or by unit, and two slots of
   // partial results a block.
-  bool by_block;
+  bool by_block, split;  // split: blocks take ranges (k_tree_wide; else units)
   int* parts;
   float *part_o, *part_ml;
 };
 
-// What a sequence's rows may see: tiles [0, a) and [b, b + n - a) of 32 tokens.
+// What a sequence's rows may see: tiles [0, a) and [b, b + n - a) of kT tokens.
 struct TreeSpan {
   int context, end, a, b, n;
 };
+template <int kT>
 __device__ __forceinline__ TreeSpan tree_span(const TreeParams& p, int64_t seq) {
   const int64_t most = min(p.a.table_width << p.c.page_shift, kMaxLen);
   const int64_t context = min((int64_t)max(p.a.context[seq], 0), most), end = min(context + p.a.drafts, most);
   TreeSpan s = {(int)context, (int)end, 0, 0, 0};
   if (p.a.window > 0) {
-    s.a = (int)((min(p.a.first, end) + kTile - 1) / kTile);
-    s.b = max(s.a, (int)(max((int64_t)0, context - p.a.window + 1) / kTile));
+    s.a = (int)((min(p.a.first, end) + kT - 1) / kT);
+    s.b = max(s.a, (int)(max((int64_t)0, context - p.a.window + 1) / kT));
   }
-  const int tiles = (int)((end + kTile - 1) / kTile);
+  const int tiles = (int)((end + kT - 1) / kT);
   s.n = s.a + max(0, tiles - s.b);
   if (s.n == 0) s.b = tiles - 1, s.n = 1;  // nothing to see: a tile that is masked, for the zeros
   return s;
@@ -66,9 +69,122 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeParams& p, int64_t seq) 
 
 __device__ __forceinline__ unsigned below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
-// Tiles of a range.
-__device__ __forceinline__ unsigned range_tiles(unsigned sum, unsigned blocks, unsigned least) {
-  return max((sum + blocks - 1) / blocks, least);
+// Context tokens from here on are inside the window of a row of this depth.
+__device__ __forceinline__ int window_start(const TreeParams& p, int context, int depth) {
+  return (int)max((int64_t)0, context + depth - p.a.window + 1);
+}
+// Tokens t0 .. t0 + 31 that are seen: of the context those from lo on and the
+// first ones, of the drafted ones those of the mask (in LDS, as load_masks lays it out).
+__device__ __forceinline__ unsigned seen_word(const TreeSpan& s, int t0, int lo, int seen_first, const unsigned* mask, int words) {
+  const int to = s.context - t0;
+  unsigned w = (below(to) & ~below(lo - t0)) | below(seen_first - t0);
+  const int at = (-to) >> 5;  // drafted token -to is the word's first
+  if (at >= -1 && at <= 2 * words - 1) {
+    const unsigned* m = mask + 1 + at;
+    w |= (unsigned)((((uint64_t)m[1] << 32) | m[0]) >> ((unsigned)-to & 31u));
+  }
+  return w;
+}
+
+// Into LDS: the masks of `tokens` drafted tokens from token0 on, less what the
+// window hides, each between two empty words; all of them together (any); all
+// tokens' depths; and the largest and smallest depth (far, preset) of these.
+__device__ __forceinline__ void load_masks(const TreeParams& p, int64_t b, const TreeSpan& s, unsigned token0, unsigned tokens,
+                                           unsigned (*mask)[kMaskRow], unsigned* any, int* depths, int* far) {
+  const unsigned words = p.a.words, drafts = (unsigned)p.a.drafts;
+  if (threadIdx.x < drafts) {
+    const uint32_t* m = (const uint32_t*)(p.a.mask + (b * drafts + threadIdx.x) * words);
+    int depth = 0;
+    for (unsigned w = 0; w <= threadIdx.x / 32; w++) depth += __popc(m[w] & below((int)(threadIdx.x - 32 * w)));
+    depths[threadIdx.x] = depth;
+  }
+  if (threadIdx.x < kMaskRow) any[threadIdx.x] = 0;
+  __syncthreads();
+  for (unsigned t = threadIdx.x; t < tokens; t += blockDim.x) {
+    const uint32_t* m = (const uint32_t*)(p.a.mask + (b * drafts + token0 + t) * words);
+    const int depth = depths[token0 + t];
+    atomicMax(&far[0], depth);
+    atomicMin(&far[1], depth);
+    mask[t][0] = 0;
+    for (unsigned w = 0; w < 2 * words; w++) {
+      unsigned v = m[w] & below((int)drafts - (int)(32 * w));
+      if (p.a.window > 0 && p.a.window < p.a.drafts) {
+        unsigned left = v;
+        while (left) {
+          const int bit = __builtin_ctz(left), d = depths[32 * w + bit];
+          left &= left - 1;
+          if (depth - d >= p.a.window && s.context + d >= p.a.first) v &= ~(1u << bit);
+        }
+      }
+      mask[t][1 + w] = v;
+      atomicOr(&any[1 + w], v);
+    }
+    mask[t][1 + 2 * words] = 0;
+  }
+  __syncthreads();
+}
+
+// A block's range of the flattened tiles of kT tokens: [x, end), in the unit (b,
+// head, rg) whose first tile is u_first; `per` tiles a range, at least `least`.
+struct RangeStart {
+  unsigned x, end, u_first, head, rg, per;
+  int64_t b;
+};
+template <int kT>
+__device__ __forceinline__ RangeStart range_start(const TreeParams& p, unsigned least, unsigned* lds_sum, int* lds_at) {
+  // each of 256 threads sums the tiles of a run of sequences; scan over the block
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const unsigned units = p.c.heads * p.row_groups;  // of a sequence
+  const unsigned batch = (unsigned)p.a.batch, each = (batch + kThreads - 1) / kThreads;
+  const unsigned b0 = min(threadIdx.x * each, batch), b1 = min(b0 + each, batch);
+  unsigned own = 0;
+  for (unsigned k = b0; k < b1; k++) own += tree_span<kT>(p, k).n * units;
+  unsigned incl = own;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const unsigned o = __shfl_up(incl, m, 64);
+    if (lane >= m) incl += o;
+  }
+  if (lane == 63) lds_sum[wave] = incl;
+  __syncthreads();
+  unsigned sum = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; w++) {
+    if (w < wave) before += lds_sum[w];
+    sum += lds_sum[w];
+  }
+  RangeStart r;
+  sum = uniform(sum);
+  r.per = max((sum + gridDim.x - 1) / gridDim.x, least);
+  r.x = blockIdx.x * r.per;
+  r.end = min(r.x + r.per, sum);
+  unsigned at = before + incl - own;  // first tile of this thread's sequences
+  if (r.x >= at && r.x < at + own) {
+    unsigned k = b0, n = tree_span<kT>(p, k).n;
+    while (r.x >= at + n * units) {
+      at += n * units;
+      n = tree_span<kT>(p, ++k).n;
+    }
+    const unsigned u = (r.x - at) / n;
+    lds_at[0] = (int)k, lds_at[1] = (int)u, lds_at[2] = (int)(at + u * n);
+  }
+  if (p.by_block && threadIdx.x == 0) p.parts[4 * blockIdx.x] = 0;
+  __syncthreads();
+  r.b = uniform(lds_at[0]);
+  const unsigned u = uniform(lds_at[1]);
+  r.u_first = uniform(lds_at[2]);
+  r.head = u / p.row_groups, r.rg = u % p.row_groups;
+  return r;
+}
+
+// Largest value and sum over the two halves of a wave, in every lane.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(w[0]) + __uint_as_float(w[1]);
 }
 
 template <int D, bool kFp4, int kTerms, int N, bool kRanges>
@@ -79,8 +195,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
   constexpr int kPad = D + 4;
   __shared__ float lds_o[kWaves][kSet][kPad];
   __shared__ float lds_m[kWaves][kSet], lds_l[kWaves][kSet], lds_top[kWaves][kSet];
-  __shared__ unsigned lds_mask[kWaves * N * kSet][kMaskRow];
-  __shared__ int lds_depth[kThreads];
+  __shared__ unsigned lds_mask[2 * N * kSet][kMaskRow];
+  __shared__ unsigned lds_any[kMaskRow];
+  __shared__ int lds_depth[kThreads], lds_far[2];
   __shared__ unsigned lds_sum[kWaves];
   __shared__ int lds_at[3];
 
@@ -99,52 +216,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
     id /= p.row_groups;
     head = id % p.c.heads;
     b = id / p.c.heads;
-    s = tree_span(p, b);
+    s = tree_span<kTile>(p, b);
     x = u_first = 0;
     end = s.n;
   } else {
-    // each thread sums the tiles of a run of sequences; scan over the block
-    const unsigned units = p.c.heads * p.row_groups;  // of a sequence
-    const unsigned batch = (unsigned)p.a.batch, each = (batch + kThreads - 1) / kThreads;
-    const unsigned b0 = min(threadIdx.x * each, batch), b1 = min(b0 + each, batch);
-    unsigned own = 0;
-    for (unsigned k = b0; k < b1; k++) own += tree_span(p, k).n * units;
-    unsigned incl = own;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const unsigned o = __shfl_up(incl, m, 64);
-      if (lane >= m) incl += o;
-    }
-    if (lane == 63) lds_sum[wave] = incl;
-    __syncthreads();
-    unsigned sum = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-      if (w < wave) before += lds_sum[w];
-      sum += lds_sum[w];
-    }
-    sum = uniform(sum);
-    per = range_tiles(sum, gridDim.x, per_tile);
-    x = blockIdx.x * per;
-    end = min(x + per, sum);
-    unsigned at = before + incl - own;  // first tile of this thread's sequences
-    if (x >= at && x < at + own) {
-      unsigned k = b0, n = tree_span(p, k).n;
-      while (x >= at + n * units) {
-        at += n * units;
-        n = tree_span(p, ++k).n;
-      }
-      const unsigned u = (x - at) / n;
-      lds_at[0] = (int)k, lds_at[1] = (int)u, lds_at[2] = (int)(at + u * n);
-    }
-    if (p.by_block && threadIdx.x == 0) p.parts[4 * blockIdx.x] = 0;
-    if (x >= end) return;
-    __syncthreads();
-    b = uniform(lds_at[0]);
-    const unsigned u = uniform(lds_at[1]);
-    u_first = uniform(lds_at[2]);
-    s = tree_span(p, b);
-    head = u / p.row_groups, rg = u % p.row_groups;
+    const RangeStart r = range_start<kTile>(p, per_tile, lds_sum, lds_at);
+    if (r.x >= r.end) return;
+    x = r.x, end = r.end, u_first = r.u_first, head = r.head, rg = r.rg, per = r.per, b = r.b;
+    s = tree_span<kTile>(p, b);
   }
 
   while (true) {
@@ -152,35 +231,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
     const int first = (int)(x - u_first), last = min(s.n, (int)(end - u_first));
     const unsigned row0 = rg * unit_rows, token0 = row0 / p.group;
     const unsigned tokens = (min(row0 + unit_rows, p.rows) - 1) / p.group - token0 + 1;
-    const unsigned words = p.a.words, drafts = (unsigned)p.a.drafts;
-
-    // the masks of the unit's tokens, less what the window hides, and all depths
-    if (threadIdx.x < drafts) {
-      const uint32_t* m = (const uint32_t*)(p.a.mask + (b * drafts + threadIdx.x) * words);
-      int depth = 0;
-      for (unsigned w = 0; w <= threadIdx.x / 32; w++) depth += __popc(m[w] & below((int)(threadIdx.x - 32 * w)));
-      lds_depth[threadIdx.x] = depth;
-    }
-    __syncthreads();
-    for (unsigned t = threadIdx.x; t < tokens; t += kThreads) {
-      const uint32_t* m = (const uint32_t*)(p.a.mask + (b * drafts + token0 + t) * words);
-      const int depth = lds_depth[token0 + t];
-      lds_mask[t][0] = 0;
-      for (unsigned w = 0; w < 2 * words; w++) {
-        unsigned v = m[w] & below((int)drafts - (int)(32 * w));
-        if (p.a.window > 0 && p.a.window < p.a.drafts) {
-          unsigned left = v;
-          while (left) {
-            const int bit = __builtin_ctz(left), d = lds_depth[32 * w + bit];
-            left &= left - 1;
-            if (depth - d >= p.a.window && s.context + d >= p.a.first) v &= ~(1u << bit);
-          }
-        }
-        lds_mask[t][1 + w] = v;
-      }
-      lds_mask[t][1 + 2 * words] = 0;
-    }
-    __syncthreads();
+    const unsigned drafts = (unsigned)p.a.drafts;
+    if (threadIdx.x < 2) lds_far[threadIdx.x] = threadIdx.x ? 0x7FFFFFFF : 0;
+    load_masks(p, b, s, token0, tokens, lds_mask, lds_any, lds_depth, lds_far);
 
     // rows: scores are scaled by |scale| (its sign is in q), never by less than
     // what keeps a masked score at -inf
@@ -203,7 +256,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
       const unsigned token = live[n] ? r / p.group : token0, qh = head * p.group + (live[n] ? r - token * p.group : 0);
       mask_at[n] = token - token0;
       lo[n] = 0;
-      if (p.a.window > 0) lo[n] = (int)max((int64_t)0, s.context + lds_depth[token] - p.a.window + 1);
+      if (p.a.window > 0) lo[n] = window_start(p, s.context, lds_depth[token]);
       lo_most = live[n] ? max(lo_most, lo[n]) : lo_most;
 #pragma unroll
       for (int st = 0; st < kSteps; st++) {
@@ -287,14 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
           unsigned any = 0;
 #pragma unroll
           for (int n = 0; n < N; n++) {
-            // context tokens in the window or among the first, then the drafted ones
-            const int to = s.context - t0;
-            unsigned w = (below(to) & ~below(lo[n] - t0)) | below(seen_first - t0);
-            const int at = (-to) >> 5;  // drafted token -to is the tile's first
-            if (at >= -1 && at <= 2 * (int)words - 1) {
-              const unsigned* mk = &lds_mask[mask_at[n]][1 + at];
-              w |= (unsigned)((((uint64_t)mk[1] << 32) | mk[0]) >> ((unsigned)-to & 31u));
-            }
+            unsigned w = seen_word(s, t0, lo[n], seen_first, lds_mask[mask_at[n]], (int)p.a.words);
             w &= (on0 ? 0xFFFFu : 0u) | (on1 ? 0xFFFF0000u : 0u);
             seen[n] = live[n] ? w : 0u;
             any |= seen[n];
@@ -491,7 +537,427 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
       rg = 0;
       if (++head == p.c.heads) {
         head = 0;
-        s = tree_span(p, ++b);
+        s = tree_span<kTile>(p, ++b);
+      }
+    }
+    x = uniform(x), u_first = uniform(u_first), head = uniform(head), rg = uniform(rg), b = uniform((int)b);
+    __syncthreads();  // it writes the same LDS
+  }
+}
+
+// Many rows (65 and more of a cache head): the eight waves of a block take 32 rows
+// each, of one tile of 8192 / D tokens that they decode together, into LDS, as
+// bf16: K by token, V by element.  (Decoded by each wave, as above, a tile costs
+// more instructions than its products take.)  The 32x32x16 product S^T = K Q^T
+// leaves 16 of 32 tokens of one row in a lane, which are the B operand of O^T +=
+// V^T P^T for V's tokens in the order 0-3, 8-11, 4-7, 12-15 of each 16.
+//
+// A wave takes sets of 32 tokens in turn.  While it forms one set's probabilities,
+// the values of the set before are added and the scores of the next one formed, so
+// matrix and vector instructions do not wait for each other.  A row's reference
+// moves only where its maximum has risen by more than 2^8 above it: the old terms
+// are seldom scaled, and probabilities of up to 2^8 lose nothing.
+constexpr int kWideWaves = 8, kWideThreads = 64 * kWideWaves;
+template <int D>
+struct Wide {
+  static constexpr int kT = 8192 / D;        // tokens of a tile: each thread decodes 16 elements of K and of V
+  static constexpr int kKRow = 2 * D + 16;   // bytes of a token in LDS; the odd number of 16 spreads rows over the banks
+  static constexpr int kVRow = 2 * kT;       // bytes of an element's row
+  // 16-byte unit c of element d's row is at c ^ swizzle(d & 31): the 16 lanes that
+  // read neighbouring elements, and those that write every fourth, use all banks
+  static __device__ __forceinline__ int swizzle(int d) {
+    return D == 64 ? ((d >> 1) & 14) ^ (d & 1) ^ ((d & 2) << 2) : D == 128 ? ((d >> 1) ^ (d >> 3)) & 7 : (d >> 2) & 3;
+  }
+};
+struct WideFlags {
+  unsigned off;     // runs of 16 tokens that are not there
+  unsigned odd[4];  // tokens with a NaN or an infinity in V
+};
+
+template <int D, bool kFp4, int kTerms, int kRowWaves>
+__global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
+  typedef Wide<D> W;
+  constexpr int kT = W::kT, kRow = kFp4 ? D / 2 : D;
+  constexpr int kTokenWaves = kWideWaves / kRowWaves;
+  constexpr int kSets = kT / 32 / kTokenWaves;  // 32-token sets of a wave's tile
+  constexpr int kUnit = 32 * kRowWaves;         // rows
+  constexpr int kOut = D / 32;                  // 32-element sets of the output
+  // two tiles of K and of V; at the end, results of the waves that shared the rows' tiles
+  constexpr int kTiles = 2 * (kT * W::kKRow + D * W::kVRow), kLane = D / 2 + 4, kShared = kRowWaves * (kTokenWaves - 1) * 64 * kLane * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kTiles > kShared ? kTiles : kShared];
+  uint8_t(*lds_k)[kT * W::kKRow] = (uint8_t(*)[kT * W::kKRow])lds;
+  uint8_t(*lds_v)[D * W::kVRow] = (uint8_t(*)[D * W::kVRow])(lds + 2 * kT * W::kKRow);
+  __shared__ unsigned lds_mask[kUnit][kMaskRow], lds_any[kMaskRow];
+  __shared__ int lds_depth[256], lds_far[2];
+  __shared__ WideFlags flags[4];
+  __shared__ unsigned lds_sum[kWideWaves];
+  __shared__ int lds_at[3];
+
+  const int lane = threadIdx.x & 63, i = lane & 31, g = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row_wave = wave / kTokenWaves, token_wave = wave % kTokenWaves;
+  unsigned x, end, u_first, head, rg, per = 0;
+  int64_t b;
+  TreeSpan s;
+  if (!p.split) {
+    unsigned id = blockIdx.x;
+    rg = id % p.row_groups;
+    id /= p.row_groups;
+    head = id % p.c.heads;
+    b = id / p.c.heads;
+    s = tree_span<kT>(p, b);
+    x = u_first = 0;
+    end = s.n;
+  } else {
+    const RangeStart r = range_start<kT>(p, 1, lds_sum, lds_at);
+    if (r.x >= r.end) return;
+    x = r.x, end = r.end, u_first = r.u_first, head = r.head, rg = r.rg, per = r.per, b = r.b;
+    s = tree_span<kT>(p, b);
+  }
+
+  // What this thread decodes: of K, elements 16 kb .. of token kt; of V, elements
+  // 4 vd .. of tokens vt .. vt + 3.  A wave's tokens, from wt on, are in one run of
+  // 16 and so in one page: addresses are scalars and constant lane offsets.
+  const int kt = threadIdx.x / (D / 16), kb = threadIdx.x % (D / 16);
+  const int vt = 4 * (threadIdx.x / (D / 4)), vd = threadIdx.x % (D / 4);
+  const int wt = wave * (kT / kWideWaves);
+  const unsigned shift = p.c.page_shift, pmask = (1u << shift) - 1;
+  const int k_off = (kt - wt) * kRow + kb * (kFp4 ? 8 : 16), ks_off = (kt - wt) * (D / 32) + kb / 2;
+  const int v_off = (vt - wt) * kRow + vd * (kFp4 ? 2 : 4), vs_off = ((vd / 8) << shift) + vt - wt;
+
+  while (true) {
+    const int first = (int)(x - u_first), last = min(s.n, (int)(end - u_first));
+    const unsigned row0 = rg * kUnit, token0 = row0 / p.group;
+    const unsigned drafts = (unsigned)p.a.drafts;
+    if (threadIdx.x < 4) flags[threadIdx.x] = {};
+    if (threadIdx.x < 2) lds_far[threadIdx.x] = threadIdx.x ? 0x7FFFFFFF : 0;
+    load_masks(p, b, s, token0, (min(row0 + kUnit, p.rows) - 1) / p.group - token0 + 1, lds_mask, lds_any, lds_depth, lds_far);
+
+    // the row of this lane
+    const unsigned r = row0 + row_wave * 32 + i;
+    const bool live = r < p.rows;
+    const unsigned token = live ? r / p.group : token0, qh = head * p.group + (live ? r - token * p.group : 0);
+    const float to_log2 = fmaxf(fabsf(p.a.scale) * kLog2e, 0x1p-100f);
+    const unsigned q_sign = p.a.scale < 0 ? 0x80008000u : 0u;
+    bf16x8 qf[D / 16];
+#pragma unroll
+    for (int st = 0; st < D / 16; st++) {
+      u32x4 w = {0, 0, 0, 0};
+      if (live) w = *(const u32x4*)(p.a.q + (b * drafts + token) * p.a.q_stride + (int64_t)qh * D + 16 * st + 8 * g);
+      qf[st] = __builtin_bit_cast(bf16x8, w ^ q_sign);
+    }
+    // context tokens inside the windows of all rows, and of some row
+    int lo_most = 0, lo_least = 0, seen_first = 0;
+    if (p.a.window > 0) {
+      lo_most = uniform(window_start(p, s.context, lds_far[0]));
+      lo_least = uniform(window_start(p, s.context, lds_far[1]));
+      seen_first = (int)min(p.a.first, (int64_t)s.context);
+    }
+
+    auto token_of = [&](int k) { return (k < s.a ? k : k - s.a + s.b) * kT; };
+    // all rows see the whole tile (where its pages are there)
+    auto whole = [&](int t0) { return t0 + kT <= s.context && (t0 >= lo_most || t0 + kT <= seen_first); };
+    // what this lane's row sees of 32 tokens
+    auto my_word = [&](int t0) {
+      const int lo = p.a.window > 0 ? window_start(p, s.context, lds_depth[token]) : 0;
+      return live ? seen_word(s, t0, lo, seen_first, lds_mask[token - token0], (int)p.a.words) : 0u;
+    };
+    const __attribute__((address_space(4))) int32_t* ids =
+        (const __attribute__((address_space(4))) int32_t*)(p.a.table + b * p.a.table_stride);
+    // the page of this wave's tokens in the tile to load next
+    int id = -1;
+    auto fetch_id = [&](int k) { id = uniform(ids[(unsigned)min(token_of(min(k, last - 1)) + wt, s.end - 1) >> shift]); };
+    // a tile's codes, as loaded (zeros where there is no page)
+    u32x4 raw_k;
+    unsigned raw_v[4], raw_ks, raw_vs;
+    bool on = false;
+    auto fetch = [&](int k) {
+      const int t = token_of(k) + wt;
+      on = k < last && t < s.end && id >= 0 && id < p.c.pages;
+      const int64_t page = (int64_t)(on ? id : 0) * p.c.heads + head, row = (page << shift) + (t & pmask);
+      const __amdgpu_buffer_rsrc_t rk = panel_rsrc(p.a.kq + row * kRow, on ? 16 * kRow : 0);
+      if constexpr (kFp4) {
+        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(rk, k_off, 0, 0);
+        raw_k.x = w.x, raw_k.y = w.y;
+      } else {
+        raw_k = __builtin_amdgcn_raw_buffer_load_b128(rk, k_off, 0, 0);
+      }
+      raw_ks = __builtin_amdgcn_raw_buffer_load_b8(panel_rsrc(p.a.ks + row * (D / 32), on ? 16 * (D / 32) : 0), ks_off, 0, 0);
+      const __amdgpu_buffer_rsrc_t rv = panel_rsrc(p.a.vq + row * kRow, on ? 16 * kRow : 0);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        if constexpr (kFp4) raw_v[e] = __builtin_amdgcn_raw_buffer_load_b16(rv, v_off + e * kRow, 0, 0);
+        else raw_v[e] = __builtin_amdgcn_raw_buffer_load_b32(rv, v_off + e * kRow, 0, 0);
+      }
+      const __amdgpu_buffer_rsrc_t rs =
+          panel_rsrc(p.a.vs + page * (D / 32 << shift) + (t & pmask), on ? ((D / 32 - 1) << shift) + 16 : 0);
+      raw_vs = __builtin_amdgcn_raw_buffer_load_b32(rs, vs_off, 0, 0);
+    };
+    // the loaded tile k, decoded: K and the values' bf16, and (after what may come
+    // between) V
+    unsigned dv[4][2];
+    auto decode = [&](int k) {
+      uint8_t* kl = lds_k[(k - first) & 1] + kt * W::kKRow + kb * 32;
+      const float scale = e8m0_as_scale(raw_ks);
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        u32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const unsigned w[1] = {kFp4 ? raw_k[q] : raw_k[2 * q + e / 2]};
+          o[e] = decode2<kFp4>(w, kFp4 ? e : e & 1, scale);
+        }
+        *(u32x4*)(kl + q * 16) = o;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const float vscale = e8m0_as_scale((raw_vs >> (8 * e)) & 0xFFu);
+        dv[e][0] = decode2<kFp4>(&raw_v[e], 0, vscale);
+        dv[e][1] = decode2<kFp4>(&raw_v[e], 1, vscale);
+      }
+    };
+    auto store_v = [&](int k) {
+      const int t0 = token_of(k);
+      if (!whole(t0) || !on) {
+        WideFlags& fl = flags[(k - first) & 3];
+        // (a run's first tokens say it: what lies past the sequence's end is masked anyway)
+        if (!on && wt % 16 == 0 && lane == 0) atomicOr(&fl.off, 1u << (wt / 16));
+        // A token that no row sees: its V bytes are whatever the page holds, so it
+        // counts as 0.  A NaN (or an infinity) of a token that some rows see must
+        // not reach the others as NaN times 0: it is set to 0, and noted.
+        const unsigned any =
+            on ? seen_word(s, t0 + (vt & ~31), lo_least, seen_first, lds_any, (int)p.a.words) >> (vt & 31) : 0;
+        unsigned odd = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            unsigned w = (any >> e) & 1 ? dv[e][h] : 0;
+            if ((w & 0x7F80u) == 0x7F80u) odd |= 1u << e, w &= 0xFFFF0000u;
+            if ((w & 0x7F800000u) == 0x7F800000u) odd |= 1u << e, w &= 0xFFFFu;
+            dv[e][h] = w;
+          }
+        if (odd) atomicOr(&fl.odd[vt / 32], odd << (vt & 31));
+      }
+      uint8_t* vl = lds_v[(k - first) & 1];
+      const int c = 2 * (vt / 16) + ((vt / 4) & 1), half = (vt / 8) & 1;
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int o = 0; o < 2; o++) {
+          const unsigned sel = o ? 0x07060302u : 0x05040100u;
+          const u32x2 w = {perm(dv[1][h], dv[0][h], sel), perm(dv[3][h], dv[2][h], sel)};
+          const int el = 4 * vd + 2 * h + o;
+          *(u32x2*)(vl + el * W::kVRow + (c ^ W::swizzle(el & 31)) * 16 + 8 * half) = w;
+        }
+    };
+
+    float ref = -INFINITY, l = 0;  // in log2 units, and of this lane's tokens
+    f32x16 acc[kOut], sc;
+    u32x4 pt[2][kTerms];
+#pragma unroll
+    for (int o = 0; o < kOut; o++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) acc[o][e] = 0;
+
+    // S^T of set n of the tile in kl; element e: token 32 n + 8 (e / 4) + 4 g + e % 4
+    auto scores = [&](const uint8_t* kl, int n) {
+      const uint8_t* at = kl + ((token_wave * kSets + n) * 32 + i) * W::kKRow + 16 * g;
+      f32x16 o;
+#pragma unroll
+      for (int e = 0; e < 16; e++) o[e] = 0;
+#pragma unroll
+      for (int st = 0; st < D / 16; st++)
+        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf16x8*)(at + 32 * st), qf[st], o, 0, 0, 0);
+      return o;
+    };
+    // the masks of set n of tile k, which not all rows see whole
+    auto mask_scores = [&](int k, int n, unsigned off) {
+      const int set = token_wave * kSets + n;
+      const unsigned o2 = off >> (2 * set);
+      const unsigned seen = my_word(token_of(k) + 32 * set) & ((o2 & 1 ? 0 : 0xFFFFu) | (o2 & 2 ? 0 : 0xFFFF0000u));
+#pragma unroll
+      for (int e = 0; e < 16; e++) sc[e] = (seen >> (8 * (e / 4) + 4 * g + e % 4)) & 1 ? sc[e] : -INFINITY;
+    };
+    // O^T += V^T P^T of half h of set n of the tile in vl
+    auto values = [&](const uint8_t* vl, int n, int h) {
+#pragma unroll
+      for (int o = 0; o < kOut; o++) {
+        const int c = 4 * (token_wave * kSets + n) + 2 * h;
+        const bf16x8 v = *(const bf16x8*)(vl + ((i * W::kVRow + (g ^ W::swizzle(i)) * 16) ^ (16 * c)) + 32 * o * W::kVRow);
+#pragma unroll
+        for (int t = 0; t < kTerms; t++)
+          acc[o] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, __builtin_bit_cast(bf16x8, pt[h][t]), acc[o], 0, 0, 0);
+      }
+    };
+    // The probabilities of the set in sc.  Returns what moves the old terms.
+    auto weights = [&]() {
+      float top = sc[0];
+#pragma unroll
+      for (int e = 1; e < 16; e++) top = fmaxf(top, sc[e]);
+      const float high = max_halves(top) * to_log2;
+      const bool rises = high > ref + 8;
+      // (the old terms are moved by the difference of the two references: exactly)
+      const float moved = rises ? high : ref, alpha = rises ? __builtin_amdgcn_exp2f(ref - high) : 1.0f;
+      const float base = moved > -INFINITY ? moved : 0.0f;  // nothing seen yet: every p is 0
+      ref = moved;
+      l *= alpha;
+      // P in bf16 terms: each takes the upper half of what the ones before it left
+      // (truncated; the last one rounded)
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[e], to_log2, -base));
+        float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[e + 1], to_log2, -base));
+        l += p0 + p1;
+#pragma unroll
+        for (int t = 0; t < kTerms; t++) {
+          if (t + 1 == kTerms) {
+            pt[e / 8][t][(e / 2) & 3] = __builtin_bit_cast(unsigned, (bf16x2){(__bf16)p0, (__bf16)p1});
+          } else {
+            const unsigned w0 = __float_as_uint(p0), w1 = __float_as_uint(p1);
+            pt[e / 8][t][(e / 2) & 3] = perm(w1, w0, 0x07060302u);
+            p0 -= __uint_as_float(w0 & 0xFFFF0000u);  // exact
+            p1 -= __uint_as_float(w1 & 0xFFFF0000u);
+          }
+        }
+      }
+      return alpha;
+    };
+    // V elements of tile k that are no numbers, for the rows that see them
+    auto odd_values = [&](int k) {
+      const int t0 = token_of(k);
+      if (whole(t0)) return;
+#pragma unroll 1
+      for (int n = 0; n < kSets; n++) {
+        const int set = token_wave * kSets + n;
+        unsigned odd = uniform((int)flags[(k - first) & 3].odd[set]);
+        const unsigned seen = odd ? my_word(t0 + 32 * set) : 0;
+        while (odd) {
+          const int bit = __builtin_ctz(odd), t = t0 + 32 * set + bit;
+          odd &= odd - 1;
+          const int64_t page = (int64_t)ids[(unsigned)t >> shift] * p.c.heads + head, row = (page << shift) + (t & pmask);
+          const bool mine = (seen >> bit) & 1;
+#pragma unroll
+          for (int o = 0; o < kOut; o++) {
+            const float scale = e8m0_as_scale(p.a.vs[((page * (D / 32) + o) << shift) + (t & pmask)]);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+              const int el = 32 * o + 8 * q + 4 * g;
+              const uint8_t* src = p.a.vq + row * kRow + (kFp4 ? el / 2 : el);
+              const unsigned w[1] = {kFp4 ? *(const uint16_t*)src : *(const unsigned*)src};
+              const unsigned d0 = decode2<kFp4>(w, 0, scale), d1 = decode2<kFp4>(w, 1, scale);
+              const float nan = __builtin_nanf("");
+              if (mine && (d0 & 0x7F80u) == 0x7F80u) acc[o][4 * q] = nan;
+              if (mine && (d0 & 0x7F800000u) == 0x7F800000u) acc[o][4 * q + 1] = nan;
+              if (mine && (d1 & 0x7F80u) == 0x7F80u) acc[o][4 * q + 2] = nan;
+              if (mine && (d1 & 0x7F800000u) == 0x7F800000u) acc[o][4 * q + 3] = nan;
+            }
+          }
+        }
+      }
+    };
+
+    // Tile k's K and V are at k & 1, its flags at k & 3.  It is loaded two turns and
+    // decoded one turn before its own.
+    fetch_id(first);
+    fetch(first);
+    fetch_id(first + 1);
+    decode(first);
+    store_v(first);
+    fetch(first + 1);
+    fetch_id(first + 2);
+    __syncthreads();
+    for (int k = first; k < last; k++) {
+      const uint8_t *kl = lds_k[(k - first) & 1], *vl = lds_v[(k - first) & 1];
+      const unsigned off = uniform((int)flags[(k - first) & 3].off);
+      const bool masked = !whole(token_of(k)) || off != 0;
+#pragma unroll
+      for (int n = 0; n < kSets; n++) {
+        sc = scores(kl, n);
+        if (masked) mask_scores(k, n, off);
+        const float alpha = weights();
+        if (__builtin_amdgcn_ballot_w64(alpha != 1.0f) != 0) {
+          asm volatile("");  // a branch: the products without it would be in every turn
+#pragma unroll
+          for (int o = 0; o < kOut; o++) acc[o] *= alpha;
+        }
+        values(vl, n, 0);
+        values(vl, n, 1);
+      }
+      if (k + 1 < last) {
+        decode(k + 1);
+        store_v(k + 1);
+      }
+      fetch(k + 2);
+      fetch_id(k + 3);
+      odd_values(k);
+      if (threadIdx.x == 0) flags[(k - first + 2) & 3] = {};
+      __syncthreads();
+    }
+
+    const bool opens = first == 0, closes = last == s.n;  // of the unit
+    if (p.split && opens && threadIdx.x == 0 && !(p.by_block && closes)) {
+      const unsigned unit = ((unsigned)b * p.c.heads + head) * p.row_groups + rg;
+      int* w = p.parts + 4 * (p.by_block ? blockIdx.x : unit);
+      w[0] = (int)((u_first + (unsigned)s.n - 1) / per - blockIdx.x) + 1;
+      w[1] = (int)blockIdx.x, w[2] = (int)unit;
+    }
+    float sum = sum_halves(l), mx = ref;
+    if constexpr (kTokenWaves > 1) {
+      static_assert(kTokenWaves == 2);
+      float* part = (float*)lds + (row_wave * 64 + lane) * kLane;
+      __syncthreads();
+      if (token_wave != 0) {
+#pragma unroll
+        for (int o = 0; o < kOut; o++)
+#pragma unroll
+          for (int q = 0; q < 4; q++)
+            *(f32x4*)(part + 4 + 16 * o + 4 * q) = (f32x4){acc[o][4 * q], acc[o][4 * q + 1], acc[o][4 * q + 2], acc[o][4 * q + 3]};
+        part[0] = mx, part[1] = sum;
+      }
+      __syncthreads();
+      if (token_wave == 0) {
+        const float om = part[0], to = fmaxf(mx, om), base = to > -INFINITY ? to : 0.0f;
+        const float f = __builtin_amdgcn_exp2f(mx - base), of = __builtin_amdgcn_exp2f(om - base);
+        sum = sum * f + part[1] * of;
+        mx = to;
+#pragma unroll
+        for (int o = 0; o < kOut; o++)
+#pragma unroll
+          for (int e = 0; e < 16; e++) acc[o][e] = acc[o][e] * f + part[4 + 16 * o + e] * of;
+      }
+    }
+    if (token_wave == 0 && live) {
+      const int64_t hq = qh;
+      // a block has at most one part of a unit that a block before it opened (slot
+      // 0) and one of a unit that it opens itself (slot 1)
+      const int64_t slot = (2 * (int64_t)blockIdx.x + (opens ? 1 : 0)) * kUnit + row_wave * 32 + i;
+#pragma unroll
+      for (int o = 0; o < kOut; o++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const int el = 32 * o + 8 * q + 4 * g;
+          const f32x4 v = {acc[o][4 * q], acc[o][4 * q + 1], acc[o][4 * q + 2], acc[o][4 * q + 3]};
+          if (!p.split || (opens && closes))
+            store_out(p.a, ((b * drafts + token) * p.a.q_heads + hq) * D + el, finish(p.a, hq, mx, sum, v));
+          else
+            *(f32x4*)(p.part_o + slot * D + el) = v;
+        }
+      if (p.split && !(opens && closes) && g == 0) {
+        p.part_ml[2 * slot] = mx;
+        p.part_ml[2 * slot + 1] = sum;
+      }
+    }
+    // the next unit: the next row group, cache head or sequence
+    if (!p.split) break;
+    x = u_first + (unsigned)last;
+    if (x >= end) break;
+    u_first = x;
+    if (++rg == p.row_groups) {
+      rg = 0;
+      if (++head == p.c.heads) {
+        head = 0;
+        s = tree_span<kT>(p, ++b);
       }
     }
     x = uniform(x), u_first = uniform(u_first), head = uniform(head), rg = uniform(rg), b = uniform((int)b);
@@ -572,51 +1038,58 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p, unsigned unit_r
 
 }  // namespace
 
-// Shape of a call's units: N sets of 16 rows a wave, 2^row_shift waves with rows
-// of their own.
+// Shape of a call's units.  Up to 64 rows of a cache head, k_tree_attend: N sets
+// of 16 rows a wave, of one or two row waves.  More, k_tree_wide.
 struct TreeUnits {
-  int sets;
+  bool wide;
+  int sets, tile;
   unsigned row_shift, rows, row_groups;  // rows of a unit; units per sequence and cache head
 };
 static TreeUnits tree_units(int64_t drafts, unsigned q_heads, const KvShape& c) {
   const int64_t rows = (int64_t)(q_heads / c.heads) * drafts;
-  const int sets = rows <= kSet ? 1 : 256 / (int)c.dim;
-  const int64_t waves = (rows + sets * kSet - 1) / (sets * kSet);
-  const unsigned shift = waves >= 3 ? 2 : waves - 1;
-  const unsigned unit = (unsigned)(sets * kSet) << shift;
-  return {sets, shift, unit, (unsigned)((rows + unit - 1) / unit)};
+  TreeUnits u;
+  u.wide = rows > 64;
+  u.sets = rows > kSet && c.dim <= 128 ? 2 : 1;
+  u.row_shift = !u.wide && rows > u.sets * kSet ? 1 : 0;
+  u.tile = u.wide ? 8192 / (int)c.dim : kTile;
+  u.rows = u.wide ? (rows > 128 || c.dim == 256 ? 256 : 128) : (u.sets * kSet) << u.row_shift;
+  u.row_groups = (unsigned)((rows + u.rows - 1) / u.rows);
+  return u;
 }
 
 // Tiles of the longest sequence that the table can name.
-static int64_t tree_tiles(int64_t drafts, const KvShape& c, int64_t table_width, int64_t window, int64_t first) {
-  int64_t most = std::min<int64_t>(table_width << c.page_shift, kMaxLen);
-  int64_t tiles = (most + kTile - 1) / kTile;
+static int64_t tree_tiles(const TreeUnits& u, int64_t drafts, const KvShape& c, int64_t table_width, int64_t window,
+                          int64_t first) {
+  const int64_t most = std::min<int64_t>(table_width << c.page_shift, kMaxLen);
+  int64_t tiles = (most + u.tile - 1) / u.tile;
   if (window > 0 && window < most && first < most)
-    tiles = std::min(tiles, (first + kTile - 1) / kTile + (window + drafts) / kTile + 2);
+    tiles = std::min(tiles, (first + u.tile - 1) / u.tile + (window + drafts) / u.tile + 2);
   return tiles;
 }
 
 // Whether blocks take ranges of the flattened tiles (and a second launch joins
 // the parts), or a unit each.
-static bool tree_ranges(int64_t units, int64_t tiles) { return tiles > (units >= 128 ? 64 : 32); }
+static bool tree_ranges(const TreeUnits& u, int64_t units, int64_t tiles) {
+  return tiles * u.tile > (units >= 128 ? 2048 : 1024);
+}
 
-constexpr int64_t kRangeBlocks = 512;
+constexpr int64_t kRangeBlocks = 512, kWideBlocks = 256;  // two and one a CU
 
 int64_t tree_attend_blocks(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
                            int64_t window, int64_t first) {
   const TreeUnits u = tree_units(drafts, q_heads, c);
-  const int64_t units = batch * c.heads * u.row_groups, tiles = tree_tiles(drafts, c, table_width, window, first);
+  const int64_t units = batch * c.heads * u.row_groups, tiles = tree_tiles(u, drafts, c, table_width, window, first);
   // flattened tile indexes are 32 bits, with room for one range more
   if (units > (0x7FFFFFFF - 4096) / tiles) return -1;
-  if (!tree_ranges(units, tiles)) return units;
-  const int64_t waves = kWaves >> u.row_shift;
-  return std::min<int64_t>(kRangeBlocks, units * ((tiles + waves - 1) / waves));
+  if (!tree_ranges(u, units, tiles)) return units;
+  const int64_t waves = u.wide ? 1 : kWaves >> u.row_shift;
+  return std::min<int64_t>(u.wide ? kWideBlocks : kRangeBlocks, units * ((tiles + waves - 1) / waves));
 }
 
 int64_t tree_attend_workspace(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
                               int64_t window, int64_t first) {
   const TreeUnits u = tree_units(drafts, q_heads, c);
-  if (!tree_ranges(batch * c.heads * u.row_groups, tree_tiles(drafts, c, table_width, window, first))) return 0;
+  if (!tree_ranges(u, batch * c.heads * u.row_groups, tree_tiles(u, drafts, c, table_width, window, first))) return 0;
   const int64_t blocks = tree_attend_blocks(batch, drafts, q_heads, c, table_width, window, first);
   return blocks * (16 + 2 * (int64_t)u.rows * (c.dim + 2) * 4);
 }
@@ -642,7 +1115,8 @@ hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, voi
   p.row_shift = u.row_shift;
   const int64_t units = a.batch * c.heads * u.row_groups;
   const int64_t blocks = tree_attend_blocks(a.batch, a.drafts, a.q_heads, c, a.table_width, a.window, a.first);
-  const bool ranges = tree_ranges(units, tree_tiles(a.drafts, c, a.table_width, a.window, a.first));
+  const bool ranges = tree_ranges(u, units, tree_tiles(u, a.drafts, c, a.table_width, a.window, a.first));
+  p.split = ranges;
   p.by_block = units >= blocks / 2;
   p.parts = (int*)workspace;  // at most a record a block, in either case
   p.part_o = (float*)((uint8_t*)workspace + blocks * 16);
@@ -650,20 +1124,39 @@ hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, voi
   const dim3 grid((unsigned)blocks), block(kThreads);
 #define MXQ_TREE_R(D, F, T, N) \
   ranges ? k_tree_attend<D, F, T, N, true><<<grid, block, 0, st>>>(p) : k_tree_attend<D, F, T, N, false><<<grid, block, 0, st>>>(p)
-#define MXQ_TREE_N(D, N)                                                      \
-  do {                                                                        \
-    if (a.bf16_out && fp4) MXQ_TREE_R(D, true, 2, N);                         \
-    else if (a.bf16_out) MXQ_TREE_R(D, false, 2, N);                          \
-    else if (fp4) MXQ_TREE_R(D, true, 3, N);                                  \
-    else MXQ_TREE_R(D, false, 3, N);                                          \
-    if (ranges) launch_join<D>(p, u.rows, p.by_block ? blocks : units, st);   \
+#define MXQ_TREE_W(D, F, T, N) k_tree_wide<D, F, T, N><<<grid, dim3(kWideThreads), 0, st>>>(p)
+#define MXQ_TREE_N(K, D, N)                          \
+  do {                                               \
+    if (a.bf16_out && fp4) K(D, true, 2, N);         \
+    else if (a.bf16_out) K(D, false, 2, N);          \
+    else if (fp4) K(D, true, 3, N);                  \
+    else K(D, false, 3, N);                          \
   } while (0)
-  if (c.dim == 64 && u.sets == 1) MXQ_TREE_N(64, 1);
-  else if (c.dim == 64) MXQ_TREE_N(64, 4);
-  else if (c.dim == 128 && u.sets == 1) MXQ_TREE_N(128, 1);
-  else if (c.dim == 128) MXQ_TREE_N(128, 2);
-  else MXQ_TREE_N(256, 1);
+  if (u.wide) {
+    if (c.dim == 64 && u.rows == 128) MXQ_TREE_N(MXQ_TREE_W, 64, 4);
+    else if (c.dim == 64) MXQ_TREE_N(MXQ_TREE_W, 64, 8);
+    else if (c.dim == 128 && u.rows == 128) MXQ_TREE_N(MXQ_TREE_W, 128, 4);
+    else if (c.dim == 128) MXQ_TREE_N(MXQ_TREE_W, 128, 8);
+    else MXQ_TREE_N(MXQ_TREE_W, 256, 8);
+  } else if (c.dim == 64 && u.sets == 1) {
+    MXQ_TREE_N(MXQ_TREE_R, 64, 1);
+  } else if (c.dim == 64) {
+    MXQ_TREE_N(MXQ_TREE_R, 64, 2);
+  } else if (c.dim == 128 && u.sets == 1) {
+    MXQ_TREE_N(MXQ_TREE_R, 128, 1);
+  } else if (c.dim == 128) {
+    MXQ_TREE_N(MXQ_TREE_R, 128, 2);
+  } else {
+    MXQ_TREE_N(MXQ_TREE_R, 256, 1);
+  }
+  if (ranges) {
+    const int64_t records = p.by_block ? blocks : units;
+    if (c.dim == 64) launch_join<64>(p, u.rows, records, st);
+    else if (c.dim == 128) launch_join<128>(p, u.rows, records, st);
+    else launch_join<256>(p, u.rows, records, st);
+  }
 #undef MXQ_TREE_N
+#undef MXQ_TREE_W
 #undef MXQ_TREE_R
   return hipGetLastError();
 }
