@@ -212,17 +212,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
   TreeSpan s;
   if constexpr (!kRanges) {
     unsigned id = blockIdx.x;
-    rg = id % p.row_groups;
+    rg = uniform(id % p.row_groups);
     id /= p.row_groups;
-    head = id % p.c.heads;
-    b = id / p.c.heads;
+    head = uniform(id % p.c.heads);
+    b = uniform(id / p.c.heads);
     s = tree_span<kTile>(p, b);
     x = u_first = 0;
     end = s.n;
   } else {
     const RangeStart r = range_start<kTile>(p, per_tile, lds_sum, lds_at);
     if (r.x >= r.end) return;
-    x = r.x, end = r.end, u_first = r.u_first, head = r.head, rg = r.rg, per = r.per, b = r.b;
+    x = uniform(r.x), end = uniform(r.end), u_first = uniform(r.u_first), head = uniform(r.head), rg = uniform(r.rg), per = uniform(r.per), b = r.b;
     s = tree_span<kTile>(p, b);
   }
 
@@ -545,28 +545,24 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
   }
 }
 
-// Many rows (65 and more of a cache head): the eight waves of a block take 32 rows
-// each, of one tile of 8192 / D tokens that they decode together, into LDS, as
+// Many rows (65 and more of a cache head): the kW waves of a block take 32 rows
+// each, of one tile of kW * 1024 / D tokens that they decode together, into LDS, as
 // bf16: K by token, V by element.  (Decoded by each wave, as above, a tile costs
 // more instructions than its products take.)  The 32x32x16 product S^T = K Q^T
 // leaves 16 of 32 tokens of one row in a lane, which are the B operand of O^T +=
 // V^T P^T for V's tokens in the order 0-3, 8-11, 4-7, 12-15 of each 16.
 //
-// A wave takes sets of 32 tokens in turn.  While it forms one set's probabilities,
-// the values of the set before are added and the scores of the next one formed, so
-// matrix and vector instructions do not wait for each other.  A row's reference
-// moves only where its maximum has risen by more than 2^8 above it: the old terms
-// are seldom scaled, and probabilities of up to 2^8 lose nothing.
-constexpr int kWideWaves = 8, kWideThreads = 64 * kWideWaves;
-template <int D>
+// A row's reference moves only where its maximum has risen by more than 2^8 above
+// it: the old terms are seldom scaled, and probabilities of up to 2^8 lose nothing.
+template <int D, int kW>
 struct Wide {
-  static constexpr int kT = 8192 / D;        // tokens of a tile: each thread decodes 16 elements of K and of V
+  static constexpr int kT = kW * 1024 / D;   // tokens of a tile: each thread decodes 16 elements of K and of V
   static constexpr int kKRow = 2 * D + 16;   // bytes of a token in LDS; the odd number of 16 spreads rows over the banks
   static constexpr int kVRow = 2 * kT;       // bytes of an element's row
   // 16-byte unit c of element d's row is at c ^ swizzle(d & 31): the 16 lanes that
   // read neighbouring elements, and those that write every fourth, use all banks
   static __device__ __forceinline__ int swizzle(int d) {
-    return D == 64 ? ((d >> 1) & 14) ^ (d & 1) ^ ((d & 2) << 2) : D == 128 ? ((d >> 1) ^ (d >> 3)) & 7 : (d >> 2) & 3;
+    return kT == 128 ? ((d >> 1) & 14) ^ (d & 1) ^ ((d & 2) << 2) : kT == 64 ? ((d >> 1) ^ (d >> 3)) & 7 : (d >> 2) & 3;
   }
 };
 struct WideFlags {
@@ -574,45 +570,39 @@ struct WideFlags {
   unsigned odd[4];  // tokens with a NaN or an infinity in V
 };
 
-template <int D, bool kFp4, int kTerms, int kRowWaves>
-__global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
-  typedef Wide<D> W;
+template <int D, bool kFp4, int kTerms, int kW>
+__global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
+  typedef Wide<D, kW> W;
   constexpr int kT = W::kT, kRow = kFp4 ? D / 2 : D;
-  constexpr int kTokenWaves = kWideWaves / kRowWaves;
-  constexpr int kSets = kT / 32 / kTokenWaves;  // 32-token sets of a wave's tile
-  constexpr int kUnit = 32 * kRowWaves;         // rows
-  constexpr int kOut = D / 32;                  // 32-element sets of the output
-  // two tiles of K and of V; at the end, results of the waves that shared the rows' tiles
-  constexpr int kTiles = 2 * (kT * W::kKRow + D * W::kVRow), kLane = D / 2 + 4, kShared = kRowWaves * (kTokenWaves - 1) * 64 * kLane * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kTiles > kShared ? kTiles : kShared];
-  uint8_t(*lds_k)[kT * W::kKRow] = (uint8_t(*)[kT * W::kKRow])lds;
-  uint8_t(*lds_v)[D * W::kVRow] = (uint8_t(*)[D * W::kVRow])(lds + 2 * kT * W::kKRow);
+  constexpr int kSets = kT / 32;  // 32-token sets of a tile
+  constexpr int kUnit = 32 * kW;  // rows
+  constexpr int kOut = D / 32;    // 32-element sets of the output
+  __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][kT * W::kKRow], lds_v[2][D * W::kVRow];
   __shared__ unsigned lds_mask[kUnit][kMaskRow], lds_any[kMaskRow];
   __shared__ int lds_depth[256], lds_far[2];
   __shared__ WideFlags flags[4];
-  __shared__ unsigned lds_sum[kWideWaves];
+  __shared__ unsigned lds_sum[kW];
   __shared__ int lds_at[3];
 
   const int lane = threadIdx.x & 63, i = lane & 31, g = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row_wave = wave / kTokenWaves, token_wave = wave % kTokenWaves;
   unsigned x, end, u_first, head, rg, per = 0;
   int64_t b;
-  TreeSpan s;
+  TreeSpan span;
   if (!p.split) {
     unsigned id = blockIdx.x;
-    rg = id % p.row_groups;
+    rg = uniform(id % p.row_groups);
     id /= p.row_groups;
-    head = id % p.c.heads;
-    b = id / p.c.heads;
-    s = tree_span<kT>(p, b);
+    head = uniform(id % p.c.heads);
+    b = uniform(id / p.c.heads);
+    span = tree_span<kT>(p, b);
     x = u_first = 0;
-    end = s.n;
+    end = span.n;
   } else {
     const RangeStart r = range_start<kT>(p, 1, lds_sum, lds_at);
     if (r.x >= r.end) return;
-    x = r.x, end = r.end, u_first = r.u_first, head = r.head, rg = r.rg, per = r.per, b = r.b;
-    s = tree_span<kT>(p, b);
+    x = uniform(r.x), end = uniform(r.end), u_first = uniform(r.u_first), head = uniform(r.head), rg = uniform(r.rg), per = uniform(r.per), b = r.b;
+    span = tree_span<kT>(p, b);
   }
 
   // What this thread decodes: of K, elements 16 kb .. of token kt; of V, elements
@@ -620,13 +610,16 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
   // 16 and so in one page: addresses are scalars and constant lane offsets.
   const int kt = threadIdx.x / (D / 16), kb = threadIdx.x % (D / 16);
   const int vt = 4 * (threadIdx.x / (D / 4)), vd = threadIdx.x % (D / 4);
-  const int wt = wave * (kT / kWideWaves);
+  const int wt = wave * (kT / kW);
   const unsigned shift = p.c.page_shift, pmask = (1u << shift) - 1;
   const int k_off = (kt - wt) * kRow + kb * (kFp4 ? 8 : 16), ks_off = (kt - wt) * (D / 32) + kb / 2;
   const int v_off = (vt - wt) * kRow + vd * (kFp4 ? 2 : 4), vs_off = ((vd / 8) << shift) + vt - wt;
 
   while (true) {
-    const int first = (int)(x - u_first), last = min(s.n, (int)(end - u_first));
+    // (the loop's variables are in vector registers, where divisions leave them)
+    x = uniform(x), u_first = uniform(u_first), head = uniform(head), rg = uniform(rg), b = uniform((int)b);
+    const TreeSpan s = {uniform(span.context), uniform(span.end), uniform(span.a), uniform(span.b), uniform(span.n)};
+    const int first = uniform(x - u_first), last = uniform(min(s.n, (int)(end - u_first)));
     const unsigned row0 = rg * kUnit, token0 = row0 / p.group;
     const unsigned drafts = (unsigned)p.a.drafts;
     if (threadIdx.x < 4) flags[threadIdx.x] = {};
@@ -634,7 +627,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
     load_masks(p, b, s, token0, (min(row0 + kUnit, p.rows) - 1) / p.group - token0 + 1, lds_mask, lds_any, lds_depth, lds_far);
 
     // the row of this lane
-    const unsigned r = row0 + row_wave * 32 + i;
+    const unsigned r = row0 + wave * 32 + i;
     const bool live = r < p.rows;
     const unsigned token = live ? r / p.group : token0, qh = head * p.group + (live ? r - token * p.group : 0);
     const float to_log2 = fmaxf(fabsf(p.a.scale) * kLog2e, 0x1p-100f);
@@ -670,10 +663,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
     // a tile's codes, as loaded (zeros where there is no page)
     u32x4 raw_k;
     unsigned raw_v[4], raw_ks, raw_vs;
-    bool on = false;
+    int on = 0;
     auto fetch = [&](int k) {
       const int t = token_of(k) + wt;
-      on = k < last && t < s.end && id >= 0 && id < p.c.pages;
+      on = uniform(k < last && t < s.end && id >= 0 && id < p.c.pages ? 1 : 0);
       const int64_t page = (int64_t)(on ? id : 0) * p.c.heads + head, row = (page << shift) + (t & pmask);
       const __amdgpu_buffer_rsrc_t rk = panel_rsrc(p.a.kq + row * kRow, on ? 16 * kRow : 0);
       if constexpr (kFp4) {
@@ -762,7 +755,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
 
     // S^T of set n of the tile in kl; element e: token 32 n + 8 (e / 4) + 4 g + e % 4
     auto scores = [&](const uint8_t* kl, int n) {
-      const uint8_t* at = kl + ((token_wave * kSets + n) * 32 + i) * W::kKRow + 16 * g;
+      const uint8_t* at = kl + (n * 32 + i) * W::kKRow + 16 * g;
       f32x16 o;
 #pragma unroll
       for (int e = 0; e < 16; e++) o[e] = 0;
@@ -773,9 +766,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
     };
     // the masks of set n of tile k, which not all rows see whole
     auto mask_scores = [&](int k, int n, unsigned off) {
-      const int set = token_wave * kSets + n;
-      const unsigned o2 = off >> (2 * set);
-      const unsigned seen = my_word(token_of(k) + 32 * set) & ((o2 & 1 ? 0 : 0xFFFFu) | (o2 & 2 ? 0 : 0xFFFF0000u));
+      const unsigned o2 = off >> (2 * n);
+      const unsigned seen = my_word(token_of(k) + 32 * n) & ((o2 & 1 ? 0 : 0xFFFFu) | (o2 & 2 ? 0 : 0xFFFF0000u));
 #pragma unroll
       for (int e = 0; e < 16; e++) sc[e] = (seen >> (8 * (e / 4) + 4 * g + e % 4)) & 1 ? sc[e] : -INFINITY;
     };
@@ -783,7 +775,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
     auto values = [&](const uint8_t* vl, int n, int h) {
 #pragma unroll
       for (int o = 0; o < kOut; o++) {
-        const int c = 4 * (token_wave * kSets + n) + 2 * h;
+        const int c = 4 * n + 2 * h;
         const bf16x8 v = *(const bf16x8*)(vl + ((i * W::kVRow + (g ^ W::swizzle(i)) * 16) ^ (16 * c)) + 32 * o * W::kVRow);
 #pragma unroll
         for (int t = 0; t < kTerms; t++)
@@ -829,11 +821,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
       if (whole(t0)) return;
 #pragma unroll 1
       for (int n = 0; n < kSets; n++) {
-        const int set = token_wave * kSets + n;
-        unsigned odd = uniform((int)flags[(k - first) & 3].odd[set]);
-        const unsigned seen = odd ? my_word(t0 + 32 * set) : 0;
+        unsigned odd = uniform((int)flags[(k - first) & 3].odd[n]);
+        const unsigned seen = odd ? my_word(t0 + 32 * n) : 0;
         while (odd) {
-          const int bit = __builtin_ctz(odd), t = t0 + 32 * set + bit;
+          const int bit = __builtin_ctz(odd), t = t0 + 32 * n + bit;
           odd &= odd - 1;
           const int64_t page = (int64_t)ids[(unsigned)t >> shift] * p.c.heads + head, row = (page << shift) + (t & pmask);
           const bool mine = (seen >> bit) & 1;
@@ -871,7 +862,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
       const uint8_t *kl = lds_k[(k - first) & 1], *vl = lds_v[(k - first) & 1];
       const unsigned off = uniform((int)flags[(k - first) & 3].off);
       const bool masked = !whole(token_of(k)) || off != 0;
-#pragma unroll
+#pragma unroll 1
       for (int n = 0; n < kSets; n++) {
         sc = scores(kl, n);
         if (masked) mask_scores(k, n, off);
@@ -902,36 +893,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
       w[0] = (int)((u_first + (unsigned)s.n - 1) / per - blockIdx.x) + 1;
       w[1] = (int)blockIdx.x, w[2] = (int)unit;
     }
-    float sum = sum_halves(l), mx = ref;
-    if constexpr (kTokenWaves > 1) {
-      static_assert(kTokenWaves == 2);
-      float* part = (float*)lds + (row_wave * 64 + lane) * kLane;
-      __syncthreads();
-      if (token_wave != 0) {
-#pragma unroll
-        for (int o = 0; o < kOut; o++)
-#pragma unroll
-          for (int q = 0; q < 4; q++)
-            *(f32x4*)(part + 4 + 16 * o + 4 * q) = (f32x4){acc[o][4 * q], acc[o][4 * q + 1], acc[o][4 * q + 2], acc[o][4 * q + 3]};
-        part[0] = mx, part[1] = sum;
-      }
-      __syncthreads();
-      if (token_wave == 0) {
-        const float om = part[0], to = fmaxf(mx, om), base = to > -INFINITY ? to : 0.0f;
-        const float f = __builtin_amdgcn_exp2f(mx - base), of = __builtin_amdgcn_exp2f(om - base);
-        sum = sum * f + part[1] * of;
-        mx = to;
-#pragma unroll
-        for (int o = 0; o < kOut; o++)
-#pragma unroll
-          for (int e = 0; e < 16; e++) acc[o][e] = acc[o][e] * f + part[4 + 16 * o + e] * of;
-      }
-    }
-    if (token_wave == 0 && live) {
+    const float sum = sum_halves(l);
+    if (live) {
       const int64_t hq = qh;
       // a block has at most one part of a unit that a block before it opened (slot
       // 0) and one of a unit that it opens itself (slot 1)
-      const int64_t slot = (2 * (int64_t)blockIdx.x + (opens ? 1 : 0)) * kUnit + row_wave * 32 + i;
+      const int64_t slot = (2 * (int64_t)blockIdx.x + (opens ? 1 : 0)) * kUnit + wave * 32 + i;
 #pragma unroll
       for (int o = 0; o < kOut; o++)
 #pragma unroll
@@ -939,12 +906,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
           const int el = 32 * o + 8 * q + 4 * g;
           const f32x4 v = {acc[o][4 * q], acc[o][4 * q + 1], acc[o][4 * q + 2], acc[o][4 * q + 3]};
           if (!p.split || (opens && closes))
-            store_out(p.a, ((b * drafts + token) * p.a.q_heads + hq) * D + el, finish(p.a, hq, mx, sum, v));
+            store_out(p.a, ((b * drafts + token) * p.a.q_heads + hq) * D + el, finish(p.a, hq, ref, sum, v));
           else
             *(f32x4*)(p.part_o + slot * D + el) = v;
         }
       if (p.split && !(opens && closes) && g == 0) {
-        p.part_ml[2 * slot] = mx;
+        p.part_ml[2 * slot] = ref;
         p.part_ml[2 * slot + 1] = sum;
       }
     }
@@ -957,10 +924,9 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_tree_wide(TreeParams p) {
       rg = 0;
       if (++head == p.c.heads) {
         head = 0;
-        s = tree_span<kT>(p, ++b);
+        span = tree_span<kT>(p, ++b);
       }
     }
-    x = uniform(x), u_first = uniform(u_first), head = uniform(head), rg = uniform(rg), b = uniform((int)b);
     __syncthreads();  // it writes the same LDS
   }
 }
@@ -1039,10 +1005,13 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p, unsigned unit_r
 }  // namespace
 
 // Shape of a call's units.  Up to 64 rows of a cache head, k_tree_attend: N sets
-// of 16 rows a wave, of one or two row waves.  More, k_tree_wide.
+// of 16 rows a wave, of one or two row waves.  More, k_tree_wide, whose blocks
+// decode for 128 or 256 rows.  Measured, D = 128 E4M3, 8 cache heads: 64 rows (64
+// sequences of 4600 tokens) 215 us and 328 us by k_tree_wide; 128 rows (32 of
+// 4600) 215 us by k_tree_attend and 192; 512 rows (4 of 20500) 512 and 350.
 struct TreeUnits {
   bool wide;
-  int sets, tile;
+  int sets, tile, blocks;  // blocks: that take ranges, one or two a CU
   unsigned row_shift, rows, row_groups;  // rows of a unit; units per sequence and cache head
 };
 static TreeUnits tree_units(int64_t drafts, unsigned q_heads, const KvShape& c) {
@@ -1051,9 +1020,10 @@ static TreeUnits tree_units(int64_t drafts, unsigned q_heads, const KvShape& c) 
   u.wide = rows > 64;
   u.sets = rows > kSet && c.dim <= 128 ? 2 : 1;
   u.row_shift = !u.wide && rows > u.sets * kSet ? 1 : 0;
-  u.tile = u.wide ? 8192 / (int)c.dim : kTile;
   u.rows = u.wide ? (rows > 128 || c.dim == 256 ? 256 : 128) : (u.sets * kSet) << u.row_shift;
   u.row_groups = (unsigned)((rows + u.rows - 1) / u.rows);
+  u.tile = u.wide ? 32 * (int)u.rows / (int)c.dim : kTile;
+  u.blocks = u.wide && u.rows == 256 ? 256 : 512;
   return u;
 }
 
@@ -1073,8 +1043,6 @@ static bool tree_ranges(const TreeUnits& u, int64_t units, int64_t tiles) {
   return tiles * u.tile > (units >= 128 ? 2048 : 1024);
 }
 
-constexpr int64_t kRangeBlocks = 512, kWideBlocks = 256;  // two and one a CU
-
 int64_t tree_attend_blocks(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
                            int64_t window, int64_t first) {
   const TreeUnits u = tree_units(drafts, q_heads, c);
@@ -1083,7 +1051,7 @@ int64_t tree_attend_blocks(int64_t batch, int64_t drafts, unsigned q_heads, cons
   if (units > (0x7FFFFFFF - 4096) / tiles) return -1;
   if (!tree_ranges(u, units, tiles)) return units;
   const int64_t waves = u.wide ? 1 : kWaves >> u.row_shift;
-  return std::min<int64_t>(u.wide ? kWideBlocks : kRangeBlocks, units * ((tiles + waves - 1) / waves));
+  return std::min<int64_t>(u.blocks, units * ((tiles + waves - 1) / waves));
 }
 
 int64_t tree_attend_workspace(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
@@ -1124,7 +1092,7 @@ hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, voi
   const dim3 grid((unsigned)blocks), block(kThreads);
 #define MXQ_TREE_R(D, F, T, N) \
   ranges ? k_tree_attend<D, F, T, N, true><<<grid, block, 0, st>>>(p) : k_tree_attend<D, F, T, N, false><<<grid, block, 0, st>>>(p)
-#define MXQ_TREE_W(D, F, T, N) k_tree_wide<D, F, T, N><<<grid, dim3(kWideThreads), 0, st>>>(p)
+#define MXQ_TREE_W(D, F, T, N) k_tree_wide<D, F, T, N><<<grid, dim3(64 * N), 0, st>>>(p)
 #define MXQ_TREE_N(K, D, N)                          \
   do {                                               \
     if (a.bf16_out && fp4) K(D, true, 2, N);         \
