@@ -44,6 +44,7 @@ struct TreeParams {
   // unit, the unit} by opening block (by_block) or by unit, and two slots of
   // partial results a block.
   bool by_block, split;  // split: blocks take ranges (k_tree_wide; else units)
+  unsigned shares;       // equal shares of a unit that a block each takes (where they take no ranges)
   int* parts;
   float *part_o, *part_ml;
 };
@@ -212,13 +213,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
   TreeSpan s;
   if constexpr (!kRanges) {
     unsigned id = blockIdx.x;
+    const unsigned share = uniform(id % p.shares);
+    id /= p.shares;
     rg = uniform(id % p.row_groups);
     id /= p.row_groups;
     head = uniform(id % p.c.heads);
     b = uniform(id / p.c.heads);
     s = tree_span<kTile>(p, b);
-    x = u_first = 0;
-    end = s.n;
+    u_first = 0;
+    x = (unsigned)((uint64_t)s.n * share / p.shares);
+    end = (unsigned)((uint64_t)s.n * (share + 1) / p.shares);
   } else {
     const RangeStart r = range_start<kTile>(p, per_tile, lds_sum, lds_at);
     if (r.x >= r.end) return;
@@ -233,7 +237,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
     const unsigned tokens = (min(row0 + unit_rows, p.rows) - 1) / p.group - token0 + 1;
     const unsigned drafts = (unsigned)p.a.drafts;
     if (threadIdx.x < 2) lds_far[threadIdx.x] = threadIdx.x ? 0x7FFFFFFF : 0;
-    load_masks(p, b, s, token0, tokens, lds_mask, lds_any, lds_depth, lds_far);
 
     // rows: scores are scaled by |scale| (its sign is in q), never by less than
     // what keeps a masked score at -inf
@@ -242,10 +245,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
     float m[N], l[N];  // of the unscaled scores, and of this lane's tokens
     f32x4 acc[N][J];
     bf16x8 qf[N][kSteps];
-    int lo[N];  // context tokens from here on are inside the row's window
     unsigned mask_at[N];
     bool live[N];
-    int lo_most = 0;
 #pragma unroll
     for (int n = 0; n < N; n++) {
       m[n] = -INFINITY, l[n] = 0;
@@ -255,9 +256,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
       live[n] = r < p.rows;
       const unsigned token = live[n] ? r / p.group : token0, qh = head * p.group + (live[n] ? r - token * p.group : 0);
       mask_at[n] = token - token0;
-      lo[n] = 0;
-      if (p.a.window > 0) lo[n] = window_start(p, s.context, lds_depth[token]);
-      lo_most = live[n] ? max(lo_most, lo[n]) : lo_most;
 #pragma unroll
       for (int st = 0; st < kSteps; st++) {
         const int d = D == 64 ? 16 * g + 8 * st : 128 * (st / 4) + 32 * g + 8 * (st & 3);
@@ -266,11 +264,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
         qf[n][st] = __builtin_bit_cast(bf16x8, w ^ q_sign);
       }
     }
-#pragma unroll
-    for (int k = 1; k < 16; k <<= 1) lo_most = max(lo_most, __shfl_xor(lo_most, k, 64));
-    lo_most = uniform(lo_most);
-    const int seen_first = p.a.window > 0 ? (int)min(p.a.first, (int64_t)s.context) : 0;
-
     {
       const unsigned shift = p.c.page_shift, pmask = (1u << shift) - 1;
       // This wave's tiles are first + sub + per_tile j, j < count.  The page ids
@@ -313,6 +306,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
         fetch_k();
         fetch_v(0);
       }
+      // (the masks while the first tile is on its way)
+      load_masks(p, b, s, token0, tokens, lds_mask, lds_any, lds_depth, lds_far);
+      int lo[N], lo_most = 0;  // context tokens from here on are inside the row's window
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        lo[n] = p.a.window > 0 ? window_start(p, s.context, lds_depth[token0 + mask_at[n]]) : 0;
+        lo_most = live[n] ? max(lo_most, lo[n]) : lo_most;
+      }
+#pragma unroll
+      for (int k = 1; k < 16; k <<= 1) lo_most = max(lo_most, __shfl_xor(lo_most, k, 64));
+      lo_most = uniform(lo_most);
+      const int seen_first = p.a.window > 0 ? (int)min(p.a.first, (int64_t)s.context) : 0;
       for (int j = 0; j < count; j++) {
         const int t0 = token_of(j);
         const bool on0 = half[0].on, on1 = half[1].on;
@@ -469,11 +474,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
     }
 
     // join the waves that shared tiles, a set at a time (maxima in log2 units from here on)
-    const bool opens = first == 0, closes = last == s.n;  // of the unit
-    if (kRanges && opens && threadIdx.x == 0 && !(p.by_block && closes)) {
+    const bool opens = kRanges ? first == 0 : blockIdx.x % p.shares == 0, closes = last == s.n;  // of the unit
+    const bool alone = kRanges ? opens && closes : p.shares == 1;
+    if (opens && threadIdx.x == 0 && (kRanges ? !(p.by_block && closes) : !alone)) {
       const unsigned unit = ((unsigned)b * p.c.heads + head) * p.row_groups + rg;
       int* w = p.parts + 4 * (p.by_block ? blockIdx.x : unit);
-      w[0] = (int)((u_first + (unsigned)s.n - 1) / per - blockIdx.x) + 1;
+      w[0] = kRanges ? (int)((u_first + (unsigned)s.n - 1) / per - blockIdx.x) + 1 : (int)p.shares;
       w[1] = (int)blockIdx.x, w[2] = (int)unit;
     }
 #pragma unroll
@@ -511,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
           sum += lds_l[wb + w][rr % kSet];
           o += *(const f32x4*)&lds_o[wb + w][rr % kSet][4 * d4];
         }
-        if (!kRanges || (opens && closes)) {
+        if (alone) {
           const unsigned token = r / p.group;
           const int64_t hq = (int64_t)head * p.group + (r - token * p.group);
           store_out(p.a, ((b * drafts + token) * p.a.q_heads + hq) * D + 4 * d4, finish(p.a, hq, mx, sum, o));
@@ -591,13 +597,16 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
   TreeSpan span;
   if (!p.split) {
     unsigned id = blockIdx.x;
+    const unsigned share = uniform(id % p.shares);
+    id /= p.shares;
     rg = uniform(id % p.row_groups);
     id /= p.row_groups;
     head = uniform(id % p.c.heads);
     b = uniform(id / p.c.heads);
     span = tree_span<kT>(p, b);
-    x = u_first = 0;
-    end = span.n;
+    u_first = 0;
+    x = (unsigned)((uint64_t)span.n * share / p.shares);
+    end = (unsigned)((uint64_t)span.n * (share + 1) / p.shares);
   } else {
     const RangeStart r = range_start<kT>(p, 1, lds_sum, lds_at);
     if (r.x >= r.end) return;
@@ -850,14 +859,16 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
 
     // Tile k's K and V are at k & 1, its flags at k & 3.  It is loaded two turns and
     // decoded one turn before its own.
-    fetch_id(first);
-    fetch(first);
-    fetch_id(first + 1);
-    decode(first);
-    store_v(first);
-    fetch(first + 1);
-    fetch_id(first + 2);
-    __syncthreads();
+    if (first < last) {  // (a share of a short sequence can be empty)
+      fetch_id(first);
+      fetch(first);
+      fetch_id(first + 1);
+      decode(first);
+      store_v(first);
+      fetch(first + 1);
+      fetch_id(first + 2);
+      __syncthreads();
+    }
     for (int k = first; k < last; k++) {
       const uint8_t *kl = lds_k[(k - first) & 1], *vl = lds_v[(k - first) & 1];
       const unsigned off = uniform((int)flags[(k - first) & 3].off);
@@ -886,11 +897,12 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
       __syncthreads();
     }
 
-    const bool opens = first == 0, closes = last == s.n;  // of the unit
-    if (p.split && opens && threadIdx.x == 0 && !(p.by_block && closes)) {
+    const bool opens = p.split ? first == 0 : blockIdx.x % p.shares == 0, closes = last == s.n;  // of the unit
+    const bool alone = p.split ? opens && closes : p.shares == 1;
+    if (opens && threadIdx.x == 0 && (p.split ? !(p.by_block && closes) : !alone)) {
       const unsigned unit = ((unsigned)b * p.c.heads + head) * p.row_groups + rg;
       int* w = p.parts + 4 * (p.by_block ? blockIdx.x : unit);
-      w[0] = (int)((u_first + (unsigned)s.n - 1) / per - blockIdx.x) + 1;
+      w[0] = p.split ? (int)((u_first + (unsigned)s.n - 1) / per - blockIdx.x) + 1 : (int)p.shares;
       w[1] = (int)blockIdx.x, w[2] = (int)unit;
     }
     const float sum = sum_halves(l);
@@ -905,12 +917,12 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
         for (int q = 0; q < 4; q++) {
           const int el = 32 * o + 8 * q + 4 * g;
           const f32x4 v = {acc[o][4 * q], acc[o][4 * q + 1], acc[o][4 * q + 2], acc[o][4 * q + 3]};
-          if (!p.split || (opens && closes))
+          if (alone)
             store_out(p.a, ((b * drafts + token) * p.a.q_heads + hq) * D + el, finish(p.a, hq, ref, sum, v));
           else
             *(f32x4*)(p.part_o + slot * D + el) = v;
         }
-      if (p.split && !(opens && closes) && g == 0) {
+      if (!alone && g == 0) {
         p.part_ml[2 * slot] = ref;
         p.part_ml[2 * slot + 1] = sum;
       }
@@ -1037,36 +1049,56 @@ static int64_t tree_tiles(const TreeUnits& u, int64_t drafts, const KvShape& c, 
   return tiles;
 }
 
-// Whether blocks take ranges of the flattened tiles (and a second launch joins
-// the parts), or a unit each.
-static bool tree_ranges(const TreeUnits& u, int64_t units, int64_t tiles) {
-  return tiles * u.tile > (units >= 128 ? 2048 : 1024);
+// How a call's tiles are cut.  By ranges, blocks take equal runs of all units'
+// tiles, whatever the sequences' lengths; a block that ends one unit and begins
+// the next pays for the masks, the rows and the results of both.  By shares, a
+// unit is cut in equal shares, a block each.
+//
+// Shares are for short calls and for one sequence, from 8 tiles a wave on: the
+// second launch and the parts cost 5 us, a wave's tile of two row sets 1.1 us.  So
+// cut, 8 tokens over 1000 (8 cache heads of 8 query heads, D = 128) take 20 us
+// instead of 35 (27 by ranges), over 8 sequences 25 (37); by two blocks a CU these 8 take 32.
+// Below 8 tiles (256 tokens, one sequence) a call takes 20 us either way.
+struct TreePlan {
+  bool ranges;
+  unsigned shares;
+  int64_t blocks;
+};
+static TreePlan tree_plan(const TreeUnits& u, const KvShape& c, int64_t batch, int64_t tiles) {
+  const int64_t units = batch * c.heads * u.row_groups, waves = u.wide ? 1 : kWaves >> u.row_shift, each = (tiles + waves - 1) / waves;
+  const bool deep = tiles * u.tile > (units >= 128 ? 2048 : 1024);
+  TreePlan t = {deep && !(batch == 1 && 4 * units <= u.blocks), 1, units};
+  if (t.ranges) {
+    t.blocks = std::min<int64_t>(u.blocks, units * each);
+  } else if (each >= 8) {
+    t.shares = (unsigned)std::max<int64_t>(1, std::min((deep ? u.blocks : u.wide ? 128 : 256) / units, each / 2));
+    t.blocks = units * t.shares;
+  }
+  return t;
 }
 
+// Blocks of a call, -1 where its tiles are too many.
 int64_t tree_attend_blocks(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
                            int64_t window, int64_t first) {
   const TreeUnits u = tree_units(drafts, q_heads, c);
-  const int64_t units = batch * c.heads * u.row_groups, tiles = tree_tiles(u, drafts, c, table_width, window, first);
+  const int64_t tiles = tree_tiles(u, drafts, c, table_width, window, first);
   // flattened tile indexes are 32 bits, with room for one range more
-  if (units > (0x7FFFFFFF - 4096) / tiles) return -1;
-  if (!tree_ranges(u, units, tiles)) return units;
-  const int64_t waves = u.wide ? 1 : kWaves >> u.row_shift;
-  return std::min<int64_t>(u.blocks, units * ((tiles + waves - 1) / waves));
+  if (batch * c.heads * u.row_groups > (0x7FFFFFFF - 4096) / tiles) return -1;
+  return tree_plan(u, c, batch, tiles).blocks;
 }
 
 int64_t tree_attend_workspace(int64_t batch, int64_t drafts, unsigned q_heads, const KvShape& c, int64_t table_width,
                               int64_t window, int64_t first) {
   const TreeUnits u = tree_units(drafts, q_heads, c);
-  if (!tree_ranges(u, batch * c.heads * u.row_groups, tree_tiles(u, drafts, c, table_width, window, first))) return 0;
-  const int64_t blocks = tree_attend_blocks(batch, drafts, q_heads, c, table_width, window, first);
-  return blocks * (16 + 2 * (int64_t)u.rows * (c.dim + 2) * 4);
+  const TreePlan t = tree_plan(u, c, batch, tree_tiles(u, drafts, c, table_width, window, first));
+  return t.ranges || t.shares > 1 ? t.blocks * (16 + 2 * (int64_t)u.rows * (c.dim + 2) * 4) : 0;
 }
 
 template <int D>
-static void launch_join(const TreeParams& p, unsigned unit_rows, int64_t records, hipStream_t st) {
+static void launch_join(const TreeParams& p, unsigned unit_rows, int64_t records, bool few, hipStream_t st) {
   constexpr int kLines = 256 / (D / 4), kFew = kLines > 8 ? kLines / 8 : 1;
   const unsigned rows = std::min(p.rows, unit_rows);
-  if (p.by_block)
+  if (few)
     k_tree_join<D, kLines><<<dim3((unsigned)records, (rows + kLines - 1) / kLines), dim3(256), 0, st>>>(p, unit_rows);
   else
     k_tree_join<D, kFew><<<dim3((unsigned)records, (rows + kFew - 1) / kFew), dim3(256), 0, st>>>(p, unit_rows);
@@ -1081,11 +1113,12 @@ hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, voi
   p.rows = p.group * (unsigned)a.drafts;
   p.row_groups = u.row_groups;
   p.row_shift = u.row_shift;
-  const int64_t units = a.batch * c.heads * u.row_groups;
-  const int64_t blocks = tree_attend_blocks(a.batch, a.drafts, a.q_heads, c, a.table_width, a.window, a.first);
-  const bool ranges = tree_ranges(u, units, tree_tiles(u, a.drafts, c, a.table_width, a.window, a.first));
+  const TreePlan t = tree_plan(u, c, a.batch, tree_tiles(u, a.drafts, c, a.table_width, a.window, a.first));
+  const int64_t units = a.batch * c.heads * u.row_groups, blocks = t.blocks;
+  const bool ranges = t.ranges;
   p.split = ranges;
-  p.by_block = units >= blocks / 2;
+  p.shares = t.shares;
+  p.by_block = ranges && units >= blocks / 2;
   p.parts = (int*)workspace;  // at most a record a block, in either case
   p.part_o = (float*)((uint8_t*)workspace + blocks * 16);
   p.part_ml = p.part_o + 2 * blocks * u.rows * c.dim;
@@ -1117,11 +1150,12 @@ hipError_t launch_tree_attend(const TreeArgs& a, const KvShape& c, bool fp4, voi
   } else {
     MXQ_TREE_N(MXQ_TREE_R, 256, 1);
   }
-  if (ranges) {
+  if (ranges || t.shares > 1) {
     const int64_t records = p.by_block ? blocks : units;
-    if (c.dim == 64) launch_join<64>(p, u.rows, records, st);
-    else if (c.dim == 128) launch_join<128>(p, u.rows, records, st);
-    else launch_join<256>(p, u.rows, records, st);
+    const bool few = blocks < 8 * units;  // parts of a unit
+    if (c.dim == 64) launch_join<64>(p, u.rows, records, few, st);
+    else if (c.dim == 128) launch_join<128>(p, u.rows, records, few, st);
+    else launch_join<256>(p, u.rows, records, few, st);
   }
 #undef MXQ_TREE_N
 #undef MXQ_TREE_W

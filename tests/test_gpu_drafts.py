@@ -346,6 +346,21 @@ def test_tree_window_over_ranges(window, first):
     tree_case(window, [4000, 100, 1600], 6, 2, 4, 64, 16, "mxfp8", window=window, first=first)
 
 
+@pytest.mark.parametrize("context,drafts,heads,group,d,window", [
+    ([0, 1, 700], 9, 2, 8, 128, 0),          # shares of the short ones that are empty
+    ([0, 1, 700], 5, 2, 8, 64, 0),
+    ([0, 1, 700], 2, 2, 3, 256, 0),
+    ([147, 1848, 2, 1], 8, 2, 9, 128, 299),
+    ([0], 8, 1, 8, 128, 0),
+    ([4999], 8, 1, 8, 128, 0),               # one long sequence, 64 rows and 65
+    ([4999], 13, 1, 5, 128, 0),
+    ([4999], 129, 1, 2, 64, 0),
+    ([4999], 1, 1, 1, 256, 3000),
+])
+def test_tree_shares(context, drafts, heads, group, d, window):
+    tree_case(71, context, drafts, heads, group, d, 16, "mxfp8", window=window, first=5 if window else 0, extra_width=60)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_tree_random(seed):
     rng = np.random.default_rng(seed + 500)
