@@ -638,3 +638,150 @@ def test_sample_outputs_and_repeat():
         for r in (0, 17):  # a row alone, split otherwise
             t1, p1 = mxq.sample(x[r:r + 1], u[r:r + 1], **s)
             assert torch.equal(t1, t[r:r + 1]) and torch.equal(p1, p[r:r + 1])
+
+
+# ------------------------------------------------------------------ the three together
+
+class Step:
+    """A step: rotation and write, attention of the
+    trees, logits (fp32 sums of the outputs) and a draw at each node."""
+
+    def __init__(self, seed, context, drafts, heads, group, d, page, fmt, vocab):
+        self.rng = np.random.default_rng(seed)
+        self.context, self.drafts, self.heads, self.group, self.d, self.fmt = context, drafts, heads, group, d, fmt
+        batch = len(context)
+        self.bits = random_trees(self.rng, batch, drafts, short=False)
+        counts = [-(-(n + drafts) // page) for n in context]
+        pages = sum(counts) + 1
+        order = self.rng.permutation(pages).astype(np.int32)
+        self.table = np.full((batch, max(counts)), -1, dtype=np.int32)
+        self.slots, at = np.zeros((batch, drafts), dtype=np.int64), 0
+        for b, c in enumerate(counts):
+            self.table[b, :c] = order[at:at + c]
+            at += c
+            pos = context[b] + np.arange(drafts)
+            self.slots[b] = self.table[b, pos // page].astype(np.int64) * page + pos % page
+        self.cache = on_device(filled_cache(self.rng, pages, page, heads, d, fmt))
+        depth = self.bits.sum(-1) - 1
+        self.positions = (np.array(context)[:, None] + np.maximum(depth, 0)).astype(np.int64)
+        self.freqs = (10000.0 ** (-np.arange(d // 2) / (d // 2))).astype(np.float32)
+        self.w = (self.rng.standard_normal((heads * group * d, vocab)) / 4).astype(np.float32)
+        self.x = torch.zeros(batch * drafts, (group + 2) * heads * d, dtype=torch.bfloat16, device="cuda")
+        self.u = torch.zeros(batch * drafts, device="cuda")
+        self.args = [dev(a) for a in (self.slots.ravel(), self.positions.ravel(), self.freqs, self.table,
+                                      np.array(context, dtype=np.int32), dm.mask_of(self.bits), self.w)]
+        self.ws, self.ws2 = (torch.full((1 << 25,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2))
+        self.new_input()
+
+    def new_input(self):
+        self.x.copy_(torch.from_numpy(self.rng.standard_normal(tuple(self.x.shape)).astype(np.float32)))
+        self.u.copy_(torch.from_numpy(self.rng.random(len(self.u)).astype(np.float32)))
+
+    def run(self):
+        h, d, g = self.heads, self.d, self.group
+        slots, positions, freqs, table, context, mask, w = self.args
+        q, k, v = (t.unflatten(1, (-1, d)) for t in self.x.split([h * g * d, h * d, h * d], 1))
+        turned = mxq.rope_append(self.cache, q, k, v, slots, positions, freqs)
+        y = mxq.tree_attention(turned, self.cache, table, context, mask, workspace=self.ws)
+        logits = y.flatten(1).float() @ w
+        return (turned, y, logits) + mxq.sample(logits, self.u, temperature=0.8, top_k=50, top_p=0.95, workspace=self.ws2)
+
+
+@pytest.mark.parametrize("context,drafts,heads,group,d,fmt,vocab", [
+    ([40, 0, 333], 7, 2, 4, 64, "mxfp8", 1000),
+    ([1500, 17], 20, 1, 8, 128, "mxfp4", 20000),
+    ([2100], 1, 2, 2, 256, "mxfp8", 9001),
+])
+def test_step_of_the_three(context, drafts, heads, group, d, fmt, vocab):
+    """Each result against 64 bits from the results before it, the cache as written."""
+    s = Step(5, context, drafts, heads, group, d, 16, fmt, vocab)
+    turned, y, logits, tokens, shares = s.run()
+    q64 = oracle.to_f64(host(turned)).reshape(len(context), drafts, heads * group, d)
+    ref, size, mag = dm.tree_attention(q64, [host(a) for a in s.cache], s.table, context, s.bits, fmt, d ** -0.5)
+    bound = tree_bound(ref, size, mag, max(context) + drafts, d, torch.bfloat16)
+    assert (np.abs(oracle.to_f64(host(y)).reshape(ref.shape) - ref) <= bound).all()
+    x64, u = host(logits).astype(np.float64), host(s.u)
+    for r in range(len(x64)):
+        dm.draw_check(x64[r], u[r], 0.8, 50, 0.95, 0.0, int(tokens[r]), float(shares[r]), f"row {r}")
+
+
+def test_step_captured_and_replayed():
+    """Two captured graphs that share the workspaces, replayed in turn with new
+    inputs and eager calls between, give what eager calls give."""
+    steps = [Step(6, [1500, 17], 20, 1, 8, 128, 16, "mxfp8", 20000), Step(7, [30, 2000, 5], 3, 2, 4, 64, 16, "mxfp4", 9001)]
+    steps[1].ws, steps[1].ws2 = steps[0].ws, steps[0].ws2
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for s in steps:
+        with torch.cuda.stream(side):
+            s.run()
+        torch.cuda.current_stream().wait_stream(side)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(s.run())
+    for turn in range(4):
+        for s, graph, out in zip(steps, graphs, outs):
+            s.new_input()
+            before = [a.clone() for a in s.cache]
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in out] + [a.clone() for a in s.cache]
+            for a, b in zip(s.cache, before):
+                a.copy_(b)
+            # eagerly, on another stream every second time
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side if turn % 2 else torch.cuda.current_stream()):
+                want = list(s.run()) + list(s.cache)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want)), turn
+
+
+def test_step_past_32_bit_offsets():
+    """Pages whose bytes lie past 2^32 of a cache, and rows of logits as far apart."""
+    heads, d, page, pages = 8, 128, 128, 33500  # 131072 bytes a page of keys
+    far = mxq.kv_cache(pages, page, heads, d)
+    near = mxq.kv_cache(8, page, heads, d)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = 6 * page
+    ids = torch.tensor([pages - 1, 5, 33000, 32768, 32767, 16384], device="cuda")
+    x = torch.randn(n, 3 * heads, d, generator=g, device="cuda").bfloat16()
+    q, k, v = x.split(heads, 1)
+    within = torch.arange(page, device="cuda")
+    freqs = 10000.0 ** (-torch.arange(64, device="cuda") / 64)
+    positions = torch.arange(n, device="cuda")
+    a = mxq.rope_append(far, q, k, v, (ids[:, None] * page + within).flatten(), positions, freqs)
+    b = mxq.rope_append(near, q, k, v, positions, positions, freqs)
+    assert torch.equal(a, b)
+    for p, t in zip(far, near):
+        assert torch.equal(p[ids].view(torch.uint8), t[:6].view(torch.uint8))
+    lens = torch.tensor([n - 20], dtype=torch.int32, device="cuda")
+    for drafts, group in ((20, 1), (20, 4)):  # few rows of a cache head, and many
+        mask = mxq.tree_mask(list(range(-1, drafts - 1)))
+        qs = torch.randn(drafts, heads * group, d, generator=g, device="cuda").bfloat16()
+        ya = mxq.tree_attention(qs, far, ids[None].int(), lens, mask)
+        yb = mxq.tree_attention(qs, near, torch.arange(6, device="cuda")[None].int(), lens, mask)
+        assert torch.equal(ya, yb) and ya.float().abs().max() > 0
+    del far
+    logits = torch.randn(3, 50001, generator=g, device="cuda")
+    wide = torch.empty((2 << 30) + (1 << 20), device="cuda")
+    rows = wide.as_strided((3, 50001), (1 << 30, 1))
+    rows.copy_(logits)
+    u = torch.rand(3, generator=g, device="cuda")
+    for kw in (dict(), dict(top_k=50, top_p=0.9), dict(min_p=0.1)):
+        ta, tb = mxq.sample(logits, u, **kw), mxq.sample(rows, u, **kw)
+        assert torch.equal(ta[0], tb[0]) and torch.equal(ta[1], tb[1])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_draft_step_example(fmt):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_step.py")
+    spec = importlib.util.spec_from_file_location("draft_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    taken, lens = example.run(fmt, batch=3, prompt=100, steps=4)
+    assert len(taken) == 3 and all(4 <= len(t) <= 4 * 4 and all(0 <= x < 64 for x in t) for t in taken)
+    for b, (t, n) in enumerate(zip(taken, lens)):
+        assert n == max(1, 100 * (b + 1) // 3) - 1 + len(t)
