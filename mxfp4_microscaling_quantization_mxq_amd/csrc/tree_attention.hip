@@ -20,6 +20,14 @@
 // Split.  As for one token: a unit is one sequence, one cache head and a group
 // of its rows; the tiles of all units in order are cut into equal ranges, one a
 // block, and ranges that end inside a unit leave partial results to be joined.
+// Short calls and single sequences are cut by shares instead (tree_plan).
+//
+// What bounds it.  Few rows: the cache's bytes (64 sequences of 8192 tokens, 8
+// query heads over each of 8 cache heads, D = 128, E4M3: 178 us, 6.2 TB/s).  64
+// rows: decoding, once for each 32 (64 sequences of 4600 tokens with 8 drafted
+// ones 212 us, 2.9 TB/s).  Many rows: products, with P in two bf16 terms or three,
+// and beside them the exponentials and the decoding (64 drafted tokens over 4 x
+// 20500: 341 us, 505 TFLOP/s counted once, 760 as issued).
 #include <type_traits>
 
 #include "mxq_attend.h"
@@ -101,26 +109,24 @@ __device__ __forceinline__ void load_masks(const TreeParams& p, int64_t b, const
   }
   if (threadIdx.x < kMaskRow) any[threadIdx.x] = 0;
   __syncthreads();
-  for (unsigned t = threadIdx.x; t < tokens; t += blockDim.x) {
-    const uint32_t* m = (const uint32_t*)(p.a.mask + (b * drafts + token0 + t) * words);
+  for (unsigned e = threadIdx.x; e < tokens * 2 * words; e += blockDim.x) {
+    const unsigned t = e / (2 * words), w = e - t * 2 * words;
     const int depth = depths[token0 + t];
+    unsigned v = ((const uint32_t*)(p.a.mask + (b * drafts + token0 + t) * words))[w] & below((int)drafts - (int)(32 * w));
+    if (p.a.window > 0 && p.a.window < p.a.drafts) {
+      unsigned left = v;
+      while (left) {
+        const int bit = __builtin_ctz(left), d = depths[32 * w + bit];
+        left &= left - 1;
+        if (depth - d >= p.a.window && s.context + d >= p.a.first) v &= ~(1u << bit);
+      }
+    }
+    mask[t][1 + w] = v;
+    atomicOr(&any[1 + w], v);
+    if (w != 0) continue;
     atomicMax(&far[0], depth);
     atomicMin(&far[1], depth);
-    mask[t][0] = 0;
-    for (unsigned w = 0; w < 2 * words; w++) {
-      unsigned v = m[w] & below((int)drafts - (int)(32 * w));
-      if (p.a.window > 0 && p.a.window < p.a.drafts) {
-        unsigned left = v;
-        while (left) {
-          const int bit = __builtin_ctz(left), d = depths[32 * w + bit];
-          left &= left - 1;
-          if (depth - d >= p.a.window && s.context + d >= p.a.first) v &= ~(1u << bit);
-        }
-      }
-      mask[t][1 + w] = v;
-      atomicOr(&any[1 + w], v);
-    }
-    mask[t][1 + 2 * words] = 0;
+    mask[t][0] = mask[t][1 + 2 * words] = 0;
   }
   __syncthreads();
 }
@@ -558,6 +564,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
 // leaves 16 of 32 tokens of one row in a lane, which are the B operand of O^T +=
 // V^T P^T for V's tokens in the order 0-3, 8-11, 4-7, 12-15 of each 16.
 //
+// The next tile but one is on its way while a tile is multiplied and the next one
+// decoded: two tiles ahead changed nothing (342 us, 345).  A wave's products wait for its
+// exponentials; forming one set's while the next one's products run needs more registers
+// than there are and spills (340 to 370).  Scalars that stay in scalar registers
+// matter most: page addresses in vector registers made a loop of each load (376).
+//
 // A row's reference moves only where its maximum has risen by more than 2^8 above
 // it: the old terms are seldom scaled, and probabilities of up to 2^8 lose nothing.
 template <int D, int kW>
@@ -869,12 +881,13 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
       fetch_id(first + 2);
       __syncthreads();
     }
+    const int sets = row0 + wave * 32 < p.rows ? kSets : 0;  // (a wave without rows decodes only)
     for (int k = first; k < last; k++) {
       const uint8_t *kl = lds_k[(k - first) & 1], *vl = lds_v[(k - first) & 1];
       const unsigned off = uniform((int)flags[(k - first) & 3].off);
       const bool masked = !whole(token_of(k)) || off != 0;
 #pragma unroll 1
-      for (int n = 0; n < kSets; n++) {
+      for (int n = 0; n < sets; n++) {
         sc = scores(kl, n);
         if (masked) mask_scores(k, n, off);
         const float alpha = weights();
