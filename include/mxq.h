@@ -477,7 +477,7 @@ MXQ_API mxq_status mxq_paged_attention(const void *q, int64_t q_stride, const ui
  * q bf16 [batch * drafts] rows at q + r * q_stride elements (row b * drafts + i
  * is token i of sequence b); context int32 [batch]; mask uint64 [batch][drafts]
  * [words]; out [batch * drafts][q_heads][head_dim] of type odt; 1 <= drafts <=
- * 256; window, first >= 0.  The table, sinks, head_dim, scale, accuracy, NaN,
+ * 256; window, first >= 0; out must not overlap q.  The table, sinks, head_dim, scale, accuracy, NaN,
  * workspace (mxq_tree_attention_workspace) and split as mxq_paged_attention.
  */
 MXQ_API mxq_status mxq_tree_attention_workspace(int64_t batch, int64_t drafts, int64_t q_heads, int64_t kv_heads,
@@ -511,7 +511,8 @@ MXQ_API mxq_status mxq_tree_attention(const void *q, int64_t q_stride, const uin
  * alignment of its type); u fp32 [rows].  Each setting is an array [rows], or one
  * value for all rows where its array is NULL (top_k int32, the others fp32; the
  * value must not be NaN).  tokens int32 [rows], shares fp32 [rows].  vocab <=
- * 2^20, rows <= 2^20.  workspace: 16-byte aligned, at least the bytes that
+ * 2^20, rows <= 2^20; tokens and shares overlap neither each other nor what is
+ * read.  workspace: 16-byte aligned, at least the bytes that
  * mxq_sample_workspace gives (may be NULL for 0); its content need not be
  * prepared, and it may be reused by any later call on the same stream.
  */

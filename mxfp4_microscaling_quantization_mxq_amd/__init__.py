@@ -847,7 +847,8 @@ def tree_attention(q, cache, table, context, mask, scale=None, window=0, first=0
     stride free).  window > 0 hides positions that far back or further, but not
     the `first` first positions of the sequence; a drafted token's position is
     context + the drafted tokens before it that it sees.  scale, sinks and
-    workspace as in paged_attention.  A token that sees nothing gives zeros."""
+    workspace as in paged_attention; out must not overlap q.  A token that sees
+    nothing gives zeros."""
     torch = _torch()
     dev = _index(cache[0])
     pages, heads, page, d, fmt = _cache(cache, dev)
@@ -925,7 +926,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=Non
     times their sum; its share is its weight over that sum.  temperature 0: the
     largest.  top_k 0, top_p 1 and min_p 0 leave all.  Each setting is a number or
     a tensor [rows] (top_k int32, the others fp32).  A row with a NaN or +inf, or
-    nothing but -inf, gives token -1 and share NaN."""
+    nothing but -inf, gives token -1 and share NaN.  tokens and shares, if given,
+    must not overlap what is read."""
     torch = _torch()
     if not isinstance(logits, torch.Tensor):
         raise TypeError(f"logits must be a torch.Tensor, got {type(logits).__name__}")

@@ -449,10 +449,10 @@ static bool tree_sizes(int64_t batch, int64_t drafts, int64_t q_heads, const mxq
                        int64_t window, int64_t first) {
   if (batch < 1 || q_heads < 1 || q_heads % c.heads != 0 || (c.dim != 64 && c.dim != 128 && c.dim != 256)) return false;
   if (drafts < 1 || drafts > 256 || table_width < 1 || table_width > 0x7FFFFFFF || window < 0 || first < 0) return false;
-  // blocks of 256 threads of both launches: below 2^32 threads
+  // blocks of up to 512 threads, and 256 of the second launch: below 2^32 threads
   if (q_heads > (1 << 20) || batch > (1 << 24) / q_heads) return false;
   const int64_t blocks = mxq::tree_attend_blocks(batch, drafts, (unsigned)q_heads, c, table_width, window, first);
-  return blocks > 0 && blocks < (1 << 24);
+  return blocks > 0 && blocks < (1 << 23);
 }
 
 mxq_status mxq_tree_attention_workspace(int64_t batch, int64_t drafts, int64_t q_heads, int64_t kv_heads,
@@ -487,6 +487,10 @@ mxq_status mxq_tree_attention(const void* q, int64_t q_stride, const uint8_t* kq
   if (!aligned16(q) || !aligned16(out) || (need > 0 && !aligned16(workspace))) return MXQ_ERROR_MISALIGNED;
   if (((uintptr_t)table & 3u) || ((uintptr_t)context & 3u) || ((uintptr_t)sinks & 3u) || ((uintptr_t)mask & 7u))
     return MXQ_ERROR_MISALIGNED;
+  // (blocks that read a row of q may run after one that has written it)
+  if (overlap(out, batch * drafts * q_heads * head_dim * (odt == MXQ_BF16 ? 2 : 4), q,
+              2 * ((batch * drafts - 1) * q_stride + q_heads * head_dim)))
+    return MXQ_ERROR_INVALID_VALUE;
   e = check_device();
   if (e != MXQ_SUCCESS) return e;
   mxq::TreeArgs a;
@@ -538,6 +542,15 @@ mxq_status mxq_sample(const void* logits, mxq_dtype dt, int64_t stride, int64_t 
   for (const void* p : {(const void*)u, (const void*)temperature_of, (const void*)top_k_of, (const void*)top_p_of,
                         (const void*)min_p_of, (const void*)tokens, (const void*)shares})
     if ((uintptr_t)p & 3u) return MXQ_ERROR_MISALIGNED;
+  // (several launches read a row's inputs)
+  const int64_t row_bytes = 4 * rows;
+  for (const void* to : {(const void*)tokens, (const void*)shares}) {
+    if (overlap(to, row_bytes, logits, (dt == MXQ_BF16 ? 2 : 4) * ((rows - 1) * stride + vocab))) return MXQ_ERROR_INVALID_VALUE;
+    for (const void* p : {(const void*)u, (const void*)temperature_of, (const void*)top_k_of, (const void*)top_p_of,
+                          (const void*)min_p_of})
+      if (p && overlap(to, row_bytes, p, row_bytes)) return MXQ_ERROR_INVALID_VALUE;
+  }
+  if (overlap(tokens, row_bytes, shares, row_bytes)) return MXQ_ERROR_INVALID_VALUE;
   mxq_status e = check_device();
   if (e != MXQ_SUCCESS) return e;
   mxq::SampleArgs a;

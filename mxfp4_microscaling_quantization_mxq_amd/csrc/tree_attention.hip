@@ -28,8 +28,6 @@
 // ones 212 us, 2.9 TB/s).  Many rows: products, with P in two bf16 terms or three,
 // and beside them the exponentials and the decoding (64 drafted tokens over 4 x
 // 20500: 341 us, 505 TFLOP/s counted once, 760 as issued).
-#include <type_traits>
-
 #include "mxq_attend.h"
 
 namespace mxq {

@@ -99,6 +99,13 @@ def test_tree_refusals(lib):
         assert tree(lib, **bad) == MISALIGNED, bad
 
 
+def test_tree_refuses_an_output_over_q(lib):
+    last = 9 * 2 * 2048  # bytes to the last of 10 rows
+    for bad in (dict(out=A), dict(q=B, out=ctypes.c_void_p(B.value + last + 2032), qs=2048),
+                dict(q=ctypes.c_void_p(B.value + 10 * 8 * 128 * 4 - 16), dt=0), dict(batch=1 << 22, width=1, qh=2, drafts=1)):
+        assert tree(lib, **dict(dict(qs=2048, dt=1), **bad)) == INVALID, bad
+
+
 def tree_workspace(lib, batch, drafts, qh, heads, page, dim, width, window=0, first=0):
     n = ctypes.c_int64(-1)
     code = lib.mxq_tree_attention_workspace(batch, drafts, qh, heads, page, dim, width, window, first, ctypes.byref(n))
@@ -176,6 +183,10 @@ def test_sample_refusals(lib):
     for bad in (dict(x=MIS2, dt=0), dict(x=ctypes.c_void_p(0x1000001)), dict(u=MIS2), dict(t_of=MIS2), dict(k_of=MIS2),
                 dict(p_of=MIS2), dict(m_of=MIS2), dict(tokens=MIS2), dict(shares=MIS2)):
         assert draw(lib, **bad) == MISALIGNED, bad
+    for bad in (dict(tokens=A), dict(shares=A), dict(tokens=B), dict(shares=B), dict(shares=C), dict(t_of=C), dict(k_of=D),
+                dict(p_of=D), dict(m_of=C), dict(tokens=ctypes.c_void_p(A.value + 4 * 296)),
+                dict(shares=ctypes.c_void_p(C.value + 8))):
+        assert draw(lib, **dict(dict(dt=0), **bad)) == INVALID, bad
     n = ctypes.c_int64(-1)
     assert lib.mxq_sample_workspace(3, 100, ctypes.byref(n)) == 0 and n.value >= 0
     assert lib.mxq_sample_workspace(0, 100, ctypes.byref(n)) == INVALID
