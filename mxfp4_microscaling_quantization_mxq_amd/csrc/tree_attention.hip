@@ -882,6 +882,12 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
     const int sets = row0 + wave * 32 < p.rows ? kSets : 0;  // (a wave without rows decodes only)
     for (int k = first; k < last; k++) {
       const uint8_t *kl = lds_k[(k - first) & 1], *vl = lds_v[(k - first) & 1];
+      if (k + 1 < last) {
+        decode(k + 1);
+        store_v(k + 1);
+      }
+      fetch(k + 2);
+      fetch_id(k + 3);
       const unsigned off = uniform((int)flags[(k - first) & 3].off);
       const bool masked = !whole(token_of(k)) || off != 0;
 #pragma unroll 1
@@ -897,12 +903,6 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
         values(vl, n, 0);
         values(vl, n, 1);
       }
-      if (k + 1 < last) {
-        decode(k + 1);
-        store_v(k + 1);
-      }
-      fetch(k + 2);
-      fetch_id(k + 3);
       odd_values(k);
       if (threadIdx.x == 0) flags[(k - first + 2) & 3] = {};
       __syncthreads();
