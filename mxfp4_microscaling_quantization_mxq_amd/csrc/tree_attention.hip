@@ -27,7 +27,7 @@
 // rows: decoding, once for each 32 (64 sequences of 4600 tokens with 8 drafted
 // ones 212 us, 2.9 TB/s).  Many rows: products, with P in two bf16 terms or three,
 // and beside them the exponentials and the decoding (64 drafted tokens over 4 x
-// 20500: 341 us, 505 TFLOP/s counted once, 760 as issued).
+// 20500: 322 us, 536 TFLOP/s counted once, 800 as issued).
 #include "mxq_attend.h"
 
 namespace mxq {
@@ -562,11 +562,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
 // leaves 16 of 32 tokens of one row in a lane, which are the B operand of O^T +=
 // V^T P^T for V's tokens in the order 0-3, 8-11, 4-7, 12-15 of each 16.
 //
-// The next tile but one is on its way while a tile is multiplied and the next one
-// decoded: two tiles ahead changed nothing (342 us, 345).  A wave's products wait for its
-// exponentials; forming one set's while the next one's products run needs more registers
-// than there are and spills (340 to 370).  Scalars that stay in scalar registers
-// matter most: page addresses in vector registers made a loop of each load (376).
+// A turn decodes the next tile, whose loads were issued a turn before, and then
+// multiplies (322 us for the size above; after the products 341; by half of the waves
+// before and half after 355; two tiles ahead no better).  A wave's products wait for its
+// exponentials; forming one set's while the next one's products run needs more
+// registers than there are and spills (340 to 370).  Scalars that stay in scalar
+// registers matter most: page addresses in vector registers made a loop of each
+// load (376).
 //
 // A row's reference moves only where its maximum has risen by more than 2^8 above
 // it: the old terms are seldom scaled, and probabilities of up to 2^8 lose nothing.
@@ -868,7 +870,7 @@ __global__ __launch_bounds__(64 * kW, 2) void k_tree_wide(TreeParams p) {
     };
 
     // Tile k's K and V are at k & 1, its flags at k & 3.  It is loaded two turns and
-    // decoded one turn before its own.
+    // decoded one turn before its own, ahead of that one's products.
     if (first < last) {  // (a share of a short sequence can be empty)
       fetch_id(first);
       fetch(first);
@@ -1031,7 +1033,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p, unsigned unit_r
 // of 16 rows a wave, of one or two row waves.  More, k_tree_wide, whose blocks
 // decode for 128 or 256 rows.  Measured, D = 128 E4M3, 8 cache heads: 64 rows (64
 // sequences of 4600 tokens) 215 us and 328 us by k_tree_wide; 128 rows (32 of
-// 4600) 215 us by k_tree_attend and 192; 512 rows (4 of 20500) 512 and 350.
+// 4600) 215 us by k_tree_attend and 182; 512 rows (4 of 20500) 512 and 322.
 struct TreeUnits {
   bool wide;
   int sets, tile, blocks;  // blocks: that take ranges, one or two a CU
