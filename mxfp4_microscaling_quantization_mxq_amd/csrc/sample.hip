@@ -235,15 +235,17 @@ struct CutLds {
   u64 wave_sum[16];
   unsigned wave_max[16];
   u64 found_mass;
-  unsigned found_count, found;
+  unsigned found_count, found_here, found;
 };
 
 // The key at which a source's elements, from the largest down, reach a count (at
 // least `count` of them) or a mass (double(sum) >= mass): eight bits at a time.
-// `above` of them lie above the source.  Returns it with what lies above the key.
+// `above` of them lie above the source.  Returns it with what lies above the key
+// and the number that have it (the lowest key, where all of them do not reach).
 struct Cut {
   unsigned key, count;
   u64 mass;
+  unsigned here;
 };
 template <bool kCount, class Source, class Mass>
 __device__ Cut cut_at(const Source& src, Cut above, unsigned count, double mass, int lowest, CutLds& sh, Mass mass_of) {
@@ -253,7 +255,7 @@ __device__ Cut cut_at(const Source& src, Cut above, unsigned count, double mass,
 #pragma unroll 1
   for (int shift = 24; shift >= lowest; shift -= 8) {
     for (int i = threadIdx.x; i < 256; i += blockDim.x) sh.bin_mass[i] = 0, sh.bin_count[i] = 0;
-    if (threadIdx.x == 0) sh.found = 0, sh.found_count = c.count, sh.found_mass = c.mass;
+    if (threadIdx.x == 0) sh.found = 0, sh.found_here = 0, sh.found_count = c.count, sh.found_mass = c.mass;
     __syncthreads();
     src.each([&](unsigned k, int index) {
       (void)index;
@@ -283,12 +285,12 @@ __device__ Cut cut_at(const Source& src, Cut above, unsigned count, double mass,
       bn += c.count - in, bm += c.mass - im;  // of what lies above this lane's bins
       // the first bin that reaches; where rounding leaves none, the lowest that holds any
       int at = -1, some = -1;
-      unsigned some_n = 0;
+      unsigned some_n = 0, some_here = 0;
       u64 some_m = 0;
 #pragma unroll
       for (int b = 0; b < 4; b++) {
         if (at >= 0) continue;
-        if (n[b] > 0) some = b, some_n = bn, some_m = bm;
+        if (n[b] > 0) some = b, some_n = bn, some_m = bm, some_here = n[b];
         if (n[b] > 0 && (kCount ? bn + n[b] >= count : (double)(bm + m[b]) >= mass)) at = b;
         bn += n[b], bm += m[b];
       }
@@ -298,10 +300,11 @@ __device__ Cut cut_at(const Source& src, Cut above, unsigned count, double mass,
         who = __builtin_amdgcn_ballot_w64(some >= 0);
         if (who) owner = 63 - __builtin_clzll(who);
       }
-      if (lane == owner) sh.found = 255 - 4 * lane - some, sh.found_count = some_n, sh.found_mass = some_m;
+      if (lane == owner)
+        sh.found = 255 - 4 * lane - some, sh.found_count = some_n, sh.found_mass = some_m, sh.found_here = some_here;
     }
     __syncthreads();
-    c.key |= sh.found << shift, c.count = sh.found_count, c.mass = sh.found_mass;
+    c.key |= sh.found << shift, c.count = sh.found_count, c.mass = sh.found_mass, c.here = sh.found_here;
     fixed |= 255u << shift;
     __syncthreads();
   }
@@ -330,7 +333,7 @@ struct Equal {
 template <class Source>
 __device__ int last_of(const Source& src, unsigned key, u64 n, CutLds& sh) {
   const Equal<Source> same = {src, key};
-  return (int)~cut_at<true>(same, {0, 0, 0}, (unsigned)min(n, (u64)0x7FFFFFFF), 0, 0, sh, [](unsigned) { return (u64)0; }).key;
+  return (int)~cut_at<true>(same, {0, 0, 0, 0}, (unsigned)min(n, (u64)0x7FFFFFFF), 0, 0, sh, [](unsigned) { return (u64)0; }).key;
 }
 
 // Cuts a source: `in_k` holds the elements among which top-k cuts, `in_p` those
@@ -346,7 +349,7 @@ __device__ Kept cut_both(const SourceK& in_k, Cut above_k, bool cut_k, unsigned 
   if (cut_k) {
     const Cut c = cut_at<true>(in_k, above_k, k, 0, kLowest, sh, mass_of);
     kept.key = whole_key<kBf16>(c.key);
-    ties = k - c.count;
+    ties = min(k - c.count, c.here);  // (fewer than k tokens above -inf: all of them)
     total = (double)(c.mass + ties * mass_of(kept.key));
   }
   if (cut_p) {
@@ -455,7 +458,7 @@ __device__ void whole_row(const SampleArgs& a, int64_t r, const Row<kBf16>& row,
     row.each([&](unsigned key, int) { total += Weights::units(wt.of(of_key(key))); });
     total = sum_block(total, sh.wave_sum);
   }
-  const Kept kept = cut_both<kBf16>(row, {0, 0, 0}, set.cut_k, (unsigned)set.k, row, {0, 0, 0}, set.cut_p, set.top_p,
+  const Kept kept = cut_both<kBf16>(row, {0, 0, 0, 0}, set.cut_k, (unsigned)set.k, row, {0, 0, 0, 0}, set.cut_p, set.top_p,
                                     (double)total, wt, set.min_w, sh);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int s = wave; s < row.segments(); s += blockDim.x / 64) {
@@ -743,7 +746,7 @@ __device__ Kept cut_list(const ListLds& list, int n, const Cuts& cuts, u64 mass_
     if (few) order = max(order, rank<false>(c, 0, mass, 0, reach, rk).order);
   }
   if (!few)
-    return cut_both<kBf16>(in_k, {0, cuts.above_k, mass_k}, cut_k, (unsigned)set.k, in_p, {0, 0, mass_p}, set.cut_p,
+    return cut_both<kBf16>(in_k, {0, cuts.above_k, mass_k, 0}, cut_k, (unsigned)set.k, in_p, {0, 0, mass_p, 0}, set.cut_p,
                            set.top_p, total, wt, set.min_w, sh);
   kept.key = (unsigned)(order >> 32), kept.last = (int)~(unsigned)order;
   return kept;

@@ -625,6 +625,29 @@ def test_sample_extreme_temperatures(temperature):
     draw_case(big, "f32", rng.random(5), temperature=1e37, top_p=0.9)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [600, 8000, 70000])
+def test_sample_top_k_past_the_finite_logits(vocab, dtype):
+    """More tokens asked for than have a finite logit, with top-p: its share is of the
+    tokens that there are.  Few and equal ones where the temperature is far below
+    the logits, then more than a list holds, equal and unequal."""
+    rng = np.random.default_rng(vocab)
+    u = [0.0, 0.3, 0.6, 0.9, 0.999, 1.0]
+    for n, p in ((2, 0.3), (3, 0.5), (40, 0.9)):
+        x = np.full((6, vocab), -np.inf)
+        for r in range(6):
+            x[r, rng.choice(vocab, n, replace=False)] = 10.0
+        for k in (n + 1, 50, vocab - 1):
+            draw_case(x, dtype, u, temperature=1e-6, top_k=k, top_p=p, what=f"{n} of {k}")
+    n = vocab * 5 // 8
+    for unequal in (0.0, 2.0 ** -12):
+        x = np.full((6, vocab), -np.inf)
+        for r in range(6):
+            x[r, rng.choice(vocab, n, replace=False)] = 1 + unequal * rng.integers(-8, 1, size=n)
+        for k in (n, n + 1, vocab * 3 // 4, vocab - 1):
+            draw_case(x, dtype, u, top_k=k, top_p=0.9, what=f"{n} of {k}")
+
+
 def test_sample_outputs_and_repeat():
     """Caller's outputs and workspace, and the same bits again."""
     rng = np.random.default_rng(8)
