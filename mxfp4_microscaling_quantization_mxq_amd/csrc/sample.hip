@@ -811,7 +811,9 @@ __global__ __launch_bounds__(kThreads, 4) void k_sample_row(SampleArgs a) {
     sum = sum_block(sum, sh.wave_sum);
     const Cuts cuts = find_cuts(packed_mass(bin[threadIdx.x]), packed_count(bin[threadIdx.x]), set, (double)sum, lds.bins.find);
     __syncthreads();  // (the list is written over it)
-    if (cuts.bin_k >= 0 || set.cut_p) {
+    // (rounded grids say nothing of where a cut lies, or that none does)
+    const bool coarse = !(fabsf(grid_top) < kGridMost);
+    if (coarse || cuts.bin_k >= 0 || set.cut_p) {
       // the candidates, and what lies above them
       u64 above_k = 0, above_p = 0;
 #pragma unroll
@@ -829,7 +831,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_sample_row(SampleArgs a) {
         }
       above_k = sum_block(above_k, sh.wave_sum);
       above_p = sum_block(above_p, sh.wave_sum);  // (and barriers)
-      if (lds_n > kList || !(fabsf(grid_top) < kGridMost)) {
+      if (coarse || lds_n > kList) {
         whole_row<kBf16>(a, r, row, set, of_key(top), mass, sh);
         return;
       }

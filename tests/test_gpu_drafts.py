@@ -648,6 +648,18 @@ def test_sample_top_k_past_the_finite_logits(vocab, dtype):
             draw_case(x, dtype, u, top_k=k, top_p=0.9, what=f"{n} of {k}")
 
 
+def test_sample_top_k_where_bins_are_coarse():
+    """A temperature below 2^-28 of neighbouring fp32 logits, whose bins of exponents
+    are hundreds apart: top-k cuts, with and without min-p."""
+    for vocab in (600, 5001, 8000, 20000):
+        x = np.full((6, vocab), 1.9999020099639893)
+        for r in range(6):
+            x[r, r * (vocab - 1) // 5] = 1.9999021291732788
+        u = [0.0, 0.3, 0.9, 0.99948, 0.9999, 1.0]
+        for s in (dict(top_k=2), dict(top_k=2, min_p=1e-9), dict(top_k=vocab - 1), dict(top_k=2, top_p=0.9999)):
+            draw_case(x, "f32", u, temperature=7.416363e-9, what=f"{vocab} {s}", **s)
+
+
 def test_sample_outputs_and_repeat():
     """Caller's outputs and workspace, and the same bits again."""
     rng = np.random.default_rng(8)
