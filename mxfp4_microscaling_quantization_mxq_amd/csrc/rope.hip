@@ -7,12 +7,12 @@
 // are quantized from the rotated values as they are (no rounding to 16 bits
 // between), values as they come.
 //
-// Roundings.  The angle is the exact product of the position and the fp32
-// frequency (two fp64 terms), reduced by pi / 2 in fp64, so far positions turn
-// as exactly as near ones; cos and sin are fp64, within 2^-50.  Keys are turned
-// in fp64 and rounded to odd in fp32, so the one rounding to a code that follows
-// is that of the fp64 value.  Queries, whose output is bf16, are turned in fp32
-// (three roundings of 2^-24).
+// Roundings.  The angle is the product of the position (all 64 bits) and the fp32
+// frequency in two fp64 terms, within 2^-66, reduced by pi / 2 in fp64, so far
+// positions turn as exactly as near ones; cos and sin are fp64, within 2^-50.
+// Keys are turned in fp64 and rounded to odd in fp32, so the one rounding to a
+// code that follows is that of the fp64 value.  Queries, whose output is bf16, are
+// turned in fp32 (three roundings of 2^-24).
 //
 // Memory bound: q, k and v are read once, q's bf16 and the codes written once
 // (64 query heads over 8, D = 128, bf16 in, MXFP8: 39 kB a token).  16384 such
@@ -35,11 +35,14 @@ struct RopeParams {
   unsigned tokens, heads_each;  // tokens of a block, and the heads it takes
 };
 
-// cos and sin of position * freq.  n is the nearest multiple of pi / 2 (two
-// fp64 terms, 107 bits), the rest is in [-pi / 4, pi / 4] up to a rounding of n,
-// where the Taylor polynomials end below 2^-55.  Angles of 2^40 and more give NaN.
-__device__ __forceinline__ double2 cos_sin(double position, double freq) {
-  const double hi = position * freq, lo = __builtin_fma(position, freq, -hi);
+// cos and sin of position * freq.  The position is p + rest (rest is 0 below 2^53).
+// n is the nearest multiple of pi / 2 (two fp64 terms, 107 bits), the angle less
+// that is in [-pi / 4, pi / 4] up to a rounding of n, where the Taylor polynomials
+// end below 2^-55.  Angles of 2^40 and more give NaN.
+__device__ __forceinline__ double2 cos_sin(int64_t position, double freq) {
+  const double high = (double)(int)(position >> 32) * 0x1p32, low = (double)(unsigned)position;
+  const double p = high + low, rest = low - (p - high);
+  const double hi = p * freq, lo = __builtin_fma(p, freq, -hi) + rest * freq;
   const double n = __builtin_rint(hi * 0x1.45f306dc9c883p-1);
   const double r = __builtin_fma(-n, 0x1.1a62633145c07p-54, __builtin_fma(-n, 0x1.921fb54442d18p+0, hi)) + lo;
   const double z = r * r;
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(RopeParams p) {
   for (unsigned i = threadIdx.x; i < here * n; i += kThreads) {
     const unsigned t = i / n, pair = i % n;
     const int64_t axis = a.axes ? min((int64_t)a.axes[pair], a.position_axes - 1) : 0;
-    table[i] = cos_sin((double)a.positions[axis * a.tokens + t0 + t], (double)a.freqs[pair]);
+    table[i] = cos_sin(a.positions[axis * a.tokens + t0 + t], (double)a.freqs[pair]);
   }
   __syncthreads();
 

@@ -126,6 +126,51 @@ def test_rope_far_and_negative_positions():
         rope_case(2, len(p), 2, 4, 64, 32, 16, "mxfp8", dtype, positions=p, freqs=f)
 
 
+def exact_turns(positions, freqs):
+    """(cos, sin) in extended precision of the angles as whole numbers of 2^-300, less
+    the nearest multiple of 2 pi."""
+    bits = 300
+
+    def arctan_of_inverse(n):
+        term, total, k = (1 << bits + 32) // n, 0, 0
+        while term:
+            total += (-1) ** k * (term // (2 * k + 1))
+            term, k = term // (n * n), k + 1
+        return total
+
+    turn = (32 * arctan_of_inverse(5) - 8 * arctan_of_inverse(239)) >> 32  # 2 pi = 8 (4 arctan 1/5 - arctan 1/239)
+    rest = np.zeros((len(positions), len(freqs)), dtype=np.longdouble)
+    for i, p in enumerate(positions):
+        for j, f in enumerate(freqs):
+            top, bottom = float(f).as_integer_ratio()
+            angle = (int(p) * top << bits) // bottom
+            left = angle - (2 * angle + turn) // (2 * turn) * turn
+            rest[i, j] = np.ldexp(np.longdouble(left >> (bits - 60)), -60)
+    return np.cos(rest), np.sin(rest)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_positions_past_53_bits(interleaved):
+    """Positions that fp64 does not hold, at frequencies that leave an angle: each turns by its own."""
+    rng = np.random.default_rng(5)
+    p = np.concatenate((2 ** 53 + np.array([-1, 1, 3]), -2 ** 53 - np.array([1, 3]), 2 ** 62 + 511 + 1024 * rng.integers(0, 1 << 40, 30),
+                        -2 ** 62 - 511 - 1024 * rng.integers(0, 1 << 40, 30), [2 ** 63 - 1, -2 ** 63, 2 ** 63 - 511])).astype(np.int64)
+    freqs = (np.float32(1.9999) * np.exp2(-24 - np.arange(32) / 8)).astype(np.float32)
+    cos, sin = exact_turns(p, freqs)
+    n, heads, d = len(p), 8, 64
+    x, x64 = stored(rng.laplace(size=(n, 3 * heads, d)), "f32")
+    q, k, v = dev(x).split(heads, 1)
+    cache = mxq.kv_cache(-(-n // 16), 16, heads, d)
+    out = mxq.rope_append(cache, q, k, v, dev(np.arange(n)), dev(p), dev(freqs), interleaved=interleaved)
+    y, span = dm.rotate(x64[:, :heads], cos, sin, interleaved)
+    got = oracle.to_f64(host(out))
+    assert ((got >= model.bf16_round(y - 2 * U * span)) & (got <= model.bf16_round(y + 2 * U * span))).all()
+    y, span = dm.rotate(x64[:, heads:2 * heads], cos, sin, interleaved)
+    at = np.arange(n)
+    kq, ks = (host(a) for a in cache[:2])
+    dm.check_codes(kq[at // 16, :, at % 16], ks[at // 16, :, at % 16], y, span * 2.0 ** -49, "mxfp8", "keys")
+
+
 def test_rope_angles_next_to_quarters():
     """Angles next to multiples of pi / 4, where the reduction changes over."""
     n = np.arange(1, 200)
