@@ -10,6 +10,8 @@ Tolerances, from the kernels' number formats (u = 2^-24 is the fp32 unit):
   u / 2) + 2^-50, held to 2 u (|a| + |b|), then one rounding to bf16, which is
   monotone.
 """
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -391,6 +393,20 @@ def test_tree_window_over_ranges(window, first):
     tree_case(window, [4000, 100, 1600], 6, 2, 4, 64, 16, "mxfp8", window=window, first=first)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("context,drafts,group,window,first", [
+    ([3000, 100, 1600], 24, 4, 1500, 40),         # 96 rows
+    ([3000, 100, 1600], 40, 5, 1100, 0),          # 200
+    ([2500, 0, 1900, 2100], 40, 16, 0, 0),        # several row groups
+    ([2500, 0, 1900, 2100], 40, 16, 1300, 1030),
+    ([2600] * 9, 33, 4, 1200, 3),                 # units that several ranges share, and ranges that share units
+])
+def test_tree_many_rows_over_ranges(context, drafts, group, window, first, d):
+    """More than 64 rows of a cache head, cut by ranges, with and without a window."""
+    tree_case(d, context, drafts, 2, group, d, 16, "mxfp4" if drafts == 33 else "mxfp8", window=window, first=first,
+              out=torch.bfloat16 if drafts == 24 else torch.float32, sinks=drafts == 40)
+
+
 @pytest.mark.parametrize("context,drafts,heads,group,d,window", [
     ([0, 1, 700], 9, 2, 8, 128, 0),          # shares of the short ones that are empty
     ([0, 1, 700], 5, 2, 8, 64, 0),
@@ -703,6 +719,27 @@ def test_sample_top_k_where_bins_are_coarse():
         u = [0.0, 0.3, 0.9, 0.99948, 0.9999, 1.0]
         for s in (dict(top_k=2), dict(top_k=2, min_p=1e-9), dict(top_k=vocab - 1), dict(top_k=2, top_p=0.9999)):
             draw_case(x, "f32", u, temperature=7.416363e-9, what=f"{vocab} {s}", **s)
+
+
+def test_sample_more_rows_than_a_pass_takes():
+    """Long rows whose workspace is reused by the rows after them: the same bits as each row alone."""
+    rng = np.random.default_rng(12)
+    rows, vocab = 1700, 9000
+    n = ctypes.c_int64()
+    assert mxq.capi().mxq_sample_workspace(rows, vocab, ctypes.byref(n)) == 0
+    one = ctypes.c_int64()
+    assert mxq.capi().mxq_sample_workspace(1, vocab, ctypes.byref(one)) == 0
+    turn = n.value // one.value
+    assert 1 < turn < rows  # rows of a pass
+    x = logits_like(rng, rows, vocab)
+    picks = [SETTINGS[int(i)] for i in rng.integers(0, len(SETTINGS), size=rows)]
+    mixed = {k: [s.get(k, v) for s in picks] for k, v in (("temperature", 1.0), ("top_k", 0), ("top_p", 1.0), ("min_p", 0.0))}
+    u = rng.random(rows).astype(np.float32)
+    tokens, shares = draw_case(x, "bf16", u, **mixed)
+    xd = dev(stored(x, "bf16")[0])
+    for r in [0, 1, turn - 2, turn - 1, turn, turn + 1, rows - 2, rows - 1]:
+        t, p = mxq.sample(xd[r:r + 1], dev(u[r:r + 1]), **{k: v[r] for k, v in mixed.items()})
+        assert int(t[0]) == tokens[r] and float(p[0]) == shares[r], r
 
 
 def test_sample_outputs_and_repeat():
