@@ -38,11 +38,11 @@ struct RopeParams {
 // cos and sin of position * freq.  The position is p + rest (rest is 0 below 2^53).
 // n is the nearest multiple of pi / 2 (two fp64 terms, 107 bits), the angle less
 // that is in [-pi / 4, pi / 4] up to a rounding of n, where the Taylor polynomials
-// end below 2^-55.  Angles of 2^40 and more give NaN.
+// end below 2^-54 (the sine's next term is r^17 / 17!).  Angles of 2^40 and more give NaN.
 __device__ __forceinline__ double2 cos_sin(int64_t position, double freq) {
   const double high = (double)(int)(position >> 32) * 0x1p32, low = (double)(unsigned)position;
   const double p = high + low, rest = low - (p - high);
-  const double hi = p * freq, lo = __builtin_fma(p, freq, -hi) + rest * freq;
+  const double hi = p * freq, lo = __builtin_fma(rest, freq, __builtin_fma(p, freq, -hi));
   const double n = __builtin_rint(hi * 0x1.45f306dc9c883p-1);
   const double r = __builtin_fma(-n, 0x1.1a62633145c07p-54, __builtin_fma(-n, 0x1.921fb54442d18p+0, hi)) + lo;
   const double z = r * r;
@@ -205,9 +205,10 @@ hipError_t launch_rope_append(const RopeArgs& a, const KvShape& c, bool bf16, bo
   const unsigned step = p.rows / p.tokens;
   const int64_t runs = (a.tokens + p.tokens - 1) / p.tokens, most = (heads + step - 1) / step;
   // Few runs: as many blocks as fill the chip, down to a head each (256 tokens of 64
-  // heads over 8: 8.7 us, with 256 blocks 9.5).  Many: 10 heads a block, enough to
-  // share the run's table and few enough that heads of a token are in flight
-  // together (16384 tokens: 144 us; all 80 heads 159, 40 157; 2048 tokens 22; 5 heads 30).
+  // heads over 8: 8.8 us, with 256 blocks 9.5, with 1024 8.0).  Many: 10 heads a block,
+  // enough to share the run's table and few enough that heads of a token are in flight
+  // together (16384 tokens: 144 us; all 80 heads 159, 40 157; 2048 tokens 22; 5 heads
+  // 29).  Not the best at each size: 4096 tokens take 40 us, with 20 heads 34.
   const int64_t splits = runs >= 128 ? (most + 9) / 10 : std::min(most, 2048 / runs);
   p.heads_each = (unsigned)((most + splits - 1) / splits * step);
   const dim3 grid((unsigned)(runs * ((heads + p.heads_each - 1) / p.heads_each))), block(kThreads);
