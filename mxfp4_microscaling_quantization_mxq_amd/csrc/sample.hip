@@ -30,7 +30,7 @@
 //   k_sample_draw: a row's list cut, and its token drawn.
 // (Joined by a ticket in k_sample_cut, whose last block of a row went on with it,
 // three launches were slower: each block's release to the other chiplets cost
-// more than a launch, 97 rows of 50001 103 us for 20 + 15.)
+// more than a launch.)
 // What a row gives depends on that row alone, not on the others of the call.
 #include <float.h>
 
@@ -56,8 +56,9 @@ constexpr float kBinsPer = 16;   // of the exponent
 constexpr int kList = 4096;
 constexpr int kRank = kThreads;  // tokens that are ranked, one a thread
 constexpr int kFew = 96;         // up to which they are ranked at once
-// Up to which a row's whole list is ranked by order and by index: 128 tokens take
-// 6 us, 192 about 13, 440 60, the other way through segments 15 for any number.
+// Up to which a row's whole list is ranked by order and by index.  k_sample_draw for
+// a row of 131072, and the other way through segments: 64 tokens 6.1 us and 8.5, 96
+// 8.2 and 8.6, 128 9.4 and 8.6, 192 17.3 and 9.3 (past 96 this way does not pay).
 constexpr int kFewListed = 192;
 // A histogram's entry: the number of tokens, and their weights in units of 2^-36
 // (cut off, so up to 2^20 of them are less than 2^-16 of the largest below).
@@ -182,8 +183,8 @@ struct Weights {
 // Bins of exponents: `grid` is a whole number that rises with x, and a bin is how
 // far it lies below that of the largest.  Below kGridMost these are exact, so bins
 // counted from a block's largest and from the row's differ by a constant.  (Rows
-// whose largest is 2^19 temperatures or more from 0 are past it and left to one
-// block.)
+// whose largest is 2^20 temperatures or more from 0 are past it and left to passes
+// over the row by one block.)
 constexpr float kGridMost = 0x1p24f;
 struct Bins {
   float per;
@@ -758,7 +759,8 @@ __device__ __forceinline__ void no_token(const SampleArgs& a, int64_t r) {
 }
 
 // Rows that one block holds.  The histogram's LDS becomes the list's, so that two
-// blocks fit a CU (1024 rows of 8000, top-k and top-p: 70 us with one, 46 with two).
+// blocks fit a CU (1024 rows of 8000, top-k and top-p: 44 us; 70 with one block a CU,
+// where two took 46).
 struct BinLds {
   FindLds find;
   u64 bin[kBins];

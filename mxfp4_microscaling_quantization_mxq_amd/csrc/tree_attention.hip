@@ -26,8 +26,10 @@
 // query heads over each of 8 cache heads, D = 128, E4M3: 178 us, 6.2 TB/s).  64
 // rows: decoding, once for each 32 (64 sequences of 4600 tokens with 8 drafted
 // ones 212 us, 2.9 TB/s).  Many rows: products, with P in two bf16 terms or three,
-// and beside them the exponentials and the decoding (64 drafted tokens over 4 x
-// 20500: 322 us, 536 TFLOP/s counted once, 800 as issued).
+// and the exponentials and the decoding, which a wave does one after another (64
+// drafted tokens over 4 x 20500: 322 us, 536 TFLOP/s counted once, 800 as issued; over
+// 4 x 9000 to 32000 the matrix cores are busy for 39 % of the time, the vector units
+// for 40 %, LDS for 29 %, with two waves a SIMD).
 #include "mxq_attend.h"
 
 namespace mxq {
@@ -563,12 +565,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_tree_attend(TreeParams p) {
 // V^T P^T for V's tokens in the order 0-3, 8-11, 4-7, 12-15 of each 16.
 //
 // A turn decodes the next tile, whose loads were issued a turn before, and then
-// multiplies (322 us for the size above; after the products 341; by half of the waves
-// before and half after 355; two tiles ahead no better).  A wave's products wait for its
-// exponentials; forming one set's while the next one's products run needs more
-// registers than there are and spills (340 to 370).  Scalars that stay in scalar
-// registers matter most: page addresses in vector registers made a loop of each
-// load (376).
+// multiplies (322 us for the size above; after the products 341, loaded two tiles
+// ahead 345; by half of the waves before and half after no better).  A wave's
+// products wait for its exponentials; forming one set's while the next one's
+// products run needs more registers than there are and spills (340 to 370).
+// Scalars that stay in scalar registers matter most: page addresses in vector
+// registers made a loop of each load (376).
 //
 // A row's reference moves only where its maximum has risen by more than 2^8 above
 // it: the old terms are seldom scaled, and probabilities of up to 2^8 lose nothing.
@@ -1032,7 +1034,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeParams p, unsigned unit_r
 // Shape of a call's units.  Up to 64 rows of a cache head, k_tree_attend: N sets
 // of 16 rows a wave, of one or two row waves.  More, k_tree_wide, whose blocks
 // decode for 128 or 256 rows.  Measured, D = 128 E4M3, 8 cache heads: 64 rows (64
-// sequences of 4600 tokens) 215 us and 328 us by k_tree_wide; 128 rows (32 of
+// sequences of 4600 tokens) 212 us and 328 us by k_tree_wide; 128 rows (32 of
 // 4600) 215 us by k_tree_attend and 182; 512 rows (4 of 20500) 512 and 322.
 struct TreeUnits {
   bool wide;
