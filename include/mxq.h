@@ -505,8 +505,10 @@ MXQ_API mxq_status mxq_tree_attention(const void *q, int64_t q_stride, const uin
  * that may be drawn is taken.  A row that holds a NaN or +inf, or nothing but
  * -inf, gives token -1 and a share of NaN.
  * Weights are fp64 and are summed as whole multiples of 2^-43 of the largest (a
- * row of more than 8192, in parts, of each part's largest), and what a row gives
- * depends on that row alone; weights below 2^-44 of the largest may count as 0.
+ * row of more than 8185, in parts of 8192 that begin at a multiple of 8 elements in
+ * memory, of each part's largest); what a row gives depends on that row alone (and,
+ * in the last bits of a long row's sums, on its alignment).  Weights below 2^-44
+ * of the largest may count as 0.
  * logits of type dt, row r at logits + r * stride elements (stride >= vocab, any
  * alignment of its type); u fp32 [rows].  Each setting is an array [rows], or one
  * value for all rows where its array is NULL (top_k int32, the others fp32; the

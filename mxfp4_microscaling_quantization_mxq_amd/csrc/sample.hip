@@ -31,7 +31,8 @@
 // (Joined by a ticket in k_sample_cut, whose last block of a row went on with it,
 // three launches were slower: each block's release to the other chiplets cost
 // more than a launch.)
-// What a row gives depends on that row alone, not on the others of the call.
+// What a row gives depends on that row alone, not on the others of the call (where
+// its blocks begin, on its alignment: that moves the last bits of their sums).
 #include <float.h>
 
 #include "mxq_device.h"
